@@ -2,13 +2,17 @@
  * dspark.h -- C ABI of the DSpark draft / schedule / verify / accept-rate path
  * for one NVIDIA GB300 GPU (sm_103a).
  *
- * Six operations, each a hand-written CUDA kernel sequence:
+ * Ten operations, each a hand-written CUDA kernel sequence:
  *   dspark_draft_block      semi-autoregressive draft block, confidence, survival
  *   dspark_schedule_prefix  hardware-aware prefix scheduler (Algorithm 1)
  *   dspark_verify           rejection-sampling verification + residual/bonus token
  *   dspark_accept_rate_tv   c* = 1 - 1/2 ||softmax(d) - softmax(t)||_1 per row
  *   dspark_training_loss    joint CE + L1 + BCE loss per row, and its gradient
  *   dspark_decode_rounds    draft -> schedule -> verify rounds, anchor carried
+ *   dspark_plan_rows        pages, positions and cache slots of the rows a step adds
+ *   dspark_write_kv         the rows' keys and values into the paged cache
+ *   dspark_paged_attention  the rows' attention over the paged cache
+ *   dspark_adjust_logits    penalties, biases and grammar masks on the target rows
  * (and _ex variants of the draft and verify calls for the gated / RNN heads)
  *
  * Sources (cited per call): the DeepSpec / DSpark walkthrough at
@@ -69,7 +73,9 @@ typedef enum {
     DSPARK_ERR_DEVICE_CHECK = 6        /* device status only: a device-side input check failed */
 } dspark_status_t;
 
-typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype_t;
+/* DSPARK_E4M3 (8 bits: sign, 4 exponent, 3 mantissa bits, largest 448) is a type of
+ * caches only. */
+typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_E4M3 = 2 } dspark_dtype_t;
 
 typedef struct CUstream_st* dspark_stream_t;   /* same type as cudaStream_t */
 
@@ -397,6 +403,137 @@ dspark_status_t dspark_training_loss(int64_t rows, int V, dspark_dtype_t dt,
                                      float* row_out, float* loss, void* grad_d, float* grad_conf,
                                      void* workspace, size_t workspace_bytes,
                                      dspark_stream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * The target model's side of a round.  Between the schedule and the verification
+ * the target model runs over the rows of each request (the anchor and the scheduled
+ * draft tokens, ell[b] + 1 of them, or a piece of a prompt); the four calls below
+ * are the parts of that step that the cache and the tokens decide.  The pages leave
+ * the target model to the serving engine (DeepSpec walkthrough sections 8.1 - 8.3:
+ * target forward, then accept, then the cache cut back to what was accepted).
+ *
+ * Paged cache: k_cache, v_cache [num_blocks][Hkv][page][D], a page's rows of one
+ * head adjacent.  Slot s is row s % page of page s / page.  block_table [B][ld]
+ * int32: entry j of request b names the page of its positions j page .. j page +
+ * page - 1.  Any page size of at least 1 is taken.
+ *
+ * Row planning.  Request b has len[b] rows in the cache before the last step's rows;
+ * advance[b] of those stay (the accepted ones and the anchor: n_accept[b] + 1), and
+ * the step adds rows[b] more.  With base = len + advance and need = ceil((base +
+ * rows) / page), a request that holds fewer pages takes need - held from the head of
+ * the ring of free pages, and one that holds more (its last rows were rejected, or it
+ * is finished: len = advance = rows = 0) gives the pages past need back to the ring's
+ * tail; requests in ascending order, pages in ascending order within one.  Pages given
+ * back in a call are not taken in the same call.
+ *
+ *   len, rows, held [B] int32; advance [B] int32, or NULL for zeros; free_state [2]
+ *   int32: the ring's head and the number of free pages; free_ring [num_blocks] int32.
+ *   Outputs: len_out [B] = base, held_out [B] = need, free_state_out [2] (each may be
+ *   the input itself); block_table and free_ring are updated in place (entries of a
+ *   table past held_out keep their old values); row_offset [B+1] int32, the requests'
+ *   first rows; and for row i: row_request[i], position[i] (base + its place in the
+ *   request) int32 and slot[i] int64, i < max_rows, with -1 in the rows past the
+ *   last.
+ * All or nothing: where a request's numbers are not consistent (detail 1: negative,
+ * more rows than its pages hold, or a ring that cannot hold what is given back), a
+ * table is full (2), the free pages do not suffice (3) or there are more than max_rows
+ * rows (4), the status is DSPARK_ERR_DEVICE_CHECK, the state outputs repeat the inputs,
+ * row_offset is all zero, the rows are all -1 and no page moves.  A page id outside
+ * [0, num_blocks) (5) gives that row slot -1.
+ * Requires 1 <= B <= 65535; max_blocks page and max_blocks B below 2^31.
+ * ------------------------------------------------------------------------ */
+size_t dspark_plan_rows_workspace_size(int B, int64_t max_rows);
+
+dspark_status_t dspark_plan_rows(int B, int page, int max_blocks, int num_blocks, int64_t max_rows,
+                                 const int32_t* len, const int32_t* advance, const int32_t* rows,
+                                 const int32_t* held, const int32_t* free_state, int32_t* free_ring,
+                                 int32_t* block_table, int64_t ld_table, int32_t* len_out, int32_t* held_out,
+                                 int32_t* free_state_out, int32_t* row_offset, int32_t* row_request,
+                                 int32_t* position, int64_t* slot, void* workspace, size_t workspace_bytes,
+                                 dspark_stream_t stream);
+
+/* Stores keys and values of a step's rows: k_cache[slot[i]] = k[i], v likewise.
+ *   k, v: row i at i * k_stride (v_stride) elements, Hkv heads of D adjacent elements
+ *   in `dt` (a slice of a fused projection needs no copy); strides in elements, rows
+ *   16-byte aligned.  slot [rows] int64; a negative one skips the row.
+ *   cache_dt: `dt`, or DSPARK_E4M3 with k_scale, v_scale [Hkv] float32 > 0: then
+ *   e4m3(x / scale[head]), nearest even, beyond +-448 the largest value, NaN kept.
+ *   Two rows must not have one slot.
+ * A slot past the last page sets DSPARK_ERR_DEVICE_CHECK and its row is skipped.
+ * D % 8 == 0 (16 for DSPARK_E4M3), D <= 256, Hkv <= 1024.  rows == 0 launches nothing. */
+size_t dspark_write_kv_workspace_size(void);
+
+dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int page, int num_blocks, dspark_dtype_t dt,
+                                dspark_dtype_t cache_dt, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, const int64_t* slot, const float* k_scale,
+                                const float* v_scale, void* k_cache, void* v_cache, void* workspace,
+                                size_t workspace_bytes, dspark_stream_t stream);
+
+/* Attention of a step's rows over the cache (their own keys and values stored).  Row i
+ * of request b (rows row_offset[b] .. row_offset[b+1] - 1 of q) stands at position
+ * len[b] + i (len: dspark_plan_rows' len_out) and sees the keys at positions up to its
+ * own, with window > 0 only the last `window` of them.  Query head hq reads key head
+ * hq / (Hq / Hkv):
+ *   s_j = scale q . k_j,  lse = ln sum_j exp(s_j),  out = sum_j exp(s_j - lse) v_j
+ * in float32, out rounded once to `dt`.  Keys and values a row does not see have no
+ * part in it, whatever they hold; pages past the last position are not read.
+ *   q: row i at i * q_stride elements, Hq heads of D adjacent elements in `dt`, 16-byte
+ *   aligned rows; out [rows][Hq][D] in `dt`; lse [rows][Hq] float32 or NULL.
+ *   rows: what q and out have room for (row_offset[B] or more; the rest is not
+ *   touched); max_rows: the most rows of one request.
+ *   cache_dt, k_scale, v_scale as for dspark_write_kv: a stored value stands for
+ *   itself times scale[head].
+ * The work is divided evenly over the GPU by the lengths on the device, so a call can be
+ * captured in a graph and replayed with other lengths.  The same inputs give the same
+ * bits.
+ * DSPARK_ERR_DEVICE_CHECK: a request whose rows or length are negative, above max_rows,
+ * above what q or its table have room for (detail 1; its rows are not written), or a
+ * page id outside [0, num_blocks) (2; page 0 is read instead).
+ * Hq % Hkv == 0, Hq <= 1024; D % 8 == 0 (16 for DSPARK_E4M3), D <= 256;
+ * max_blocks page and max_rows Hq / Hkv below 2^31 - 1024. */
+size_t dspark_paged_attention_workspace_size(int D);
+
+dspark_status_t dspark_paged_attention(int B, int64_t rows, int max_rows, int Hq, int Hkv, int D, int page,
+                                       int max_blocks, int num_blocks, dspark_dtype_t dt, dspark_dtype_t cache_dt,
+                                       const void* q, int64_t q_stride, const int32_t* row_offset,
+                                       const int32_t* len, const int32_t* block_table, int64_t ld_table,
+                                       const void* k_cache, const void* v_cache, const float* k_scale,
+                                       const float* v_scale, float scale, int window, void* out, float* lse,
+                                       void* workspace, size_t workspace_bytes, dspark_stream_t stream);
+
+/* Penalties, biases and grammar masks on the target rows, before dspark_verify (its
+ * t_logits layout: logits, out [B][R][V] in `dt`, R = gamma + 1).  For token v of row k
+ * (0-based) of request b, n(v) = how often v stands in the request's output: tokens
+ * prompt_len[b] .. history_len[b] - 1 of history[b] and the draft's first k tokens; s(v):
+ * whether it stands in the prompt (the first prompt_len[b] tokens) or in that output:
+ *   y = x;  if s(v): y = y > 0 ? y / repetition[b] : y * repetition[b];
+ *   y -= frequency[b] n(v);  if n(v) > 0: y -= presence[b];  y += bias(v);
+ *   masked: y = -inf
+ * in float32, rounded once.  Untouched tokens keep their bits.
+ *   ell [B] int32 in 0..R-1: only rows 0..ell[b] are read and written (those that
+ *   dspark_verify reads); NULL: all.  history [B][ld_history] int32 with history_len;
+ *   prompt_len NULL: no prompt.  draft [B][R-1] int32 or NULL.  repetition (> 0),
+ *   frequency, presence [B] float32, each may be NULL (1, 0, 0).
+ *   bias_token [B][n_bias] int32 (-1: unused), bias_value [B][n_bias] float32; entries of
+ *   one token add up in their order.
+ *   mask_row [B][R] int32: the row of mask that holds for this row, -1 for none; mask
+ *   [n_mask][ld_mask] uint32: bit v % 32 of word v / 32 set: v is allowed.  A row whose
+ *   mask allows nothing becomes -inf throughout (dspark_verify then has nothing to draw).
+ *   out may be logits itself; any other overlap is refused.
+ * DSPARK_ERR_DEVICE_CHECK: ell outside 0..R-1 (detail 1; the request is not written),
+ * lengths outside 0 <= prompt_len <= history_len <= ld_history (2; read as no history),
+ * a token outside [0, V) (3 history or draft, 4 bias; ignored), mask_row outside
+ * -1..n_mask-1 (5; read as -1).
+ * R <= DSPARK_MAX_GAMMA + 1, n_bias <= 2047, ld_history up to 1,048,543. */
+size_t dspark_adjust_logits_workspace_size(void);
+
+dspark_status_t dspark_adjust_logits(int B, int R, int V, dspark_dtype_t dt, const void* logits,
+                                     const int32_t* ell, const int32_t* history, int64_t ld_history,
+                                     const int32_t* prompt_len, const int32_t* history_len, const int32_t* draft,
+                                     const float* repetition, const float* frequency, const float* presence,
+                                     const int32_t* bias_token, const float* bias_value, int n_bias,
+                                     const int32_t* mask_row, const uint32_t* mask, int n_mask, int64_t ld_mask,
+                                     void* out, void* workspace, size_t workspace_bytes, dspark_stream_t stream);
 
 #ifdef __cplusplus
 }

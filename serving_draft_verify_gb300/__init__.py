@@ -9,6 +9,10 @@ from ._binding import (  # noqa: F401
     LIB_PATH,
     MAX_GAMMA,
     dspark_accept_rate_tv,
+    dspark_adjust_logits,
+    dspark_paged_attention,
+    dspark_plan_rows,
+    dspark_write_kv,
     dspark_training_loss,
     dspark_decode_rounds,
     dspark_draft_block_ex,

@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(_HERE, "_build", "libdspark.so")
 DSPARK_OK = 0
 DSPARK_F32 = 0
 DSPARK_BF16 = 1
+DSPARK_E4M3 = 2
 MAX_GAMMA = 32
 
 _c_int, _c_i64, _c_u64, _c_size, _c_float = (ctypes.c_int, ctypes.c_int64, ctypes.c_uint64,
@@ -51,6 +52,18 @@ _SIGNATURES = {
                                        _c_float, _p, _c_float, _c_u64, _p, _p, _p, _p, _p, _p, _p, _c_size, _p]),
     "dspark_verify_ex": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _p, _p, _p, _p, _p, _p, _p, _p, _p,
                                   _c_float, _c_u64, _p, _p, _p, _p, _c_size, _p]),
+    "dspark_plan_rows_workspace_size": (_c_size, [_c_int, _c_i64]),
+    "dspark_plan_rows": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_i64, _p, _p, _p, _p, _p, _p, _p, _c_i64, _p, _p,
+                                  _p, _p, _p, _p, _p, _p, _c_size, _p]),
+    "dspark_write_kv_workspace_size": (_c_size, []),
+    "dspark_write_kv": (_c_int, [_c_i64, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _p, _c_i64, _p, _c_i64, _p,
+                                 _p, _p, _p, _p, _p, _c_size, _p]),
+    "dspark_paged_attention_workspace_size": (_c_size, [_c_int]),
+    "dspark_paged_attention": (_c_int, [_c_int, _c_i64] + [_c_int] * 9 + [_p, _c_i64, _p, _p, _p, _c_i64, _p, _p, _p,
+                                        _p, _c_float, _c_int, _p, _p, _p, _c_size, _p]),
+    "dspark_adjust_logits_workspace_size": (_c_size, []),
+    "dspark_adjust_logits": (_c_int, [_c_int, _c_int, _c_int, _c_int, _p, _p, _p, _c_i64, _p, _p, _p, _p, _p, _p, _p,
+                                      _p, _c_int, _p, _p, _c_int, _c_i64, _p, _p, _c_size, _p]),
     "dspark_debug_draft_logits": (_c_int, [_c_int, _c_int, _c_int, _p, _p, _p, _p, _p, _p, _c_size, _p]),
     "dspark_debug_enable_phase_timing": (_c_int, [_c_int]),
     "dspark_debug_phase_times": (_c_int, [_p, _c_int]),
@@ -534,4 +547,204 @@ def dspark_verify_ex(t_logits, U, W1, W2, x0, x, lse_d, logp_d, ell, temperature
                                 _ptr(x), _ptr(lse_d), _ptr(logp_d), _ptr(ell), float(temperature),
                                 int(seed) & (2**64 - 1), ctypes.addressof(hs), _ptr(out["n_accept"]),
                                 _ptr(out["next_token"]), _ptr(ws), _nbytes(ws), _stream(stream)))
+    return out
+
+
+# --------------------------------------------- the target model's side of a round ---
+def _device_of(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _on(t, dev, shape, dtype, name):
+    """A contiguous tensor of this shape and type on device index `dev`."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _need(t, shape, dtype, name)
+        raise ValueError(f"{name} is on another device")
+
+
+def _opt(t, dev, shape, dtype, name):
+    """As _on, for a tensor that may be absent; returns its address."""
+    if t is None:
+        return None
+    _on(t, dev, shape, dtype, name)
+    return t.data_ptr()
+
+
+def _heads(t, dev, dtype, name):
+    """Rows of heads [n, heads, D]: the heads adjacent, the rows at any stride; returns that
+    stride in elements."""
+    if t.get_device() != dev or t.dtype is not dtype or t.dim() != 3:
+        raise ValueError(f"{name} must be a 3-dimensional CUDA tensor of {dtype} on the call's device")
+    n, heads, D = t.shape
+    s = t.stride()
+    if (D > 1 and s[2] != 1) or (heads > 1 and s[1] != D):
+        raise ValueError(f"{name}: the heads of a row must be adjacent")
+    return s[0] if n > 1 else heads * D
+
+
+def _scratch(nbytes, like, workspace, stream, *made):
+    """The workspace (allocated here if None).  Memory that this call allocated and that work on
+    another stream than the current one uses is tied to that stream."""
+    if workspace is None:
+        workspace = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=like.device)
+        made = (*made, workspace)
+    elif workspace.get_device() != like.get_device():
+        raise ValueError("workspace is on another device")
+    if stream is not None:
+        for t in made:
+            t.record_stream(stream)
+    return workspace
+
+
+_PLAN_OUT = ("length", "held", "free_state", "row_offset", "row_request", "position", "slot")
+
+
+def dspark_plan_rows(length, rows, held, free_state, free_ring, block_table, page, max_rows, advance=None, out=None,
+                     workspace=None, stream=None):
+    """Pages, positions and cache slots of the rows a step adds.  length, rows, held, advance
+    [B], free_state [2] (head, free pages), free_ring [num_blocks], block_table [B, max_blocks],
+    all int32; block_table and free_ring are updated in place.  Returns dict length, held [B],
+    free_state [2], row_offset [B + 1], row_request, position [max_rows] (int32) and slot
+    [max_rows] (int64); `out` may hold length, held and free_state themselves."""
+    lib = load()
+    dev = _device_of(length, "length")
+    B, = length.shape
+    nb, = free_ring.shape
+    width = block_table.shape[1]
+    i32 = torch.int32
+    _on(length, dev, (B,), i32, "length")
+    _on(rows, dev, (B,), i32, "rows")
+    _on(held, dev, (B,), i32, "held")
+    _on(free_state, dev, (2,), i32, "free_state")
+    _on(free_ring, dev, (nb,), i32, "free_ring")
+    _on(block_table, dev, (B, width), i32, "block_table")
+    adv = _opt(advance, dev, (B,), i32, "advance")
+    made = ()
+    if out is None:
+        new = lambda n, t=i32: torch.empty(n, dtype=t, device=length.device)  # noqa: E731
+        out = dict(length=new(B), held=new(B), free_state=new(2), row_offset=new(B + 1), row_request=new(max_rows),
+                   position=new(max_rows), slot=new(max_rows, torch.int64))
+        made = tuple(out.values())
+    for k, n in zip(_PLAN_OUT, (B, B, 2, B + 1, max_rows, max_rows, max_rows)):
+        _on(out[k], dev, (n,), torch.int64 if k == "slot" else i32, k)
+    ws = _scratch(lib.dspark_plan_rows_workspace_size(B, max_rows), length, workspace, stream, *made)
+    _check("dspark_plan_rows",
+           lib.dspark_plan_rows(B, page, width, nb, max_rows, length.data_ptr(), adv, rows.data_ptr(), held.data_ptr(),
+                                free_state.data_ptr(), free_ring.data_ptr(), block_table.data_ptr(), width,
+                                *[out[k].data_ptr() for k in _PLAN_OUT], ws.data_ptr(), _nbytes(ws), _stream(stream)))
+    return out
+
+
+def _cache_code(k_cache, v_cache, k_scale, v_scale, dev, dtype):
+    """Type code of the caches and the addresses of their scales."""
+    shape = k_cache.shape
+    if len(shape) != 4:
+        raise ValueError("caches have the shape [num_blocks, Hkv, page, D]")
+    t = k_cache.dtype
+    _on(k_cache, dev, shape, t, "k_cache")
+    _on(v_cache, dev, shape, t, "v_cache")
+    if t is torch.float8_e4m3fn:
+        if k_scale is None or v_scale is None:
+            raise ValueError("8-bit caches need k_scale and v_scale")
+        return DSPARK_E4M3, _opt(k_scale, dev, (shape[1],), torch.float32, "k_scale"), \
+            _opt(v_scale, dev, (shape[1],), torch.float32, "v_scale")
+    if t is not dtype:
+        raise TypeError(f"caches of {t} for rows of {dtype}")
+    if k_scale is not None or v_scale is not None:
+        raise ValueError("only 8-bit caches have scales")
+    return (DSPARK_BF16 if t is torch.bfloat16 else DSPARK_F32), None, None
+
+
+def dspark_write_kv(k, v, slot, k_cache, v_cache, k_scale=None, v_scale=None, workspace=None, stream=None):
+    """Stores the rows' keys and values: k, v [n, Hkv, D] (rows at any stride: slices of a fused
+    projection) at slot [n] int64 (negative: none) of the caches [num_blocks, Hkv, page, D], of
+    the rows' type or float8_e4m3fn with k_scale, v_scale [Hkv] float32."""
+    lib = load()
+    dev = _device_of(k_cache, "k_cache")
+    nb, Hkv, page, D = k_cache.shape
+    dt = _dtype_code(k, v)
+    ks, vs = _heads(k, dev, k.dtype, "k"), _heads(v, dev, k.dtype, "v")
+    n = k.shape[0]
+    if k.shape != (n, Hkv, D) or v.shape != (n, Hkv, D):
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} for caches of {Hkv} heads of {D}")
+    _on(slot, dev, (n,), torch.int64, "slot")
+    code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, k.dtype)
+    ws = _scratch(lib.dspark_write_kv_workspace_size(), k_cache, workspace, stream)
+    _check("dspark_write_kv",
+           lib.dspark_write_kv(n, Hkv, D, page, nb, dt, code, k.data_ptr(), ks, v.data_ptr(), vs, slot.data_ptr(), ksc,
+                               vsc, k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(), _nbytes(ws),
+                               _stream(stream)))
+
+
+def dspark_paged_attention(q, row_offset, length, block_table, k_cache, v_cache, max_rows, scale=None, window=0,
+                           k_scale=None, v_scale=None, out=None, workspace=None, stream=None):
+    """Attention of a step's rows over the paged cache.  q [n, Hq, D] (rows at any stride);
+    row_offset [B + 1], length [B] (rows in the cache before the step), block_table [B,
+    max_blocks] int32; max_rows: the most rows of one request; scale: 1 / sqrt(D) by default.
+    Returns dict out [n, Hq, D] and lse [n, Hq] float32 (an `out` without lse skips it)."""
+    lib = load()
+    dev = _device_of(k_cache, "k_cache")
+    nb, Hkv, page, D = k_cache.shape
+    B, = length.shape
+    qs = _heads(q, dev, q.dtype, "q")
+    n, Hq, qd = q.shape
+    if qd != D:
+        raise ValueError(f"q has heads of {qd}, the caches of {D}")
+    width = block_table.shape[1]
+    _on(row_offset, dev, (B + 1,), torch.int32, "row_offset")
+    _on(length, dev, (B,), torch.int32, "length")
+    _on(block_table, dev, (B, width), torch.int32, "block_table")
+    code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, q.dtype)
+    made = ()
+    if out is None:
+        out = dict(out=torch.empty((n, Hq, D), dtype=q.dtype, device=q.device),
+                   lse=torch.empty((n, Hq), dtype=torch.float32, device=q.device))
+        made = tuple(out.values())
+    _on(out["out"], dev, (n, Hq, D), q.dtype, "out")
+    lse = _opt(out.get("lse"), dev, (n, Hq), torch.float32, "lse")
+    ws = _scratch(lib.dspark_paged_attention_workspace_size(D), q, workspace, stream, *made)
+    _check("dspark_paged_attention",
+           lib.dspark_paged_attention(B, n, max_rows, Hq, Hkv, D, page, width, nb, _dtype_code(q), code, q.data_ptr(),
+                                      qs, row_offset.data_ptr(), length.data_ptr(), block_table.data_ptr(), width,
+                                      k_cache.data_ptr(), v_cache.data_ptr(), ksc, vsc,
+                                      D ** -0.5 if scale is None else float(scale), int(window),
+                                      out["out"].data_ptr(), lse, ws.data_ptr(), _nbytes(ws), _stream(stream)))
+    return out
+
+
+def dspark_adjust_logits(logits, history=None, prompt_len=None, history_len=None, draft=None, ell=None,
+                         repetition=None, frequency=None, presence=None, bias_token=None, bias_value=None,
+                         mask_row=None, mask=None, out=None, workspace=None, stream=None):
+    """Penalties, biases and grammar masks on the target rows [B, R, V] (R = gamma + 1), in place
+    with out=logits.  history [B, L] with prompt_len, history_len [B]; draft [B, R - 1]; ell [B]
+    (rows 0..ell[b] are done); repetition, frequency, presence [B] float32; bias_token,
+    bias_value [B, n]; mask_row [B, R] (-1: none) into mask [n_mask, ceil(V / 32)] (int32 words,
+    bit v % 32 of word v // 32: allowed).  Each group may be absent."""
+    lib = load()
+    dev = _device_of(logits, "logits")
+    B, R, V = logits.shape
+    i32, f32 = torch.int32, torch.float32
+    _on(logits, dev, (B, R, V), logits.dtype, "logits")
+    width = history.shape[1] if history is not None else 0
+    n_bias = bias_token.shape[1] if bias_token is not None else 0
+    n_mask, words = mask.shape if mask is not None else (0, (V + 31) // 32)
+    made = ()
+    if out is None:
+        out = torch.empty_like(logits)
+        made = (out,)
+    _on(out, dev, (B, R, V), logits.dtype, "out")
+    ws = _scratch(lib.dspark_adjust_logits_workspace_size(), logits, workspace, stream, *made)
+    _check("dspark_adjust_logits",
+           lib.dspark_adjust_logits(
+               B, R, V, _dtype_code(logits), logits.data_ptr(), _opt(ell, dev, (B,), i32, "ell"),
+               _opt(history, dev, (B, width), i32, "history"), width, _opt(prompt_len, dev, (B,), i32, "prompt_len"),
+               _opt(history_len, dev, (B,), i32, "history_len"), _opt(draft, dev, (B, R - 1), i32, "draft"),
+               _opt(repetition, dev, (B,), f32, "repetition"), _opt(frequency, dev, (B,), f32, "frequency"),
+               _opt(presence, dev, (B,), f32, "presence"), _opt(bias_token, dev, (B, n_bias), i32, "bias_token"),
+               _opt(bias_value, dev, (B, n_bias), f32, "bias_value"), n_bias,
+               _opt(mask_row, dev, (B, R), i32, "mask_row"), _opt(mask, dev, (n_mask, words), i32, "mask"), n_mask,
+               words, out.data_ptr(), ws.data_ptr(), _nbytes(ws), _stream(stream)))
     return out

@@ -1,0 +1,276 @@
+// Shared parts of dspark_paged_attention's kernels: the work list and how it is
+// divided over the GPU, and the joining of parts.
+//
+// Mathematics.  For query row i (0-based) of request b, at position len_b + i, and
+// query head hq of key head h, with scores s_j = scale q . k_j over the visible keys
+// j <= len_b + i (j > len_b + i - window with a window):
+//   lse = ln sum_j exp(s_j),  out = sum_j exp(s_j - lse) v_j.
+// A part of the keys gives m = max s_j, l = sum exp(s_j - m), o = sum exp(s_j - m)
+// v_j; two parts join as m = max(m1, m2), l = sum_i l_i exp(m_i - m), likewise o.
+// Scores are kept in units of log 2, so that exp is ex2.
+//
+// Work list.  The query rows of one key head (row i, head g of its group; index
+// i G + g) are cut into tiles of M, and the keys a tile can see into units of KT.
+// All units of all (request, key head, tile) segments stand in one line, and block c
+// of n (n no more than W) takes units [c W / n, (c + 1) W / n): an even division whatever the lengths
+// are, found by every block from the lengths on the device.  A segment that no
+// block holds whole is joined by the last of its blocks to finish (a counter, nobody
+// waits), its parts always in the order of the keys, so results do not depend on
+// who came last.
+#pragma once
+
+#include "common.cuh"
+#include "host_common.h"
+
+namespace dspark {
+namespace attn {
+
+struct Args {
+    int B, Hq, Hkv, G, D, page, max_blocks, num_blocks, max_rows, window;
+    int64_t rows, ld_table, q_stride;
+    const void* q;
+    const int32_t *row_offset, *length, *table;
+    const void *kc, *vc;
+    const float *k_scale, *v_scale;
+    float scale_log2;                 // scale * log2(e)
+    void* out;
+    float* lse;
+    StatusBlock* status;
+    uint32_t* counters;               // [grid] parts that are done of the segment that starts in a block's range
+    float* part_ml;                   // [2 grid][M][2]
+    float* part_o;                    // [2 grid][M][D]
+};
+
+constexpr size_t kCounterBytes = 4096;      // up to 1024 blocks
+constexpr int kMaxGrid = 1024;
+
+struct Request {
+    int row0, n, len;                 // first row, rows, keys before the step
+};
+// What the lengths say about request b; an inconsistent one has no rows.
+__device__ __forceinline__ Request request_of(const Args& p, int b, bool tell) {
+    Request r;
+    r.row0 = p.row_offset[b];
+    const int64_t n = static_cast<int64_t>(p.row_offset[b + 1]) - r.row0;
+    r.len = p.length[b];
+    const int64_t cap = static_cast<int64_t>(p.max_blocks) * p.page;
+    const bool ok = n >= 0 && n <= p.max_rows && r.row0 >= 0 && r.row0 + n <= p.rows && r.len >= 0 && r.len + n <= cap;
+    if (!ok && tell) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 1);
+    r.n = ok ? static_cast<int>(n) : 0;
+    return r;
+}
+// The keys [lo, hi) that tile t of a request's query rows can see, and its units.
+struct Span {
+    int lo, hi;                       // lo on a unit's border
+    __device__ __forceinline__ int units(int KT) const { return hi > lo ? (hi - lo + KT - 1) / KT : 1; }
+};
+template <int M, int KT>
+__device__ __forceinline__ Span span_of(const Args& p, const Request& r, int t) {
+    const int first = t * M / p.G;
+    const int last = (min(static_cast<int64_t>(t + 1) * M, static_cast<int64_t>(r.n) * p.G) - 1) / p.G;
+    Span s;
+    s.hi = r.len + last + 1;
+    const int lo = p.window > 0 ? max(0, r.len + first - p.window + 1) : 0;
+    s.lo = lo / KT * KT;
+    return s;
+}
+template <int M>
+__device__ __forceinline__ int tiles_of(const Args& p, const Request& r) {
+    return static_cast<int>((static_cast<int64_t>(r.n) * p.G + M - 1) / M);
+}
+// Units of one key head of a request.
+template <int M, int KT>
+__device__ __forceinline__ int64_t head_units(const Args& p, const Request& r) {
+    int64_t u = 0;
+    const int nt = tiles_of<M>(p, r);
+    for (int t = 0; t < nt; ++t) u += span_of<M, KT>(p, r, t).units(KT);
+    return u;
+}
+
+// The block's first unit: request, and units into it; found by all threads together.
+// scratch: 34 words of 8 bytes.
+struct Start {
+    int64_t total, first, last;       // units in all, and this block's [first, last)
+    int grid;                         // blocks that have units (no more than there are units)
+    int b;
+    int64_t into;                     // units before `first` in request b
+};
+template <int M, int KT, int kThreads>
+__device__ __forceinline__ Start find_start(const Args& p, long long* scratch) {
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += p.Hkv * head_units<M, KT>(p, request_of(p, b, blockIdx.x == 0));
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) scratch[w] = inc;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int i = 0; i < kThreads / 32; ++i) {
+        if (i < w) before += scratch[i];
+        total += scratch[i];
+    }
+    const long long at = before + inc - mine;
+    Start s;
+    s.total = total;
+    s.grid = total < gridDim.x ? static_cast<int>(total) : static_cast<int>(gridDim.x);
+    const int64_t c = blockIdx.x, n = s.grid;
+    s.first = c < n ? total * c / n : total;
+    s.last = c < n ? total * (c + 1) / n : total;
+    if (at <= s.first && s.first < at + mine) {
+        long long u = at;
+        for (int b = b0; b < b1; ++b) {
+            const long long c = p.Hkv * head_units<M, KT>(p, request_of(p, b, false));
+            if (s.first < u + c) {
+                scratch[32] = b;
+                scratch[33] = s.first - u;
+                break;
+            }
+            u += c;
+        }
+    }
+    __syncthreads();
+    s.b = static_cast<int>(scratch[32]);
+    s.into = scratch[33];
+    return s;
+}
+
+// The block that holds unit u of `total` over `grid` blocks.
+__device__ __forceinline__ int block_of(int64_t u, int64_t total, int grid) {
+    return static_cast<int>(((u + 1) * grid - 1) / total);
+}
+
+// A piece of a segment: units [u0, u1) of the segment's `units`.
+struct Piece {
+    Request r;
+    int b, h, tile;
+    Span span;
+    int u0, u1, units;
+    int64_t seg_first;                // the segment's first unit in the line
+    __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units; }
+};
+
+// Walks the block's units piece by piece (every thread the same way).
+template <int M, int KT>
+struct Walk {
+    const Args& p;
+    int64_t at, last, req_first, req_units;
+    int b;
+    Request r;
+    __device__ __forceinline__ Walk(const Args& args, const Start& s) : p(args), at(s.first), last(s.last), b(s.b) {
+        if (at < last) {
+            r = request_of(p, b, false);
+            req_first = at - s.into;
+            req_units = p.Hkv * head_units<M, KT>(p, r);
+        }
+    }
+    __device__ __forceinline__ bool next(Piece& out) {
+        if (at >= last) return false;
+        while (at >= req_first + req_units) {
+            req_first += req_units;
+            if (++b >= p.B) return false;      // only where the lengths change under the call
+            r = request_of(p, b, false);
+            req_units = p.Hkv * head_units<M, KT>(p, r);
+        }
+        const int64_t per_head = req_units / p.Hkv;
+        int64_t into = at - req_first;
+        out.h = static_cast<int>(into / per_head);
+        into -= out.h * per_head;
+        int t = 0;
+        Span sp = span_of<M, KT>(p, r, 0);
+        const int nt = tiles_of<M>(p, r);
+        while (into >= sp.units(KT) && t + 1 < nt) {
+            into -= sp.units(KT);
+            sp = span_of<M, KT>(p, r, ++t);
+        }
+        out.r = r;
+        out.b = b;
+        out.tile = t;
+        out.span = sp;
+        out.units = sp.units(KT);
+        out.u0 = static_cast<int>(into);
+        out.seg_first = at - into;
+        const int64_t left = last - at, rest = out.units - into;
+        const int n = static_cast<int>(left < rest ? left : rest);
+        out.u1 = out.u0 + n;
+        at += n;
+        return true;
+    }
+};
+
+// Where a part of a segment goes: two places a block, one for the part that starts its
+// segment (it is the block's last piece) and one for a part that does not.
+__device__ __forceinline__ int64_t part_place(int block, bool starts) { return 2ll * block + (starts ? 1 : 0); }
+
+// The page id at entry j of request b's table, checked.
+__device__ __forceinline__ int page_id(const Args& p, int b, int j) {
+    int id = __ldg(p.table + static_cast<int64_t>(b) * p.ld_table + j);
+    if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks)) {
+        set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 2);
+        id = 0;
+    }
+    return id;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_out(const Args& p, int64_t row, int head, int d, float x);
+template <>
+__device__ __forceinline__ void store_out<float>(const Args& p, int64_t row, int head, int d, float x) {
+    static_cast<float*>(p.out)[(row * p.Hq + head) * p.D + d] = x;
+}
+template <>
+__device__ __forceinline__ void store_out<__nv_bfloat16>(const Args& p, int64_t row, int head, int d, float x) {
+    static_cast<__nv_bfloat16*>(p.out)[(row * p.Hq + head) * p.D + d] = __float2bfloat16_rn(x);
+}
+
+// ln of the sum from a maximum in units of log 2 and the sum at it.
+__device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f || l != l ? (m + log2f(l)) * kLn2 : m; }
+
+// Announces a stored part; true in the block that has to join the segment.  All threads.
+__device__ __forceinline__ bool part_done(const Args& p, const Piece& pc, const Start& st, int* s_flag) {
+    const int c0 = block_of(pc.seg_first, st.total, st.grid);
+    const int c1 = block_of(pc.seg_first + pc.units - 1, st.total, st.grid);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) *s_flag = atomicAdd(&p.counters[c0], 1u) == static_cast<unsigned>(c1 - c0);
+    __syncthreads();
+    const bool join = *s_flag != 0;
+    if (join) __threadfence();
+    return join;
+}
+
+// Joins the parts of a segment, in the order of the keys, and writes its rows.
+template <typename T, int M, int kThreads>
+__device__ __forceinline__ void join_parts(const Args& p, const Piece& pc, const Start& st) {
+    const int c0 = block_of(pc.seg_first, st.total, st.grid);
+    const int c1 = block_of(pc.seg_first + pc.units - 1, st.total, st.grid);
+    const int valid = static_cast<int>(min(static_cast<int64_t>(M), static_cast<int64_t>(pc.r.n) * p.G - static_cast<int64_t>(pc.tile) * M));
+    const float ninf = -__uint_as_float(0x7f800000u);
+    for (int e = threadIdx.x; e < valid * p.D; e += kThreads) {
+        const int m = e / p.D, d = e - m * p.D;
+        float mx = ninf, l = 0.f, o = 0.f;
+        for (int c = c0; c <= c1; ++c) {
+            const int64_t at = part_place(c, c == c0) * M + m;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at);
+            const float x = __ldcg(p.part_o + at * p.D + d);
+            const float nm = fmaxf(mx, ml.x);
+            const float use = nm == ninf ? 0.f : nm;
+            const float a = fast_exp2(mx - use), c2 = fast_exp2(ml.x - use);
+            l = l * a + ml.y * c2;
+            o = o * a + x * c2;
+            mx = nm;
+        }
+        const int qi = pc.tile * M + m, row = qi / p.G, head = pc.h * p.G + qi % p.G;
+        store_out<T>(p, static_cast<int64_t>(pc.r.row0) + row, head, d, l != 0.f ? o / l : 0.f);
+        if (d == 0 && p.lse != nullptr)
+            p.lse[(static_cast<int64_t>(pc.r.row0) + row) * p.Hq + head] = lse_of(mx, l);
+    }
+}
+
+}  // namespace attn
+}  // namespace dspark

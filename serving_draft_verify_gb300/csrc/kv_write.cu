@@ -1,0 +1,168 @@
+// dspark_write_kv: the keys and values of a step's rows into the paged cache.
+//
+// cache[slot / page][head][slot % page][:] = row[head][:], copied, or stored in
+// 8 bits as e4m3(clamp(x / scale[head], +-448)), rounded to nearest even.  The
+// quotient is formed in float32 by an IEEE division; NaN stays NaN.
+//
+// Bound by memory: each element is read once and written once.  A thread moves
+// eight elements (one or two 16-byte loads); a block takes as many whole rows as
+// give it four such items a thread, all loads issued before the first store.
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "host_common.h"
+
+namespace dspark {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kItems = 4;
+
+struct WriteArgs {
+    int64_t rows, k_stride, v_stride, slots;   // strides in elements
+    int heads, D, page, rows_per_block, parts;  // parts: 8-element pieces of one row of one tensor
+    const void *k, *v;
+    const int64_t* slot;
+    const float *k_scale, *v_scale;
+    void *kc, *vc;
+    StatusBlock* status;
+};
+
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+    uint4 w;
+    __device__ void load(const void* p) { w = __ldg(static_cast<const uint4*>(p)); }
+    __device__ void store(void* p) const { *static_cast<uint4*>(p) = w; }
+    __device__ void floats(float* f) const {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = bf16lo(u[i]);
+            f[2 * i + 1] = bf16hi(u[i]);
+        }
+    }
+};
+template <>
+struct Eight<float> {
+    float4 a, b;
+    __device__ void load(const void* p) {
+        a = __ldg(static_cast<const float4*>(p));
+        b = __ldg(static_cast<const float4*>(p) + 1);
+    }
+    __device__ void store(void* p) const {
+        static_cast<float4*>(p)[0] = a;
+        static_cast<float4*>(p)[1] = b;
+    }
+    __device__ void floats(float* f) const {
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+        f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    }
+};
+
+template <typename T, bool kFp8>
+__global__ void __launch_bounds__(kThreads) write_kv(WriteArgs p) {
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_block;
+    const int64_t left = p.rows - row0;
+    const int nrows = left < p.rows_per_block ? static_cast<int>(left) : p.rows_per_block;
+    const int per_row = 2 * p.parts, total = nrows * per_row, per_head = p.D / 8;
+    for (int i0 = threadIdx.x; i0 < total; i0 += kThreads * kItems) {
+        Eight<T> x[kItems];
+        int64_t to[kItems];
+        int head[kItems];
+        bool is_v[kItems];
+#pragma unroll
+        for (int j = 0; j < kItems; ++j) {
+            const int i = i0 + j * kThreads;
+            to[j] = -1;
+            if (i < total) {
+                const int r = i / per_row, e = i - r * per_row;
+                is_v[j] = e >= p.parts;
+                const int part = is_v[j] ? e - p.parts : e;
+                head[j] = part / per_head;
+                const int64_t slot = __ldg(p.slot + row0 + r);
+                if (slot >= p.slots) {
+                    if (e == 0) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 1);
+                } else if (slot >= 0) {
+                    const int64_t block = slot / p.page, off = slot - block * p.page;
+                    to[j] = ((block * p.heads + head[j]) * p.page + off) * p.D + (part - head[j] * per_head) * 8;
+                    const T* from = is_v[j] ? static_cast<const T*>(p.v) + (row0 + r) * p.v_stride
+                                            : static_cast<const T*>(p.k) + (row0 + r) * p.k_stride;
+                    x[j].load(from + static_cast<int64_t>(part) * 8);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kItems; ++j) {
+            if (to[j] < 0) continue;
+            void* cache = is_v[j] ? p.vc : p.kc;
+            if constexpr (kFp8) {
+                const float s = __ldg((is_v[j] ? p.v_scale : p.k_scale) + head[j]);
+                float f[8];
+                x[j].floats(f);
+                uint32_t w[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float2 lo = make_float2(__fdiv_rn(f[4 * h], s), __fdiv_rn(f[4 * h + 1], s));
+                    const float2 hi = make_float2(__fdiv_rn(f[4 * h + 2], s), __fdiv_rn(f[4 * h + 3], s));
+                    w[h] = __nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
+                           (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3)) << 16);
+                }
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + to[j]) = make_uint2(w[0], w[1]);
+            } else {
+                x[j].store(static_cast<T*>(cache) + to[j]);
+            }
+        }
+    }
+}
+
+}  // namespace
+}  // namespace dspark
+
+extern "C" size_t dspark_write_kv_workspace_size(void) { return dspark::kStatusBytes; }
+
+extern "C" dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int page, int num_blocks, dspark_dtype_t dt,
+                                           dspark_dtype_t cache_dt, const void* k, int64_t k_stride, const void* v,
+                                           int64_t v_stride, const int64_t* slot, const float* k_scale,
+                                           const float* v_scale, void* k_cache, void* v_cache, void* workspace,
+                                           size_t workspace_bytes, dspark_stream_t stream) {
+    using namespace dspark;
+    if (rows < 0 || rows > 0x7fffffffll || Hkv < 1 || Hkv > 1024 || D < 8 || D > 256 || D % 8 != 0 || page < 1 ||
+        num_blocks < 1)
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    if ((dt != DSPARK_BF16 && dt != DSPARK_F32) || (cache_dt != dt && cache_dt != DSPARK_E4M3))
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    if (cache_dt == DSPARK_E4M3 && (D % 16 != 0 || k_scale == nullptr || v_scale == nullptr))
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    const int64_t width = static_cast<int64_t>(Hkv) * D, align = dt == DSPARK_BF16 ? 8 : 4;
+    if (k_stride < width || v_stride < width || k_stride % align != 0 || v_stride % align != 0)
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    if (k_cache == nullptr || v_cache == nullptr || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k) ||
+        !aligned16(v) || (rows > 0 && (k == nullptr || v == nullptr || slot == nullptr)))
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    if (workspace == nullptr || !aligned256(workspace)) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < dspark_write_kv_workspace_size()) return DSPARK_ERR_WORKSPACE_TOO_SMALL;
+    clear_stale_error();
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (clear_status(workspace, s) != DSPARK_OK) return DSPARK_ERR_CUDA;
+    if (rows == 0) return DSPARK_OK;
+    WriteArgs p{};
+    p.rows = rows, p.k_stride = k_stride, p.v_stride = v_stride;
+    p.slots = static_cast<int64_t>(num_blocks) * page;
+    p.heads = Hkv, p.D = D, p.page = page;
+    p.parts = static_cast<int>(width / 8);
+    const int want = kThreads * kItems / (2 * p.parts);
+    p.rows_per_block = want > 1 ? want : 1;
+    p.k = k, p.v = v, p.slot = slot, p.k_scale = k_scale, p.v_scale = v_scale, p.kc = k_cache, p.vc = v_cache;
+    p.status = static_cast<StatusBlock*>(workspace);
+    const unsigned grid = static_cast<unsigned>((rows + p.rows_per_block - 1) / p.rows_per_block);
+    if (dt == DSPARK_BF16) {
+        if (cache_dt == DSPARK_E4M3) write_kv<__nv_bfloat16, true><<<grid, kThreads, 0, s>>>(p);
+        else write_kv<__nv_bfloat16, false><<<grid, kThreads, 0, s>>>(p);
+    } else {
+        if (cache_dt == DSPARK_E4M3) write_kv<float, true><<<grid, kThreads, 0, s>>>(p);
+        else write_kv<float, false><<<grid, kThreads, 0, s>>>(p);
+    }
+    return launch_status();
+}
