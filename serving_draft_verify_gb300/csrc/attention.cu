@@ -3,12 +3,13 @@
 #include <cuda_fp8.h>
 
 #include "attn.cuh"
+#include "attn_mma.cuh"
 
 namespace dspark {
 namespace attn {
 namespace {
 
-// ------------------------------------------------------- plain arithmetic ---
+// ------------------------------------------------------------ float32 rows ---
 // Sixteen query rows (four a warp) over 32 keys a unit, float32 throughout: a lane is
 // a key for the scores and a column for the values.
 constexpr int kSimtM = 16, kSimtKT = 32, kSimtThreads = 128;
@@ -20,17 +21,12 @@ __device__ __forceinline__ float4 load4<float>(const void* base, int64_t i) {
     return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i));
 }
 template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const void* base, int64_t i) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + i));
-    return make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
-}
-template <>
 __device__ __forceinline__ float4 load4<__nv_fp8_e4m3>(const void* base, int64_t i) {
     const __nv_fp8x4_e4m3 u = *reinterpret_cast<const __nv_fp8x4_e4m3*>(static_cast<const uint8_t*>(base) + i);
     return static_cast<float4>(u);
 }
 
-template <typename T, typename C, int kCols>
+template <typename C, int kCols>
 __global__ void __launch_bounds__(kSimtThreads) attend_simt(Args p) {
     constexpr int M = kSimtM, KT = kSimtKT;
     extern __shared__ float4 smem4[];
@@ -56,7 +52,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(Args p) {
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (m < valid) {
                 const int qi = pc.tile * M + m;
-                x = load4<T>(p.q, (static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.q_stride +
+                x = load4<float>(p.q, (static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.q_stride +
                                       static_cast<int64_t>(pc.h * p.G + qi % p.G) * p.D + d);
             }
             *reinterpret_cast<float4*>(s_q + m * p.D + d) = make_float4(x.x * qs, x.y * qs, x.z * qs, x.w * qs);
@@ -134,7 +130,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(Args p) {
                 const int64_t row = static_cast<int64_t>(pc.r.row0) + qi / p.G;
 #pragma unroll
                 for (int c = 0; c < kCols; ++c)
-                    if (lane + 32 * c < p.D) store_out<T>(p, row, head, lane + 32 * c, l[r] != 0.f ? o[r][c] * vs / l[r] : 0.f);
+                    if (lane + 32 * c < p.D) store_out<float>(p, row, head, lane + 32 * c, l[r] != 0.f ? o[r][c] * vs / l[r] : 0.f);
                 if (lane == 0 && p.lse != nullptr) p.lse[row * p.Hq + head] = lse_of(mx[r], l[r]);
             }
         } else {
@@ -147,38 +143,41 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(Args p) {
                     if (lane + 32 * c < p.D) p.part_o[at * p.D + lane + 32 * c] = o[r][c] * vs;
                 if (lane == 0) reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(mx[r], l[r]);
             }
-            if (part_done(p, pc, st, &s_flag)) join_parts<T, M, kSimtThreads>(p, pc, st);
+            if (part_done(p, pc, st, &s_flag)) join_parts<float, M, kSimtThreads>(p, pc, st);
         }
     }
 }
 
-template <typename T, typename C, int kCols>
-dspark_status_t launch_simt(const Args& p, int grid, cudaStream_t s) {
+template <typename C, int kCols>
+dspark_status_t launch_simt(const Args& p, cudaStream_t s) {
     const size_t smem = (static_cast<size_t>(kSimtM) * p.D + 2 * kSimtKT * (p.D + 4) + kSimtM * kSimtKT) * 4;
     static OncePerDevice once;
     if (once.run(current_device(), [] {
-            return cudaFuncSetAttribute(attend_simt<T, C, kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            return cudaFuncSetAttribute(attend_simt<C, kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (kSimtM * 256 + 2 * kSimtKT * 260 + kSimtM * kSimtKT) * 4);
         }) != cudaSuccess)
         return DSPARK_ERR_CUDA;
-    attend_simt<T, C, kCols><<<grid, kSimtThreads, smem, s>>>(p);
+    const int grid = grid_for(sm_count(current_device()) * (kCols <= 4 ? 4 : 2), kSimtM);
+    if (grid < 1) return DSPARK_ERR_CUDA;
+    attend_simt<C, kCols><<<grid, kSimtThreads, smem, s>>>(p);
     return launch_status();
 }
-template <typename T, typename C>
-dspark_status_t launch_simt(const Args& p, int grid, cudaStream_t s) {
-    if (p.D <= 64) return launch_simt<T, C, 2>(p, grid, s);
-    if (p.D <= 128) return launch_simt<T, C, 4>(p, grid, s);
-    return launch_simt<T, C, 8>(p, grid, s);
+template <typename C>
+dspark_status_t launch_f32(const Args& p, cudaStream_t s) {
+    if (p.D <= 64) return launch_simt<C, 2>(p, s);
+    if (p.D <= 128) return launch_simt<C, 4>(p, s);
+    return launch_simt<C, 8>(p, s);
 }
 
-// Blocks of the launch: as many as can be resident, so that the even division is one wave.
-int grid_of(int D) {
-    const int sms = sm_count(current_device());
-    const int per_sm = D <= 128 ? 4 : 2;
-    const int n = sms * per_sm;
-    return n > kMaxGrid ? kMaxGrid : n;
+// bf16 rows: the instructions take 16 query rows at a time, two such tiles where a request has
+// more than 16 (and the output rows still fit the registers).
+template <bool kFp8>
+dspark_status_t launch_bf16(const Args& p, cudaStream_t s) {
+    const bool two = static_cast<int64_t>(p.max_rows) * p.G > 16;
+    if (p.D <= 64) return two ? launch_mma<kFp8, 2, 64>(p, s) : launch_mma<kFp8, 1, 64>(p, s);
+    if (p.D <= 128) return two ? launch_mma<kFp8, 2, 128>(p, s) : launch_mma<kFp8, 1, 128>(p, s);
+    return launch_mma<kFp8, 1, 256>(p, s);
 }
-constexpr int kPartRows = kSimtM;
 
 }  // namespace
 }  // namespace attn
@@ -187,8 +186,7 @@ constexpr int kPartRows = kSimtM;
 extern "C" size_t dspark_paged_attention_workspace_size(int D) {
     using namespace dspark;
     if (D < 1) return 0;
-    const size_t places = 2 * static_cast<size_t>(attn::kMaxGrid) * attn::kPartRows;
-    return kStatusBytes + attn::kCounterBytes + places * (static_cast<size_t>(D) + 2) * 4;
+    return kStatusBytes + attn::kCounterBytes + static_cast<size_t>(attn::kMaxPartRows) * (D + 2) * 4;
 }
 
 extern "C" dspark_status_t dspark_paged_attention(
@@ -233,13 +231,8 @@ extern "C" dspark_status_t dspark_paged_attention(
     p.status = reinterpret_cast<StatusBlock*>(ws);
     p.counters = reinterpret_cast<uint32_t*>(ws + kStatusBytes);
     p.part_ml = reinterpret_cast<float*>(ws + kStatusBytes + attn::kCounterBytes);
-    p.part_o = p.part_ml + 2 * static_cast<size_t>(attn::kMaxGrid) * attn::kPartRows * 2;
-    const int grid = attn::grid_of(D);
-    if (grid < 1) return DSPARK_ERR_CUDA;
-    if (dt == DSPARK_BF16) {
-        if (cache_dt == DSPARK_E4M3) return attn::launch_simt<__nv_bfloat16, __nv_fp8_e4m3>(p, grid, s);
-        return attn::launch_simt<__nv_bfloat16, __nv_bfloat16>(p, grid, s);
-    }
-    if (cache_dt == DSPARK_E4M3) return attn::launch_simt<float, __nv_fp8_e4m3>(p, grid, s);
-    return attn::launch_simt<float, float>(p, grid, s);
+    p.part_o = p.part_ml + 2 * static_cast<size_t>(attn::kMaxPartRows);
+    const bool fp8 = cache_dt == DSPARK_E4M3;
+    if (dt == DSPARK_BF16) return fp8 ? attn::launch_bf16<true>(p, s) : attn::launch_bf16<false>(p, s);
+    return fp8 ? attn::launch_f32<__nv_fp8_e4m3>(p, s) : attn::launch_f32<float>(p, s);
 }

@@ -41,8 +41,15 @@ struct Args {
     float* part_o;                    // [2 grid][M][D]
 };
 
-constexpr size_t kCounterBytes = 4096;      // up to 1024 blocks
 constexpr int kMaxGrid = 1024;
+constexpr size_t kCounterBytes = kMaxGrid * 4;
+constexpr int kMaxPartRows = 40960;         // query rows of all places: 2 grid M of any launch
+
+// Blocks of a launch: as many as can be resident, so that the even division is one wave.
+inline int grid_for(int resident, int M) {
+    int n = resident < kMaxGrid ? resident : kMaxGrid;
+    return n < kMaxPartRows / (2 * M) ? n : kMaxPartRows / (2 * M);
+}
 
 struct Request {
     int row0, n, len;                 // first row, rows, keys before the step
