@@ -4,6 +4,7 @@
 
 #include "attn.cuh"
 #include "attn_mma.cuh"
+#include "attn_tc.cuh"
 
 namespace dspark {
 namespace attn {
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(Args p) {
                     if (lane + 32 * c < p.D) p.part_o[at * p.D + lane + 32 * c] = o[r][c] * vs;
                 if (lane == 0) reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(mx[r], l[r]);
             }
-            if (part_done(p, pc, st, &s_flag)) join_parts<float, M, kSimtThreads>(p, pc, st);
+            if (part_done(p, pc, st, &s_flag, tid, [] { __syncthreads(); })) join_parts<float, M, kSimtThreads>(p, pc, st, tid);
         }
     }
 }
@@ -173,7 +174,10 @@ dspark_status_t launch_f32(const Args& p, cudaStream_t s) {
 // more than 16 (and the output rows still fit the registers).
 template <bool kFp8>
 dspark_status_t launch_bf16(const Args& p, cudaStream_t s) {
-    const bool two = static_cast<int64_t>(p.max_rows) * p.G > 16;
+    const int64_t most = static_cast<int64_t>(p.max_rows) * p.G;
+    if constexpr (!kFp8)
+        if (most > 32 && tc_fits(p)) return p.D <= 64 ? launch_tc<64>(p, s) : launch_tc<128>(p, s);
+    const bool two = most > 16;
     if (p.D <= 64) return two ? launch_mma<kFp8, 2, 64>(p, s) : launch_mma<kFp8, 1, 64>(p, s);
     if (p.D <= 128) return two ? launch_mma<kFp8, 2, 128>(p, s) : launch_mma<kFp8, 1, 128>(p, s);
     return launch_mma<kFp8, 1, 256>(p, s);

@@ -238,14 +238,17 @@ __device__ __forceinline__ void store_out<__nv_bfloat16>(const Args& p, int64_t 
 // ln of the sum from a maximum in units of log 2 and the sum at it.
 __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f || l != l ? (m + log2f(l)) * kLn2 : m; }
 
-// Announces a stored part; true in the block that has to join the segment.  All threads.
-__device__ __forceinline__ bool part_done(const Args& p, const Piece& pc, const Start& st, int* s_flag) {
+// Announces a stored part; true in the block that has to join the segment.  Called by the
+// `tid` 0 .. n - 1 that stored it, which sync() brings together.
+template <class Sync>
+__device__ __forceinline__ bool part_done(const Args& p, const Piece& pc, const Start& st, int* s_flag, int tid,
+                                          Sync sync) {
     const int c0 = block_of(pc.seg_first, st.total, st.grid);
     const int c1 = block_of(pc.seg_first + pc.units - 1, st.total, st.grid);
     __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) *s_flag = atomicAdd(&p.counters[c0], 1u) == static_cast<unsigned>(c1 - c0);
-    __syncthreads();
+    sync();
+    if (tid == 0) *s_flag = atomicAdd(&p.counters[c0], 1u) == static_cast<unsigned>(c1 - c0);
+    sync();
     const bool join = *s_flag != 0;
     if (join) __threadfence();
     return join;
@@ -253,12 +256,12 @@ __device__ __forceinline__ bool part_done(const Args& p, const Piece& pc, const 
 
 // Joins the parts of a segment, in the order of the keys, and writes its rows.
 template <typename T, int M, int kThreads>
-__device__ __forceinline__ void join_parts(const Args& p, const Piece& pc, const Start& st) {
+__device__ __forceinline__ void join_parts(const Args& p, const Piece& pc, const Start& st, int tid) {
     const int c0 = block_of(pc.seg_first, st.total, st.grid);
     const int c1 = block_of(pc.seg_first + pc.units - 1, st.total, st.grid);
     const int valid = static_cast<int>(min(static_cast<int64_t>(M), static_cast<int64_t>(pc.r.n) * p.G - static_cast<int64_t>(pc.tile) * M));
     const float ninf = -__uint_as_float(0x7f800000u);
-    for (int e = threadIdx.x; e < valid * p.D; e += kThreads) {
+    for (int e = tid; e < valid * p.D; e += kThreads) {
         const int m = e / p.D, d = e - m * p.D;
         float mx = ninf, l = 0.f, o = 0.f;
         for (int c = c0; c <= c1; ++c) {

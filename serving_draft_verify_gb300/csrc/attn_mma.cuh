@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
                 if (d == 0) reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(big - kShift, sum);
             }
         }
-        if (!whole && part_done(p, pc, st, &s_flag)) join_parts<__nv_bfloat16, M, kThreads>(p, pc, st);
+        if (!whole && part_done(p, pc, st, &s_flag, tid, [] { __syncthreads(); })) join_parts<__nv_bfloat16, M, kThreads>(p, pc, st, tid);
         __syncthreads();
     }
 }

@@ -1,0 +1,528 @@
+// Attention of many query rows a request (verification of a long draft, wide groups of
+// heads, prompts): 128 query rows of a key head at a time on tcgen05.
+//
+// At 128 rows a key costs 4 * 128 * D operations for 4 D bytes, more than the warp-level
+// instructions can do while the bytes arrive, and less than tcgen05 can: per unit of 128 keys
+// at D = 128 the products take about 1536 tensor cycles (S once, P V twice) and the softmax
+// about as many of one warpgroup, next to 2800 cycles for the unit's 64 KB at the measured
+// bandwidth.  So one block an SM, with a warp for each thing that can run by itself:
+//
+//   warp 0      keys and values into two-stage rings by TMA (boxes of up to 128 rows that lie on one
+//               page, 128-byte swizzle), running ahead across pieces;
+//   warp 1      the products: S = Q K^T into one of two TMEM buffers, one unit ahead, and
+//               O += P V with P from TMEM and V as it lies (its rows are the contraction:
+//               an MN-major operand);
+//   warps 2, 3  the next piece's queries into the other of two buffers;
+//   warps 4-7   a thread a query row: maximum, P = 2^(S - m) as two bf16 terms (high + low, so
+//               that 16 bits of P count) into TMEM, the sum, and the output at the end.
+// The output in TMEM is rescaled only where a maximum has grown by more than 2^8 over the one
+// in use (the factor stays in P and the sum alike until then).
+//
+// TMEM (512 columns): S 2 x 128, P 64 high + 64 low, O up to 128.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "attn_mma.cuh"
+#include "engine.cuh"
+#include "tc.cuh"
+
+namespace dspark {
+namespace attn {
+
+// Shared-memory descriptor of an MN-major operand with the 128-byte swizzle: 64 elements of the
+// M / N extent to a 128-byte row, a row for every k; 8 rows 1024 bytes apart (stride), the next 64
+// elements `half` bytes apart (leading).
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t half) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((half >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+// D[tmem] (+)= A[tmem] B[smem desc].
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+constexpr int kTcM = 128, kTcKT = 128, kTcThreads = 256, kTcRows = 128;   // kTcRows: threads of the softmax
+
+template <int DT>
+struct TcShape {
+    static constexpr int kHalves = DT / 64;
+    static constexpr int kHalf = 128 * 128;                  // bytes of 64 columns of 128 rows
+    static constexpr int kTile = kHalves * kHalf;
+    static constexpr int kSmem = 6 * kTile + 1024;           // Q, K, V twice each; 1024: alignment
+};
+struct TcBars {
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], q_empty[2], s_full[2], s_empty[2], p_full, pv_done;
+};
+
+// The units of a block one by one, over its pieces.
+struct Units {
+    Walk<kTcM, kTcKT> walk;
+    Piece pc;
+    int u, piece;
+    bool ok;
+    __device__ __forceinline__ Units(const Args& p, const Start& st) : walk(p, st), u(0), piece(0) {
+        ok = walk.next(pc);
+        if (ok) u = pc.u0;
+    }
+    __device__ __forceinline__ bool first() const { return u == pc.u0; }
+    __device__ __forceinline__ bool last() const { return u + 1 == pc.u1; }
+    __device__ __forceinline__ void next() {
+        if (++u < pc.u1) return;
+        ok = walk.next(pc);
+        if (ok) {
+            u = pc.u0;
+            ++piece;
+        }
+    }
+};
+
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(x ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attend_tc(Args p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int box) {
+    using Sh = TcShape<DT>;
+    extern __shared__ unsigned char raw[];
+    unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    unsigned char* s_q = smem;                               // [2] tiles: [halves][128 rows][128 bytes]
+    unsigned char* s_k = smem + 2 * Sh::kTile;
+    unsigned char* s_v = smem + 4 * Sh::kTile;
+    __shared__ long long scratch[34];
+    __shared__ __align__(8) TcBars bars;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_flag;
+    __shared__ volatile int s_dead, s_keep;                  // s_keep: the piece's first product adds to what O holds
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.k_full[i], 1);
+            mbar_init(&bars.k_empty[i], 1);
+            mbar_init(&bars.v_full[i], 1);
+            mbar_init(&bars.v_empty[i], 1);
+            mbar_init(&bars.q_full[i], 64);
+            mbar_init(&bars.q_empty[i], 1);
+            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.s_empty[i], kTcRows);
+        }
+        mbar_init(&bars.p_full, kTcRows);
+        mbar_init(&bars.pv_done, 1);
+        fence_mbar_init();
+        s_dead = 0;
+        s_keep = 0;
+    }
+    if (w == 1) tc::tmem_alloc(&s_tmem, 512);
+    tc::fence_before_sync();
+    const Start st = find_start<kTcM, kTcKT, kTcThreads>(p, scratch);
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s_tmem, t_p = tmem + 256, t_o = tmem + 384;
+
+    // A wait that runs out ends all waiting: every role goes on through its units without
+    // issuing anything, so that the block ends, and the status tells.
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (s_dead) return;
+        if (!mbar_wait(bar, parity & 1)) {
+            s_dead = 1;
+            set_status(p.status, DSPARK_ERR_TIMEOUT, 1);
+        }
+    };
+
+    if (w == 0) {
+        // ------------------------------------------------------- keys and values ---
+        const uint64_t policy = policy_evict_normal();
+        uint32_t i = 0;
+        for (Units un(p, st); un.ok; un.next(), ++i) {
+            const int stage = i & 1, k0 = un.pc.span.lo + un.u * kTcKT;
+            const int keys = min(kTcKT, un.pc.span.hi - k0), boxes = (keys + box - 1) / box;
+            const uint32_t bytes = boxes * box * 128 * Sh::kHalves;
+            // lane l has box l: its row in both tiles
+            int y = 0;
+            if (lane < boxes) {
+                const int key = k0 + lane * box, blk = key / p.page;
+                y = (page_id(p, un.pc.b, blk) * p.Hkv + un.pc.h) * p.page + (key - blk * p.page);
+            }
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                uint64_t* full = kv ? &bars.v_full[stage] : &bars.k_full[stage];
+                if (lane == 0) {
+                    wait(kv ? &bars.v_empty[stage] : &bars.k_empty[stage], (i >> 1) + 1);
+                    if (!s_dead) mbar_arrive_expect_tx(full, bytes);
+                }
+                __syncwarp();
+                if (s_dead) continue;
+                unsigned char* to = (kv ? s_v : s_k) + stage * Sh::kTile;
+                if (lane < boxes)
+                    for (int h = 0; h < Sh::kHalves; ++h)
+                        tc::tma_load_2d(to + h * Sh::kHalf + lane * box * 128, kv ? &vmap : &kmap, 64 * h, y, full, policy);
+            }
+        }
+        if (s_dead && lane == 0) {
+            // copies still in flight end before the block does
+            for (uint32_t j = i > 2 ? i - 2 : 0; j < i; ++j) {
+                mbar_wait(&bars.k_full[j & 1], (j >> 1) & 1);
+                mbar_wait(&bars.v_full[j & 1], (j >> 1) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (w == 1) {
+        // -------------------------------------------------------------- products ---
+        if (lane == 0) {
+            const uint32_t id_s = tc::idesc_bf16_f32(kTcM, kTcKT);
+            const uint32_t id_o = tc::idesc_bf16_f32(kTcM, DT) | (1u << 16);      // B is MN-major
+            uint32_t iq = 0;
+            auto scores = [&](const Units& un) {
+                const int stage = iq & 1, qb = un.piece & 1;
+                if (un.first()) wait(&bars.q_full[qb], un.piece >> 1);
+                wait(&bars.s_empty[stage], (iq >> 1) + 1);
+                wait(&bars.k_full[stage], iq >> 1);
+                tc::fence_after_sync();
+                if (!s_dead) {
+                    const uint32_t qa = smem_u32(s_q) + qb * Sh::kTile, ka = smem_u32(s_k) + stage * Sh::kTile;
+#pragma unroll
+                    for (int ks = 0; ks < DT / 16; ++ks) {
+                        const uint32_t off = (ks >> 2) * Sh::kHalf + (ks & 3) * 32;
+                        tc::mma_bf16(tmem + stage * 128, tc::smem_desc_sw128(qa + off), tc::smem_desc_sw128(ka + off), id_s, ks > 0);
+                    }
+                    tc::commit(&bars.s_full[stage]);
+                    tc::commit(&bars.k_empty[stage]);
+                    if (un.last()) tc::commit(&bars.q_empty[qb]);
+                }
+                ++iq;
+            };
+            Units ahead(p, st);
+            if (ahead.ok) {
+                scores(ahead);
+                ahead.next();
+            }
+            uint32_t i = 0;
+            for (Units un(p, st); un.ok; un.next(), ++i) {
+                if (ahead.ok) {
+                    scores(ahead);
+                    ahead.next();
+                }
+                const int stage = i & 1;
+                wait(&bars.v_full[stage], i >> 1);
+                wait(&bars.p_full, i);
+                tc::fence_after_sync();
+                if (!s_dead) {
+                    const uint32_t va = smem_u32(s_v) + stage * Sh::kTile;
+                    const bool keep = !un.first() || s_keep;
+#pragma unroll
+                    for (int ks = 0; ks < kTcKT / 16; ++ks)
+                        mma_bf16_ts(t_o, t_p + ks * 8, desc_mn_sw128(va + ks * 2048, Sh::kHalf), id_o, keep || ks > 0);
+#pragma unroll
+                    for (int ks = 0; ks < kTcKT / 16; ++ks)
+                        mma_bf16_ts(t_o, t_p + 64 + ks * 8, desc_mn_sw128(va + ks * 2048, Sh::kHalf), id_o, 1);
+                    tc::commit(&bars.pv_done);
+                    tc::commit(&bars.v_empty[stage]);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (w < 4) {
+        // --------------------------------------------------------------- queries ---
+        Walk<kTcM, kTcKT> walk(p, st);
+        Piece pc;
+        for (int n = 0; walk.next(pc); ++n) {
+            wait(&bars.q_empty[n & 1], (n >> 1) + 1);
+            const int left = pc.r.n * p.G - pc.tile * kTcM, valid = left < kTcM ? left : kTcM;
+            unsigned char* to = s_q + (n & 1) * Sh::kTile;
+#pragma unroll 4
+            for (int e = tid - 64; e < kTcM * (DT / 8); e += 64) {
+                const int m = e / (DT / 8), c = e % (DT / 8);
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (m < valid && c * 8 < p.D) {
+                    const int qi = pc.tile * kTcM + m;
+                    x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                             (static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.q_stride +
+                                                             static_cast<int64_t>(pc.h * p.G + qi % p.G) * p.D + c * 8));
+                }
+                *reinterpret_cast<uint4*>(to + (c >> 3) * Sh::kHalf + m * 128 + (((c & 7) ^ (m & 7)) << 4)) = x;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&bars.q_full[n & 1]);
+        }
+    } else {
+        // --------------------------------------------------------------- softmax ---
+        const int m = tid - 128;                             // the thread's query row and TMEM lane
+        const uint32_t lanes = static_cast<uint32_t>(w - 4) << 21;   // (warp's first lane) << 16
+        const float ninf = -__uint_as_float(0x7f800000u);
+        float used = ninf, l = 0.f;
+        uint32_t i = 0;
+        for (Units un(p, st); un.ok; un.next(), ++i) {
+            const Piece& pc = un.pc;
+            const int stage = i & 1, k0 = pc.span.lo + un.u * kTcKT;
+            const int left = pc.r.n * p.G - pc.tile * kTcM, valid = left < kTcM ? left : kTcM;
+            const int pos = pc.r.len + (pc.tile * kTcM + m) / p.G;
+            const int pos_lo = pc.r.len + pc.tile * kTcM / p.G, pos_hi = pc.span.hi - 1;
+            const bool busy = (w - 4) * 32 < valid;          // the warp has rows
+            const bool masked = k0 + kTcKT - 1 > pos_lo || (p.window > 0 && k0 <= pos_hi - p.window);
+            if (un.first()) {
+                used = ninf;
+                l = 0.f;
+                if (m == 0) s_keep = 0;
+            }
+            // the columns of this unit that the row sees: [c_lo, c_hi)
+            const int c_hi = min(pos, pos_hi) + 1 - k0, c_lo = p.window > 0 ? pos - p.window + 1 - k0 : 0;
+            if (masked) {
+                // Values at keys past the last one, and values that are not finite at keys that only
+                // some rows see, must not meet the product (0 times them is not 0).  The former become
+                // 0; the latter are added here to the rows that see them and become 0 too.
+                wait(&bars.v_full[stage], i >> 1);
+                unsigned char* v = s_v + stage * Sh::kTile;
+                bool odd = false;
+                const int key = k0 + m;
+                if (key >= pc.span.hi) {
+                    for (int h = 0; h < Sh::kHalves; ++h)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            *reinterpret_cast<uint4*>(v + h * Sh::kHalf + m * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+                } else {
+                    for (int h = 0; h < Sh::kHalves; ++h)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(v + h * Sh::kHalf + m * 128 + c * 16);
+                            odd |= any_odd<false>(x.x) || any_odd<false>(x.y) || any_odd<false>(x.z) || any_odd<false>(x.w);
+                        }
+                }
+                const bool some = softmax_any(odd);
+                if (un.first() && m == 0 && some) s_keep = 1;
+                if (some) {
+                    if (i > 0) wait(&bars.pv_done, i - 1);
+                    tc::fence_after_sync();
+                    for (int c = 0; c < DT; c += 32) {
+                        float o[32];
+                        if (un.first()) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = 0.f;
+                        } else {
+                            tc::tmem_ld32(t_o + lanes + c, o);
+                            tc::tmem_ld_wait();
+                        }
+                        for (int j = max(c_lo, 0); j < min(c_hi, kTcKT); ++j) {
+                            const unsigned char* at = v + (c >> 6) * Sh::kHalf + j * 128;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const int d = (c & 63) + k;
+                                const uint32_t bits = *reinterpret_cast<const uint16_t*>(at + (((d >> 3) ^ (j & 7)) << 4) + (d & 7) * 2);
+                                if (any_odd<false>(bits)) o[k] += bf16lo(bits);
+                            }
+                        }
+                        __syncwarp();
+                        tmem_st32(t_o + lanes + c, reinterpret_cast<const uint32_t*>(o));
+                    }
+                    tmem_st_wait();
+                    softmax_sync();
+                    for (int h = 0; h < Sh::kHalves; ++h)
+                        for (int c = 0; c < 32; ++c) {
+                            uint32_t* x = reinterpret_cast<uint32_t*>(v + h * Sh::kHalf + m * 128) + c;
+                            *x = without_odd<false>(*x);
+                        }
+                }
+                fence_proxy_async_smem();
+            }
+            wait(&bars.s_full[stage], i >> 1);
+            tc::fence_after_sync();
+            float s[kTcKT];
+            if (busy) {
+#pragma unroll
+                for (int c = 0; c < kTcKT; c += 32) tc::tmem_ld32(tmem + stage * 128 + lanes + c, s + c);
+                tc::tmem_ld_wait();
+            }
+            tc::fence_before_sync();
+            mbar_arrive(&bars.s_empty[stage]);
+            uint32_t hi[kTcKT / 2];
+            if (busy) {
+                float top = ninf;
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < kTcKT; ++c) {
+                        s[c] = c >= c_lo && c < c_hi ? s[c] * p.scale_log2 : ninf;
+                        top = fmaxf(top, s[c]);
+                    }
+                } else {
+                    float t4[4] = {ninf, ninf, ninf, ninf};
+#pragma unroll
+                    for (int c = 0; c < kTcKT; ++c) {
+                        s[c] *= p.scale_log2;
+                        t4[c & 3] = fmaxf(t4[c & 3], s[c]);
+                    }
+                    top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                }
+                if (un.first()) {
+                    used = top;
+                } else if (__any_sync(0xffffffffu, top > used + 8.f)) {
+                    const float next = fmaxf(used, top);
+                    const float a = fast_exp2(used - (next == ninf ? 0.f : next));
+                    wait(&bars.pv_done, i - 1);
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int c = 0; c < DT; c += 32) {
+                        float o[32];
+                        tc::tmem_ld32(t_o + lanes + c, o);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] *= a;
+                        tmem_st32(t_o + lanes + c, reinterpret_cast<const uint32_t*>(o));
+                    }
+                    tmem_st_wait();
+                    l *= a;
+                    used = next;
+                }
+                const float use = used == ninf ? 0.f : used;
+                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < kTcKT; c += 2) {
+                    const float e0 = fast_exp2(s[c] - use), e1 = fast_exp2(s[c + 1] - use);
+                    l4[c & 2] += e0;
+                    l4[(c & 2) + 1] += e1;
+                    hi[c / 2] = pack_bf16(e0, e1);
+                    s[c / 2] = __uint_as_float(pack_bf16(e0 - bf16lo(hi[c / 2]), e1 - bf16hi(hi[c / 2])));
+                }
+                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+            }
+            if (i > 0) wait(&bars.pv_done, i - 1);           // the last product has read P
+            tc::fence_after_sync();
+            if (busy) {
+                tmem_st32(t_p + lanes, hi);
+                tmem_st32(t_p + lanes + 32, hi + 32);
+                tmem_st32(t_p + lanes + 64, reinterpret_cast<const uint32_t*>(s));
+                tmem_st32(t_p + lanes + 96, reinterpret_cast<const uint32_t*>(s) + 32);
+                tmem_st_wait();
+            }
+            tc::fence_before_sync();
+            mbar_arrive(&bars.p_full);
+
+            if (!un.last()) continue;
+            // ---- the piece is done: its rows out of TMEM
+            wait(&bars.pv_done, i);
+            tc::fence_after_sync();
+            const bool whole = pc.whole(), mine = m < valid;
+            const int qi = pc.tile * kTcM + m, head = pc.h * p.G + qi % p.G;
+            const int64_t row = static_cast<int64_t>(pc.r.row0) + qi / p.G;
+            const int64_t at = part_place(blockIdx.x, pc.u0 == 0) * kTcM + m;
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            if (busy) {
+#pragma unroll 1
+                for (int c = 0; c < DT; c += 32) {
+                    float o[32];
+                    tc::tmem_ld32(t_o + lanes + c, o);
+                    tc::tmem_ld_wait();
+                    if (!mine) continue;
+                    if (whole) {
+                        __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + (row * p.Hq + head) * p.D + c;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) {
+                            if (c + k >= p.D) break;
+                            uint4 x = make_uint4(0, 0, 0, 0);
+                            if (l != 0.f)
+                                x = make_uint4(pack_bf16(o[k] * inv, o[k + 1] * inv), pack_bf16(o[k + 2] * inv, o[k + 3] * inv),
+                                               pack_bf16(o[k + 4] * inv, o[k + 5] * inv), pack_bf16(o[k + 6] * inv, o[k + 7] * inv));
+                            *reinterpret_cast<uint4*>(to + k) = x;
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            if (c + k >= p.D) break;
+                            *reinterpret_cast<float4*>(p.part_o + at * p.D + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                        }
+                    }
+                }
+                if (mine) {
+                    if (!whole) reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(used, l);
+                    else if (p.lse != nullptr) p.lse[row * p.Hq + head] = lse_of(used, l);
+                }
+            }
+            tc::fence_before_sync();
+            if (!whole && part_done(p, pc, st, &s_flag, m, [] { softmax_sync(); }))
+                join_parts<__nv_bfloat16, kTcM, kTcRows>(p, pc, st, m);
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (w == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Rows of a TMA box: the largest power of two that divides the page, so that a box lies on one
+// page and units (multiples of 128 keys) start on a box.
+inline int tc_box(int page) {
+    const int b = page & -page;
+    return b < 128 ? b : 128;
+}
+// Whether the caches can be read so: 64 columns to a box, 8 rows are the swizzle's period, and
+// rows are counted in 32 bits.
+inline bool tc_fits(const Args& p) {
+    return p.D >= 64 && p.D <= 128 && tc_box(p.page) >= 8 && static_cast<int64_t>(p.num_blocks) * p.Hkv * p.page <= 0x7fffffffll;
+}
+inline bool encode_cache(CUtensorMap* map, const void* cache, const Args& p, int box) {
+    auto enc = eng::tensor_map_encoder();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.D), static_cast<cuuint64_t>(p.num_blocks) * p.Hkv * p.page};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.D) * 2};
+    const cuuint32_t size[2] = {64, static_cast<cuuint32_t>(box)};
+    const cuuint32_t step[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(cache), dims, strides, size, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DT>
+dspark_status_t launch_tc(const Args& p, cudaStream_t s) {
+    static OncePerDevice once;
+    const int dev = current_device();
+    if (once.run(dev, [] {
+            return cudaFuncSetAttribute(attend_tc<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<DT>::kSmem);
+        }) != cudaSuccess)
+        return DSPARK_ERR_CUDA;
+    CUtensorMap km, vm;
+    const int box = tc_box(p.page);
+    if (!encode_cache(&km, p.kc, p, box) || !encode_cache(&vm, p.vc, p, box)) return DSPARK_ERR_CUDA;
+    const int grid = grid_for(sm_count(dev), kTcM);
+    if (grid < 1) return DSPARK_ERR_CUDA;
+    attend_tc<DT><<<grid, kTcThreads, TcShape<DT>::kSmem, s>>>(p, km, vm, box);
+    return launch_status();
+}
+
+}  // namespace attn
+}  // namespace dspark
