@@ -28,7 +28,7 @@ __device__ __forceinline__ float4 load4<__nv_fp8_e4m3>(const void* base, int64_t
 }
 
 template <typename C, int kCols>
-__global__ void __launch_bounds__(kSimtThreads) attend_simt(Args p) {
+__global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constant__ Args p) {
     constexpr int M = kSimtM, KT = kSimtKT;
     extern __shared__ float4 smem4[];
     const int ld = p.D + 4;
@@ -37,6 +37,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(Args p) {
     float* s_v = s_k + KT * ld;                        // [KT][ld]
     float* s_p = s_v + KT * ld;                        // [M][KT]: exp of the scores, -1 where masked
     __shared__ long long scratch[34];
+    __shared__ float2 s_row[M];
     __shared__ int s_flag;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const float ninf = -__uint_as_float(0x7f800000u);
@@ -131,7 +132,8 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(Args p) {
                 const int64_t row = static_cast<int64_t>(pc.r.row0) + qi / p.G;
 #pragma unroll
                 for (int c = 0; c < kCols; ++c)
-                    if (lane + 32 * c < p.D) store_out<float>(p, row, head, lane + 32 * c, l[r] != 0.f ? o[r][c] * vs / l[r] : 0.f);
+                    if (lane + 32 * c < p.D)
+                        static_cast<float*>(p.out)[(row * p.Hq + head) * p.D + lane + 32 * c] = l[r] != 0.f ? o[r][c] * vs / l[r] : 0.f;
                 if (lane == 0 && p.lse != nullptr) p.lse[row * p.Hq + head] = lse_of(mx[r], l[r]);
             }
         } else {
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(Args p) {
                     if (lane + 32 * c < p.D) p.part_o[at * p.D + lane + 32 * c] = o[r][c] * vs;
                 if (lane == 0) reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(mx[r], l[r]);
             }
-            if (part_done(p, pc, st, &s_flag, tid, [] { __syncthreads(); })) join_parts<float, M, kSimtThreads>(p, pc, st, tid);
+            if (part_done(p, pc, st, &s_flag, tid, [] { __syncthreads(); })) join_parts<float, M, kSimtThreads>(p, pc, st, s_row, tid, [] { __syncthreads(); });
         }
     }
 }

@@ -224,15 +224,11 @@ __device__ __forceinline__ int page_id(const Args& p, int b, int j) {
     return id;
 }
 
-template <typename T>
-__device__ __forceinline__ void store_out(const Args& p, int64_t row, int head, int d, float x);
-template <>
-__device__ __forceinline__ void store_out<float>(const Args& p, int64_t row, int head, int d, float x) {
-    static_cast<float*>(p.out)[(row * p.Hq + head) * p.D + d] = x;
-}
-template <>
-__device__ __forceinline__ void store_out<__nv_bfloat16>(const Args& p, int64_t row, int head, int d, float x) {
-    static_cast<__nv_bfloat16*>(p.out)[(row * p.Hq + head) * p.D + d] = __float2bfloat16_rn(x);
+// Four adjacent output elements, rounded once.
+__device__ __forceinline__ void store_four(float* to, float4 x) { *reinterpret_cast<float4*>(to) = x; }
+__device__ __forceinline__ void store_four(__nv_bfloat16* to, float4 x) {
+    __nv_bfloat162 two[2] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w)};
+    *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(two);
 }
 
 // ln of the sum from a maximum in units of log 2 and the sum at it.
@@ -254,31 +250,81 @@ __device__ __forceinline__ bool part_done(const Args& p, const Piece& pc, const 
     return join;
 }
 
-// Joins the parts of a segment, in the order of the keys, and writes its rows.
-template <typename T, int M, int kThreads>
-__device__ __forceinline__ void join_parts(const Args& p, const Piece& pc, const Start& st, int tid) {
+// Joins the parts of a segment, in the order of the keys, and writes its rows.  First a
+// row's maximum and sum over the parts (s_row, M entries), then its elements: a thread has
+// four pieces of four elements and loads them from four parts at a time, since one block
+// reads all of it and waits for nothing but L2.
+template <typename T, int M, int kThreads, class Sync>
+__device__ __noinline__ void join_parts(const Args& p, Piece pc, Start st, float2* s_row, int tid,
+                                           Sync sync) {
+    constexpr int kE = 4, kC = 4;
     const int c0 = block_of(pc.seg_first, st.total, st.grid);
     const int c1 = block_of(pc.seg_first + pc.units - 1, st.total, st.grid);
-    const int valid = static_cast<int>(min(static_cast<int64_t>(M), static_cast<int64_t>(pc.r.n) * p.G - static_cast<int64_t>(pc.tile) * M));
+    const int left = pc.r.n * p.G - pc.tile * M, valid = left < M ? left : M;
     const float ninf = -__uint_as_float(0x7f800000u);
-    for (int e = tid; e < valid * p.D; e += kThreads) {
-        const int m = e / p.D, d = e - m * p.D;
-        float mx = ninf, l = 0.f, o = 0.f;
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+    for (int m = tid; m < valid; m += kThreads) {
+        float mx = ninf, l = 0.f;
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(ml + part_place(c, c == c0) * M + m).x);
+        const float use = mx == ninf ? 0.f : mx;
+#pragma unroll 4
         for (int c = c0; c <= c1; ++c) {
-            const int64_t at = part_place(c, c == c0) * M + m;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at);
-            const float x = __ldcg(p.part_o + at * p.D + d);
-            const float nm = fmaxf(mx, ml.x);
-            const float use = nm == ninf ? 0.f : nm;
-            const float a = fast_exp2(mx - use), c2 = fast_exp2(ml.x - use);
-            l = l * a + ml.y * c2;
-            o = o * a + x * c2;
-            mx = nm;
+            const float2 x = __ldcg(ml + part_place(c, c == c0) * M + m);
+            l += x.y * fast_exp2(x.x - use);
         }
-        const int qi = pc.tile * M + m, row = qi / p.G, head = pc.h * p.G + qi % p.G;
-        store_out<T>(p, static_cast<int64_t>(pc.r.row0) + row, head, d, l != 0.f ? o / l : 0.f);
-        if (d == 0 && p.lse != nullptr)
-            p.lse[(static_cast<int64_t>(pc.r.row0) + row) * p.Hq + head] = lse_of(mx, l);
+        s_row[m] = make_float2(use, l);
+        if (p.lse != nullptr) {
+            const int qi = pc.tile * M + m;
+            p.lse[(static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.Hq + pc.h * p.G + qi % p.G] = lse_of(mx, l);
+        }
+    }
+    sync();
+    const int four = p.D / 4, total = valid * four;
+    for (int e0 = tid; e0 < total; e0 += kE * kThreads) {
+        float4 o[kE];
+#pragma unroll
+        for (int k = 0; k < kE; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = c0; c <= c1; c += kC) {
+            float4 x[kC][kE];
+            float f[kC][kE];
+#pragma unroll
+            for (int i = 0; i < kC; ++i)
+#pragma unroll
+                for (int k = 0; k < kE; ++k) {
+                    const int e = e0 + k * kThreads;
+                    x[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    f[i][k] = ninf;
+                    if (c + i <= c1 && e < total) {
+                        const int64_t at = part_place(c + i, c + i == c0) * M + e / four;
+                        f[i][k] = __ldcg(ml + at).x;
+                        x[i][k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * p.D) + e % four);
+                    }
+                }
+#pragma unroll
+            for (int k = 0; k < kE; ++k) {
+                const int e = e0 + k * kThreads;
+                const float use = e < total ? s_row[e / four].x : 0.f;
+#pragma unroll
+                for (int i = 0; i < kC; ++i) {
+                    const float a = fast_exp2(f[i][k] - use);
+                    o[k].x = fmaf(x[i][k].x, a, o[k].x);
+                    o[k].y = fmaf(x[i][k].y, a, o[k].y);
+                    o[k].z = fmaf(x[i][k].z, a, o[k].z);
+                    o[k].w = fmaf(x[i][k].w, a, o[k].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kE; ++k) {
+            const int e = e0 + k * kThreads;
+            if (e >= total) continue;
+            const int m = e / four, qi = pc.tile * M + m;
+            const float l = s_row[m].y, inv = l != 0.f ? 1.f / l : 0.f;
+            T* to = static_cast<T*>(p.out) + ((static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.Hq + pc.h * p.G + qi % p.G) * p.D;
+            store_four(to + (e % four) * 4, l != 0.f ? make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv)
+                                                     : make_float4(0.f, 0.f, 0.f, 0.f));
+        }
     }
 }
 

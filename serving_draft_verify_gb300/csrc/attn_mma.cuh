@@ -122,7 +122,7 @@ __device__ __forceinline__ uint32_t without_odd(uint32_t u) {
 }
 
 template <bool kFp8, int MT, int DT>
-__global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_mma(Args p) {
+__global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_mma(const __grid_constant__ Args p) {
     using Sh = MmaShape<kFp8, MT, DT>;
     constexpr int M = Sh::M, KS = Sh::KS, KT = Sh::KT, kRow = Sh::kRow, kStages = Sh::kStages;
     constexpr int kThreads = Sh::kThreads, kWarps = Sh::kWarps;
@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long scratch[34];
     __shared__ float s_m[kWarps][M], s_l[kWarps][M], s_qs[M];
+    __shared__ float2 s_row[M];
     __shared__ int s_flag;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
     const float ninf = -__uint_as_float(0x7f800000u);
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
                 if (d == 0) reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(big - kShift, sum);
             }
         }
-        if (!whole && part_done(p, pc, st, &s_flag, tid, [] { __syncthreads(); })) join_parts<__nv_bfloat16, M, kThreads>(p, pc, st, tid);
+        if (!whole && part_done(p, pc, st, &s_flag, tid, [] { __syncthreads(); })) join_parts<__nv_bfloat16, M, kThreads>(p, pc, st, s_row, tid, [] { __syncthreads(); });
         __syncthreads();
     }
 }

@@ -13,10 +13,13 @@
 //               O += P V with P from TMEM and V as it lies (its rows are the contraction:
 //               an MN-major operand);
 //   warps 2, 3  the next piece's queries into the other of two buffers;
-//   warps 4-7   a thread a query row: maximum, P = 2^(S - m) as two bf16 terms (high + low, so
-//               that 16 bits of P count) into TMEM, the sum, and the output at the end.
+//   warps 4-11  two threads a query row, each with half of a unit's keys: P = 2^(S - m) as two
+//               bf16 terms (high + low, so that 16 bits of P count) into TMEM, the sum, and half of
+//               the output's columns at the end.
 // The output in TMEM is rescaled only where a maximum has grown by more than 2^8 over the one
-// in use (the factor stays in P and the sum alike until then).
+// in use (the factor stays in P and the sum alike until then), so the two threads of a row
+// exchange their maxima in those units alone.  One thread a row left the softmax at 5500 cycles
+// a unit (one warp a scheduler, and its code too long for the instruction cache).
 //
 // TMEM (512 columns): S 2 x 128, P 64 high + 64 low, O up to 128.
 #pragma once
@@ -53,20 +56,29 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+// 32 consecutive TMEM columns of this warp's lanes from every k-th of v.
+template <int k>
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
         "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
         "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(__float_as_uint(v[0 * k])), "r"(__float_as_uint(v[1 * k])), "r"(__float_as_uint(v[2 * k])),
+        "r"(__float_as_uint(v[3 * k])), "r"(__float_as_uint(v[4 * k])), "r"(__float_as_uint(v[5 * k])),
+        "r"(__float_as_uint(v[6 * k])), "r"(__float_as_uint(v[7 * k])), "r"(__float_as_uint(v[8 * k])),
+        "r"(__float_as_uint(v[9 * k])), "r"(__float_as_uint(v[10 * k])), "r"(__float_as_uint(v[11 * k])),
+        "r"(__float_as_uint(v[12 * k])), "r"(__float_as_uint(v[13 * k])), "r"(__float_as_uint(v[14 * k])),
+        "r"(__float_as_uint(v[15 * k])), "r"(__float_as_uint(v[16 * k])), "r"(__float_as_uint(v[17 * k])),
+        "r"(__float_as_uint(v[18 * k])), "r"(__float_as_uint(v[19 * k])), "r"(__float_as_uint(v[20 * k])),
+        "r"(__float_as_uint(v[21 * k])), "r"(__float_as_uint(v[22 * k])), "r"(__float_as_uint(v[23 * k])),
+        "r"(__float_as_uint(v[24 * k])), "r"(__float_as_uint(v[25 * k])), "r"(__float_as_uint(v[26 * k])),
+        "r"(__float_as_uint(v[27 * k])), "r"(__float_as_uint(v[28 * k])), "r"(__float_as_uint(v[29 * k])),
+        "r"(__float_as_uint(v[30 * k])), "r"(__float_as_uint(v[31 * k]))
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-constexpr int kTcM = 128, kTcKT = 128, kTcThreads = 256, kTcRows = 128;   // kTcRows: threads of the softmax
+constexpr int kTcM = 128, kTcKT = 128, kTcThreads = 384, kTcSoft = 256;   // kTcSoft: threads of the softmax
 
 template <int DT>
 struct TcShape {
@@ -101,13 +113,13 @@ struct Units {
     }
 };
 
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool softmax_any(bool x) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "barrier.cta.red.or.pred q, 1, 256, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
         : "r"(x ? 1u : 0u)
@@ -117,7 +129,7 @@ __device__ __forceinline__ bool softmax_any(bool x) {
 
 template <int DT>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    attend_tc(Args p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int box) {
+    attend_tc(const __grid_constant__ Args p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int box) {
     using Sh = TcShape<DT>;
     extern __shared__ unsigned char raw[];
     unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -127,6 +139,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __shared__ long long scratch[34];
     __shared__ __align__(8) TcBars bars;
     __shared__ uint32_t s_tmem;
+    __shared__ float2 s_row[kTcM];
+    __shared__ float s_two[2][kTcM];                         // what the two threads of a row tell each other
     __shared__ int s_flag;
     __shared__ volatile int s_dead, s_keep;                  // s_keep: the piece's first product adds to what O holds
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -140,9 +154,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&bars.q_full[i], 64);
             mbar_init(&bars.q_empty[i], 1);
             mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.s_empty[i], kTcRows);
+            mbar_init(&bars.s_empty[i], kTcSoft);
         }
-        mbar_init(&bars.p_full, kTcRows);
+        mbar_init(&bars.p_full, kTcSoft);
         mbar_init(&bars.pv_done, 1);
         fence_mbar_init();
         s_dead = 0;
@@ -282,8 +296,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     } else {
         // --------------------------------------------------------------- softmax ---
-        const int m = tid - 128;                             // the thread's query row and TMEM lane
-        const uint32_t lanes = static_cast<uint32_t>(w - 4) << 21;   // (warp's first lane) << 16
+        const int m = (tid - 128) & 127, half = (tid - 128) >> 7;   // the query row (TMEM lane), the half of the keys
+        const uint32_t lanes = static_cast<uint32_t>(w & 3) << 21;  // (warp's first lane) << 16
+        constexpr int kCols = DT / 2, kKeys = kTcKT / 2;
+        const int d0 = half * kCols;                                // first of the thread's output columns
         const float ninf = -__uint_as_float(0x7f800000u);
         float used = ninf, l = 0.f;
         uint32_t i = 0;
@@ -291,44 +307,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const Piece& pc = un.pc;
             const int stage = i & 1, k0 = pc.span.lo + un.u * kTcKT;
             const int left = pc.r.n * p.G - pc.tile * kTcM, valid = left < kTcM ? left : kTcM;
-            const int pos = pc.r.len + (pc.tile * kTcM + m) / p.G;
+            const bool busy = (w & 3) * 32 < valid;                 // the warp has rows
             const int pos_lo = pc.r.len + pc.tile * kTcM / p.G, pos_hi = pc.span.hi - 1;
-            const bool busy = (w - 4) * 32 < valid;          // the warp has rows
             const bool masked = k0 + kTcKT - 1 > pos_lo || (p.window > 0 && k0 <= pos_hi - p.window);
+            int c_lo = 0, c_hi = kTcKT;                             // the columns of this unit that the row sees
             if (un.first()) {
                 used = ninf;
                 l = 0.f;
-                if (m == 0) s_keep = 0;
+                if (tid == 128) s_keep = 0;
             }
-            // the columns of this unit that the row sees: [c_lo, c_hi)
-            const int c_hi = min(pos, pos_hi) + 1 - k0, c_lo = p.window > 0 ? pos - p.window + 1 - k0 : 0;
             if (masked) {
+                const int pos = pc.r.len + (pc.tile * kTcM + m) / p.G;
+                c_hi = min(min(pos, pos_hi) + 1 - k0, kTcKT);
+                if (p.window > 0) c_lo = max(pos - p.window + 1 - k0, 0);
                 // Values at keys past the last one, and values that are not finite at keys that only
                 // some rows see, must not meet the product (0 times them is not 0).  The former become
                 // 0; the latter are added here to the rows that see them and become 0 too.
                 wait(&bars.v_full[stage], i >> 1);
                 unsigned char* v = s_v + stage * Sh::kTile;
                 bool odd = false;
-                const int key = k0 + m;
-                if (key >= pc.span.hi) {
-                    for (int h = 0; h < Sh::kHalves; ++h)
+                if (half < Sh::kHalves) {
+                    uint4* x = reinterpret_cast<uint4*>(v + half * Sh::kHalf + m * 128);
+                    if (k0 + m >= pc.span.hi) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) x[c] = make_uint4(0, 0, 0, 0);
+                    } else {
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
-                            *reinterpret_cast<uint4*>(v + h * Sh::kHalf + m * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-                } else {
-                    for (int h = 0; h < Sh::kHalves; ++h)
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(v + h * Sh::kHalf + m * 128 + c * 16);
-                            odd |= any_odd<false>(x.x) || any_odd<false>(x.y) || any_odd<false>(x.z) || any_odd<false>(x.w);
-                        }
+                            odd |= any_odd<false>(x[c].x) || any_odd<false>(x[c].y) || any_odd<false>(x[c].z) || any_odd<false>(x[c].w);
+                    }
                 }
                 const bool some = softmax_any(odd);
-                if (un.first() && m == 0 && some) s_keep = 1;
+                if (un.first() && tid == 128 && some) s_keep = 1;
                 if (some) {
                     if (i > 0) wait(&bars.pv_done, i - 1);
                     tc::fence_after_sync();
-                    for (int c = 0; c < DT; c += 32) {
+#pragma unroll 1
+                    for (int c = d0; c < d0 + kCols; c += 32) {
                         float o[32];
                         if (un.first()) {
 #pragma unroll
@@ -337,7 +352,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             tc::tmem_ld32(t_o + lanes + c, o);
                             tc::tmem_ld_wait();
                         }
-                        for (int j = max(c_lo, 0); j < min(c_hi, kTcKT); ++j) {
+#pragma unroll 1
+                        for (int j = c_lo; j < c_hi; ++j) {
                             const unsigned char* at = v + (c >> 6) * Sh::kHalf + j * 128;
 #pragma unroll
                             for (int k = 0; k < 32; ++k) {
@@ -347,13 +363,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                         }
                         __syncwarp();
-                        tmem_st32(t_o + lanes + c, reinterpret_cast<const uint32_t*>(o));
+                        tmem_st32<1>(t_o + lanes + c, o);
                     }
                     tmem_st_wait();
                     softmax_sync();
-                    for (int h = 0; h < Sh::kHalves; ++h)
+                    if (half < Sh::kHalves)
                         for (int c = 0; c < 32; ++c) {
-                            uint32_t* x = reinterpret_cast<uint32_t*>(v + h * Sh::kHalf + m * 128) + c;
+                            uint32_t* x = reinterpret_cast<uint32_t*>(v + half * Sh::kHalf + m * 128) + c;
                             *x = without_odd<false>(*x);
                         }
                 }
@@ -361,71 +377,72 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             wait(&bars.s_full[stage], i >> 1);
             tc::fence_after_sync();
-            float s[kTcKT];
+            float s[kKeys];
+            float top = ninf;
             if (busy) {
-#pragma unroll
-                for (int c = 0; c < kTcKT; c += 32) tc::tmem_ld32(tmem + stage * 128 + lanes + c, s + c);
+                tc::tmem_ld32(tmem + stage * 128 + lanes + half * kKeys, s);
+                tc::tmem_ld32(tmem + stage * 128 + lanes + half * kKeys + 32, s + 32);
                 tc::tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < kKeys; ++c) s[c] *= p.scale_log2;
+                if (masked) {
+                    c_lo -= half * kKeys;
+                    c_hi -= half * kKeys;
+#pragma unroll
+                    for (int c = 0; c < kKeys; ++c)
+                        if (c < c_lo || c >= c_hi) s[c] = ninf;
+                }
+                float t4[4] = {ninf, ninf, ninf, ninf};
+#pragma unroll
+                for (int c = 0; c < kKeys; ++c) t4[c & 3] = fmaxf(t4[c & 3], s[c]);
+                top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
             }
             tc::fence_before_sync();
             mbar_arrive(&bars.s_empty[stage]);
-            uint32_t hi[kTcKT / 2];
-            if (busy) {
-                float top = ninf;
-                if (masked) {
-#pragma unroll
-                    for (int c = 0; c < kTcKT; ++c) {
-                        s[c] = c >= c_lo && c < c_hi ? s[c] * p.scale_log2 : ninf;
-                        top = fmaxf(top, s[c]);
-                    }
-                } else {
-                    float t4[4] = {ninf, ninf, ninf, ninf};
-#pragma unroll
-                    for (int c = 0; c < kTcKT; ++c) {
-                        s[c] *= p.scale_log2;
-                        t4[c & 3] = fmaxf(t4[c & 3], s[c]);
-                    }
-                    top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-                }
-                if (un.first()) {
-                    used = top;
-                } else if (__any_sync(0xffffffffu, top > used + 8.f)) {
-                    const float next = fmaxf(used, top);
+            if (softmax_any(un.first() || top > used + 8.f)) {
+                s_two[half][m] = top;
+                softmax_sync();
+                const float next = fmaxf(used, fmaxf(s_two[0][m], s_two[1][m]));
+                if (!un.first()) {
                     const float a = fast_exp2(used - (next == ninf ? 0.f : next));
                     wait(&bars.pv_done, i - 1);
                     tc::fence_after_sync();
+                    if (busy) {
 #pragma unroll 1
-                    for (int c = 0; c < DT; c += 32) {
-                        float o[32];
-                        tc::tmem_ld32(t_o + lanes + c, o);
-                        tc::tmem_ld_wait();
+                        for (int c = d0; c < d0 + kCols; c += 32) {
+                            float o[32];
+                            tc::tmem_ld32(t_o + lanes + c, o);
+                            tc::tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] *= a;
-                        tmem_st32(t_o + lanes + c, reinterpret_cast<const uint32_t*>(o));
+                            for (int k = 0; k < 32; ++k) o[k] *= a;
+                            tmem_st32<1>(t_o + lanes + c, o);
+                        }
+                        tmem_st_wait();
                     }
-                    tmem_st_wait();
                     l *= a;
-                    used = next;
                 }
+                used = next;
+            }
+            if (busy) {
                 const float use = used == ninf ? 0.f : used;
                 float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int c = 0; c < kTcKT; c += 2) {
+                for (int c = 0; c < kKeys; c += 2) {
                     const float e0 = fast_exp2(s[c] - use), e1 = fast_exp2(s[c + 1] - use);
                     l4[c & 2] += e0;
                     l4[(c & 2) + 1] += e1;
-                    hi[c / 2] = pack_bf16(e0, e1);
-                    s[c / 2] = __uint_as_float(pack_bf16(e0 - bf16lo(hi[c / 2]), e1 - bf16hi(hi[c / 2])));
+                    // the two terms of both take the scores' places: high, then low
+                    const uint32_t hi = pack_bf16(e0, e1);
+                    s[c] = __uint_as_float(hi);
+                    s[c + 1] = __uint_as_float(pack_bf16(e0 - bf16lo(hi), e1 - bf16hi(hi)));
                 }
                 l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
             }
-            if (i > 0) wait(&bars.pv_done, i - 1);           // the last product has read P
+            if (i > 0) wait(&bars.pv_done, i - 1);                  // the last product has read P
             tc::fence_after_sync();
             if (busy) {
-                tmem_st32(t_p + lanes, hi);
-                tmem_st32(t_p + lanes + 32, hi + 32);
-                tmem_st32(t_p + lanes + 64, reinterpret_cast<const uint32_t*>(s));
-                tmem_st32(t_p + lanes + 96, reinterpret_cast<const uint32_t*>(s) + 32);
+                tmem_st32<2>(t_p + lanes + half * 32, s);
+                tmem_st32<2>(t_p + lanes + 64 + half * 32, s + 1);
                 tmem_st_wait();
             }
             tc::fence_before_sync();
@@ -433,8 +450,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
             if (!un.last()) continue;
             // ---- the piece is done: its rows out of TMEM
+            s_two[half][m] = l;
             wait(&bars.pv_done, i);
             tc::fence_after_sync();
+            softmax_sync();
+            l = s_two[0][m] + s_two[1][m];
             const bool whole = pc.whole(), mine = m < valid;
             const int qi = pc.tile * kTcM + m, head = pc.h * p.G + qi % p.G;
             const int64_t row = static_cast<int64_t>(pc.r.row0) + qi / p.G;
@@ -442,12 +462,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const float inv = l != 0.f ? 1.f / l : 0.f;
             if (busy) {
 #pragma unroll 1
-                for (int c = 0; c < DT; c += 32) {
+                for (int c = d0; c < d0 + kCols; c += 32) {
                     float o[32];
                     tc::tmem_ld32(t_o + lanes + c, o);
                     tc::tmem_ld_wait();
-                    if (!mine) continue;
-                    if (whole) {
+                    if (mine && whole) {
                         __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + (row * p.Hq + head) * p.D + c;
 #pragma unroll
                         for (int k = 0; k < 32; k += 8) {
@@ -458,22 +477,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                                pack_bf16(o[k + 4] * inv, o[k + 5] * inv), pack_bf16(o[k + 6] * inv, o[k + 7] * inv));
                             *reinterpret_cast<uint4*>(to + k) = x;
                         }
-                    } else {
+                    } else if (mine) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
                             if (c + k >= p.D) break;
                             *reinterpret_cast<float4*>(p.part_o + at * p.D + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
                         }
                     }
+                    __syncwarp();
                 }
-                if (mine) {
+                if (mine && half == 0) {
                     if (!whole) reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(used, l);
                     else if (p.lse != nullptr) p.lse[row * p.Hq + head] = lse_of(used, l);
                 }
             }
             tc::fence_before_sync();
-            if (!whole && part_done(p, pc, st, &s_flag, m, [] { softmax_sync(); }))
-                join_parts<__nv_bfloat16, kTcM, kTcRows>(p, pc, st, m);
+            if (!whole && part_done(p, pc, st, &s_flag, tid - 128, [] { softmax_sync(); }))
+                join_parts<__nv_bfloat16, kTcM, kTcSoft>(p, pc, st, s_row, tid - 128, [] { softmax_sync(); });
         }
     }
     tc::fence_before_sync();
