@@ -7,19 +7,20 @@
 // about as many of one warpgroup, next to 2800 cycles for the unit's 64 KB at the measured
 // bandwidth.  So one block an SM, with a warp for each thing that can run by itself:
 //
-//   warp 0      keys and values into two-stage rings by TMA (boxes of up to 128 rows that lie on one
-//               page, 128-byte swizzle), running ahead across pieces;
-//   warp 1      the products: S = Q K^T into one of two TMEM buffers, one unit ahead, and
-//               O += P V with P from TMEM and V as it lies (its rows are the contraction:
-//               an MN-major operand);
-//   warps 2, 3  the next piece's queries into the other of two buffers;
+//   warp 0      keys into a ring of two units by TMA (boxes of up to 128 rows that lie on one page,
+//               128-byte swizzle), running ahead across pieces;
+//   warp 1      S = Q K^T into one of two TMEM buffers, a unit ahead;
+//   warp 2      O += P V with P from TMEM and V as it lies (its rows are the contraction: an
+//               MN-major operand);
+//   warp 3      values like the keys, and before a piece's its queries, into the other of two buffers;
 //   warps 4-11  two threads a query row, each with half of a unit's keys: P = 2^(S - m) as two
 //               bf16 terms (high + low, so that 16 bits of P count) into TMEM, the sum, and half of
 //               the output's columns at the end.
 // The output in TMEM is rescaled only where a maximum has grown by more than 2^8 over the one
 // in use (the factor stays in P and the sum alike until then), so the two threads of a row
-// exchange their maxima in those units alone.  One thread a row left the softmax at 5500 cycles
-// a unit (one warp a scheduler, and its code too long for the instruction cache).
+// exchange their maxima in those units alone.  The instruction cache is a bound here: with six
+// roles in one kernel, what runs once a piece or never (the walk, the joining, waits that have to
+// wait) stands in functions of its own.
 //
 // TMEM (512 columns): S 2 x 128, P 64 high + 64 low, O up to 128.
 #pragma once
@@ -91,27 +92,16 @@ struct TcBars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], q_empty[2], s_full[2], s_empty[2], p_full, pv_done;
 };
 
-// The units of a block one by one, over its pieces.
-struct Units {
-    Walk<kTcM, kTcKT> walk;
-    Piece pc;
-    int u, piece;
-    bool ok;
-    __device__ __forceinline__ Units(const Args& p, const Start& st) : walk(p, st), u(0), piece(0) {
-        ok = walk.next(pc);
-        if (ok) u = pc.u0;
+__device__ __noinline__ bool next_piece(Walk<kTcM, kTcKT>& walk, Piece& pc) { return walk.next(pc); }
+// A wait that runs out ends all waiting: every role goes on through its units without issuing
+// anything, so that the block ends, and the status tells.
+__device__ __noinline__ void long_wait(uint64_t* bar, uint32_t parity, volatile int* dead, StatusBlock* status) {
+    if (*dead) return;
+    if (!mbar_wait(bar, parity)) {
+        *dead = 1;
+        set_status(status, DSPARK_ERR_TIMEOUT, 1);
     }
-    __device__ __forceinline__ bool first() const { return u == pc.u0; }
-    __device__ __forceinline__ bool last() const { return u + 1 == pc.u1; }
-    __device__ __forceinline__ void next() {
-        if (++u < pc.u1) return;
-        ok = walk.next(pc);
-        if (ok) {
-            u = pc.u0;
-            ++piece;
-        }
-    }
-};
+}
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool softmax_any(bool x) {
@@ -151,7 +141,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&bars.k_empty[i], 1);
             mbar_init(&bars.v_full[i], 1);
             mbar_init(&bars.v_empty[i], 1);
-            mbar_init(&bars.q_full[i], 64);
+            mbar_init(&bars.q_full[i], 32);
             mbar_init(&bars.q_empty[i], 1);
             mbar_init(&bars.s_full[i], 1);
             mbar_init(&bars.s_empty[i], kTcSoft);
@@ -169,67 +159,85 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc::fence_after_sync();
     const uint32_t tmem = s_tmem, t_p = tmem + 256, t_o = tmem + 384;
 
-    // A wait that runs out ends all waiting: every role goes on through its units without
-    // issuing anything, so that the block ends, and the status tells.
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (s_dead) return;
-        if (!mbar_wait(bar, parity & 1)) {
-            s_dead = 1;
-            set_status(p.status, DSPARK_ERR_TIMEOUT, 1);
-        }
+        if (!mbar_try_wait(bar, parity & 1)) long_wait(bar, parity & 1, &s_dead, p.status);
     };
+    Walk<kTcM, kTcKT> walk(p, st);
+    Piece pc;
+    uint32_t i = 0;                                          // units done
 
-    if (w == 0) {
-        // ------------------------------------------------------- keys and values ---
+    if (w == 0 || w == 3) {
+        // -------------------------------- keys; queries (a piece at a time) and values ---
+        const bool keys = w == 0;
+        const CUtensorMap* map = keys ? &kmap : &vmap;
+        uint64_t *full = keys ? bars.k_full : bars.v_full, *empty = keys ? bars.k_empty : bars.v_empty;
+        unsigned char* ring = keys ? s_k : s_v;
         const uint64_t policy = policy_evict_normal();
-        uint32_t i = 0;
-        for (Units un(p, st); un.ok; un.next(), ++i) {
-            const int stage = i & 1, k0 = un.pc.span.lo + un.u * kTcKT;
-            const int keys = min(kTcKT, un.pc.span.hi - k0), boxes = (keys + box - 1) / box;
-            const uint32_t bytes = boxes * box * 128 * Sh::kHalves;
-            // lane l has box l: its row in both tiles
-            int y = 0;
-            if (lane < boxes) {
-                const int key = k0 + lane * box, blk = key / p.page;
-                y = (page_id(p, un.pc.b, blk) * p.Hkv + un.pc.h) * p.page + (key - blk * p.page);
-            }
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                uint64_t* full = kv ? &bars.v_full[stage] : &bars.k_full[stage];
-                if (lane == 0) {
-                    wait(kv ? &bars.v_empty[stage] : &bars.k_empty[stage], (i >> 1) + 1);
-                    if (!s_dead) mbar_arrive_expect_tx(full, bytes);
+        for (uint32_t n = 0; next_piece(walk, pc); ++n) {
+            if (!keys) {
+                wait(&bars.q_empty[n & 1], (n >> 1) + 1);
+                const int left = pc.r.n * p.G - pc.tile * kTcM, valid = left < kTcM ? left : kTcM;
+                const uint32_t to = smem_u32(s_q) + (n & 1) * Sh::kTile;
+                const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
+#pragma unroll 2
+                for (int e = lane; e < kTcM * (DT / 8); e += 32) {
+                    const int m = e / (DT / 8), c = e % (DT / 8), qi = pc.tile * kTcM + m;
+                    const bool real = m < valid && c * 8 < p.D;
+                    const int64_t at = real ? (static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.q_stride +
+                                                  static_cast<int64_t>(pc.h * p.G + qi % p.G) * p.D + c * 8
+                                            : 0;
+                    copy16(to + (c >> 3) * Sh::kHalf + m * 128 + (((c & 7) ^ (m & 7)) << 4), q + at, real);
                 }
-                __syncwarp();
-                if (s_dead) continue;
-                unsigned char* to = (kv ? s_v : s_k) + stage * Sh::kTile;
-                if (lane < boxes)
-                    for (int h = 0; h < Sh::kHalves; ++h)
-                        tc::tma_load_2d(to + h * Sh::kHalf + lane * box * 128, kv ? &vmap : &kmap, 64 * h, y, full, policy);
+                cp_async_wait_all();
+                fence_proxy_async_smem();
+                mbar_arrive(&bars.q_full[n & 1]);
+            }
+            const int hi = pc.span.hi, b = pc.b, h = pc.h;
+            int k0 = pc.span.lo + pc.u0 * kTcKT;
+#pragma unroll 1
+            for (int u = pc.u0; u < pc.u1; ++u, ++i, k0 += kTcKT) {
+                const int stage = i & 1, boxes = (min(kTcKT, hi - k0) + box - 1) / box;
+                // lane l finds the row of box l; lane 0 issues them all (an instruction that several
+                // lanes issue goes lane by lane, at several times the cost)
+                int y = 0;
+                if (lane < boxes) {
+                    const int key = k0 + lane * box, blk = key / p.page;
+                    y = (page_id(p, b, blk) * p.Hkv + h) * p.page + (key - blk * p.page);
+                }
+                if (lane == 0) {
+                    wait(&empty[stage], (i >> 1) + 1);
+                    if (!s_dead) mbar_arrive_expect_tx(&full[stage], boxes * box * 128 * Sh::kHalves);
+                }
+                unsigned char* to = ring + stage * Sh::kTile;
+#pragma unroll 1
+                for (int j = 0; j < boxes; ++j, to += box * 128) {
+                    const int yj = __shfl_sync(0xffffffffu, y, j);
+                    if (lane == 0 && !s_dead)
+#pragma unroll
+                        for (int c = 0; c < Sh::kHalves; ++c)
+                            tc::tma_load_2d(to + c * Sh::kHalf, map, 64 * c, yj, &full[stage], policy);
+                }
             }
         }
-        if (s_dead && lane == 0) {
-            // copies still in flight end before the block does
-            for (uint32_t j = i > 2 ? i - 2 : 0; j < i; ++j) {
-                mbar_wait(&bars.k_full[j & 1], (j >> 1) & 1);
-                mbar_wait(&bars.v_full[j & 1], (j >> 1) & 1);
-            }
-        }
+        // where a wait ran out, copies still in flight end before the block does
+        if (s_dead && lane == 0)
+            for (uint32_t j = i > 2 ? i - 2 : 0; j < i; ++j) mbar_wait(&full[j & 1], (j >> 1) & 1);
         __syncwarp();
     } else if (w == 1) {
-        // -------------------------------------------------------------- products ---
+        // ---------------------------------------------------------------- scores ---
         if (lane == 0) {
-            const uint32_t id_s = tc::idesc_bf16_f32(kTcM, kTcKT);
-            const uint32_t id_o = tc::idesc_bf16_f32(kTcM, DT) | (1u << 16);      // B is MN-major
-            uint32_t iq = 0;
-            auto scores = [&](const Units& un) {
-                const int stage = iq & 1, qb = un.piece & 1;
-                if (un.first()) wait(&bars.q_full[qb], un.piece >> 1);
-                wait(&bars.s_empty[stage], (iq >> 1) + 1);
-                wait(&bars.k_full[stage], iq >> 1);
-                tc::fence_after_sync();
-                if (!s_dead) {
-                    const uint32_t qa = smem_u32(s_q) + qb * Sh::kTile, ka = smem_u32(s_k) + stage * Sh::kTile;
+            constexpr uint32_t id_s = tc::idesc_bf16_f32(kTcM, kTcKT);
+            for (uint32_t n = 0; next_piece(walk, pc); ++n) {
+                const uint32_t qa = smem_u32(s_q) + (n & 1) * Sh::kTile;
+                wait(&bars.q_full[n & 1], n >> 1);
+#pragma unroll 1
+                for (int u = pc.u1 - pc.u0; u > 0; --u, ++i) {
+                    const int stage = i & 1;
+                    const uint32_t ka = smem_u32(s_k) + stage * Sh::kTile;
+                    wait(&bars.s_empty[stage], (i >> 1) + 1);
+                    wait(&bars.k_full[stage], i >> 1);
+                    tc::fence_after_sync();
+                    if (s_dead) continue;
 #pragma unroll
                     for (int ks = 0; ks < DT / 16; ++ks) {
                         const uint32_t off = (ks >> 2) * Sh::kHalf + (ks & 3) * 32;
@@ -237,63 +245,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     tc::commit(&bars.s_full[stage]);
                     tc::commit(&bars.k_empty[stage]);
-                    if (un.last()) tc::commit(&bars.q_empty[qb]);
+                    if (u == 1) tc::commit(&bars.q_empty[n & 1]);
                 }
-                ++iq;
-            };
-            Units ahead(p, st);
-            if (ahead.ok) {
-                scores(ahead);
-                ahead.next();
             }
-            uint32_t i = 0;
-            for (Units un(p, st); un.ok; un.next(), ++i) {
-                if (ahead.ok) {
-                    scores(ahead);
-                    ahead.next();
-                }
-                const int stage = i & 1;
-                wait(&bars.v_full[stage], i >> 1);
-                wait(&bars.p_full, i);
-                tc::fence_after_sync();
-                if (!s_dead) {
-                    const uint32_t va = smem_u32(s_v) + stage * Sh::kTile;
-                    const bool keep = !un.first() || s_keep;
+        }
+        __syncwarp();
+    } else if (w == 2) {
+        // ---------------------------------------------------------------- output ---
+        if (lane == 0) {
+            constexpr uint32_t id_o = tc::idesc_bf16_f32(kTcM, DT) | (1u << 16);      // B is MN-major
+            while (next_piece(walk, pc)) {
+                const int n = pc.u1 - pc.u0;
+#pragma unroll 1
+                for (int u = 0; u < n; ++u, ++i) {
+                    const int stage = i & 1;
+                    const uint64_t vd = desc_mn_sw128(smem_u32(s_v) + stage * Sh::kTile, Sh::kHalf);
+                    wait(&bars.v_full[stage], i >> 1);
+                    wait(&bars.p_full, i);
+                    tc::fence_after_sync();
+                    if (s_dead) continue;
+                    const bool keep = u > 0 || s_keep;
+                    // 16 keys a step: 2048 bytes on in V, 8 columns on in P (the high terms, then the low)
 #pragma unroll
-                    for (int ks = 0; ks < kTcKT / 16; ++ks)
-                        mma_bf16_ts(t_o, t_p + ks * 8, desc_mn_sw128(va + ks * 2048, Sh::kHalf), id_o, keep || ks > 0);
-#pragma unroll
-                    for (int ks = 0; ks < kTcKT / 16; ++ks)
-                        mma_bf16_ts(t_o, t_p + 64 + ks * 8, desc_mn_sw128(va + ks * 2048, Sh::kHalf), id_o, 1);
+                    for (int ks = 0; ks < kTcKT / 8; ++ks)
+                        mma_bf16_ts(t_o, t_p + ks * 8, vd + (ks & 7) * (2048 >> 4), id_o, keep || ks > 0);
                     tc::commit(&bars.pv_done);
                     tc::commit(&bars.v_empty[stage]);
                 }
             }
         }
         __syncwarp();
-    } else if (w < 4) {
-        // --------------------------------------------------------------- queries ---
-        Walk<kTcM, kTcKT> walk(p, st);
-        Piece pc;
-        for (int n = 0; walk.next(pc); ++n) {
-            wait(&bars.q_empty[n & 1], (n >> 1) + 1);
-            const int left = pc.r.n * p.G - pc.tile * kTcM, valid = left < kTcM ? left : kTcM;
-            unsigned char* to = s_q + (n & 1) * Sh::kTile;
-#pragma unroll 4
-            for (int e = tid - 64; e < kTcM * (DT / 8); e += 64) {
-                const int m = e / (DT / 8), c = e % (DT / 8);
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (m < valid && c * 8 < p.D) {
-                    const int qi = pc.tile * kTcM + m;
-                    x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                             (static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.q_stride +
-                                                             static_cast<int64_t>(pc.h * p.G + qi % p.G) * p.D + c * 8));
-                }
-                *reinterpret_cast<uint4*>(to + (c >> 3) * Sh::kHalf + m * 128 + (((c & 7) ^ (m & 7)) << 4)) = x;
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(&bars.q_full[n & 1]);
-        }
     } else {
         // --------------------------------------------------------------- softmax ---
         const int m = (tid - 128) & 127, half = (tid - 128) >> 7;   // the query row (TMEM lane), the half of the keys
@@ -301,157 +282,153 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         constexpr int kCols = DT / 2, kKeys = kTcKT / 2;
         const int d0 = half * kCols;                                // first of the thread's output columns
         const float ninf = -__uint_as_float(0x7f800000u);
-        float used = ninf, l = 0.f;
-        uint32_t i = 0;
-        for (Units un(p, st); un.ok; un.next(), ++i) {
-            const Piece& pc = un.pc;
-            const int stage = i & 1, k0 = pc.span.lo + un.u * kTcKT;
+        while (next_piece(walk, pc)) {
+            float used = ninf, l = 0.f;
             const int left = pc.r.n * p.G - pc.tile * kTcM, valid = left < kTcM ? left : kTcM;
-            const bool busy = (w & 3) * 32 < valid;                 // the warp has rows
+            const bool busy = (w & 3) * 32 < valid;                     // the warp has rows
+            const int pos = pc.r.len + (pc.tile * kTcM + m) / p.G;      // the row's position, the tile's first and last
             const int pos_lo = pc.r.len + pc.tile * kTcM / p.G, pos_hi = pc.span.hi - 1;
-            const bool masked = k0 + kTcKT - 1 > pos_lo || (p.window > 0 && k0 <= pos_hi - p.window);
-            int c_lo = 0, c_hi = kTcKT;                             // the columns of this unit that the row sees
-            if (un.first()) {
-                used = ninf;
-                l = 0.f;
-                if (tid == 128) s_keep = 0;
-            }
-            if (masked) {
-                const int pos = pc.r.len + (pc.tile * kTcM + m) / p.G;
-                c_hi = min(min(pos, pos_hi) + 1 - k0, kTcKT);
-                if (p.window > 0) c_lo = max(pos - p.window + 1 - k0, 0);
-                // Values at keys past the last one, and values that are not finite at keys that only
-                // some rows see, must not meet the product (0 times them is not 0).  The former become
-                // 0; the latter are added here to the rows that see them and become 0 too.
-                wait(&bars.v_full[stage], i >> 1);
-                unsigned char* v = s_v + stage * Sh::kTile;
-                bool odd = false;
-                if (half < Sh::kHalves) {
-                    uint4* x = reinterpret_cast<uint4*>(v + half * Sh::kHalf + m * 128);
-                    if (k0 + m >= pc.span.hi) {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) x[c] = make_uint4(0, 0, 0, 0);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            odd |= any_odd<false>(x[c].x) || any_odd<false>(x[c].y) || any_odd<false>(x[c].z) || any_odd<false>(x[c].w);
-                    }
-                }
-                const bool some = softmax_any(odd);
-                if (un.first() && tid == 128 && some) s_keep = 1;
-                if (some) {
-                    if (i > 0) wait(&bars.pv_done, i - 1);
-                    tc::fence_after_sync();
+            const int n = pc.u1 - pc.u0;
+            int k0 = pc.span.lo + pc.u0 * kTcKT;
+            if (tid == 128) s_keep = 0;
 #pragma unroll 1
-                    for (int c = d0; c < d0 + kCols; c += 32) {
-                        float o[32];
-                        if (un.first()) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = 0.f;
-                        } else {
-                            tc::tmem_ld32(t_o + lanes + c, o);
-                            tc::tmem_ld_wait();
-                        }
-#pragma unroll 1
-                        for (int j = c_lo; j < c_hi; ++j) {
-                            const unsigned char* at = v + (c >> 6) * Sh::kHalf + j * 128;
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                const int d = (c & 63) + k;
-                                const uint32_t bits = *reinterpret_cast<const uint16_t*>(at + (((d >> 3) ^ (j & 7)) << 4) + (d & 7) * 2);
-                                if (any_odd<false>(bits)) o[k] += bf16lo(bits);
-                            }
-                        }
-                        __syncwarp();
-                        tmem_st32<1>(t_o + lanes + c, o);
-                    }
-                    tmem_st_wait();
-                    softmax_sync();
-                    if (half < Sh::kHalves)
-                        for (int c = 0; c < 32; ++c) {
-                            uint32_t* x = reinterpret_cast<uint32_t*>(v + half * Sh::kHalf + m * 128) + c;
-                            *x = without_odd<false>(*x);
-                        }
-                }
-                fence_proxy_async_smem();
-            }
-            wait(&bars.s_full[stage], i >> 1);
-            tc::fence_after_sync();
-            float s[kKeys];
-            float top = ninf;
-            if (busy) {
-                tc::tmem_ld32(tmem + stage * 128 + lanes + half * kKeys, s);
-                tc::tmem_ld32(tmem + stage * 128 + lanes + half * kKeys + 32, s + 32);
-                tc::tmem_ld_wait();
-#pragma unroll
-                for (int c = 0; c < kKeys; ++c) s[c] *= p.scale_log2;
+            for (int u = 0; u < n; ++u, ++i, k0 += kTcKT) {
+                const int stage = i & 1;
+                const bool first = u == 0;
+                const bool masked = k0 + kTcKT - 1 > pos_lo || (p.window > 0 && k0 <= pos_hi - p.window);
+                int c_lo = 0, c_hi = kTcKT;                             // the columns of this unit that the row sees
                 if (masked) {
-                    c_lo -= half * kKeys;
-                    c_hi -= half * kKeys;
+                    c_hi = min(min(pos, pos_hi) + 1 - k0, kTcKT);
+                    if (p.window > 0) c_lo = max(pos - p.window + 1 - k0, 0);
+                    // Values at keys past the last one, and values that are not finite at keys that only
+                    // some rows see, must not meet the product (0 times them is not 0).  The former become
+                    // 0; the latter are added here to the rows that see them and become 0 too.
+                    wait(&bars.v_full[stage], i >> 1);
+                    unsigned char* v = s_v + stage * Sh::kTile;
+                    bool odd = false;
+                    if (half < Sh::kHalves) {
+                        uint4* x = reinterpret_cast<uint4*>(v + half * Sh::kHalf + m * 128);
+                        if (k0 + m > pos_hi) {
 #pragma unroll
-                    for (int c = 0; c < kKeys; ++c)
-                        if (c < c_lo || c >= c_hi) s[c] = ninf;
-                }
-                float t4[4] = {ninf, ninf, ninf, ninf};
+                            for (int c = 0; c < 8; ++c) x[c] = make_uint4(0, 0, 0, 0);
+                        } else {
 #pragma unroll
-                for (int c = 0; c < kKeys; ++c) t4[c & 3] = fmaxf(t4[c & 3], s[c]);
-                top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-            }
-            tc::fence_before_sync();
-            mbar_arrive(&bars.s_empty[stage]);
-            if (softmax_any(un.first() || top > used + 8.f)) {
-                s_two[half][m] = top;
-                softmax_sync();
-                const float next = fmaxf(used, fmaxf(s_two[0][m], s_two[1][m]));
-                if (!un.first()) {
-                    const float a = fast_exp2(used - (next == ninf ? 0.f : next));
-                    wait(&bars.pv_done, i - 1);
-                    tc::fence_after_sync();
-                    if (busy) {
+                            for (int c = 0; c < 8; ++c)
+                                odd |= any_odd<false>(x[c].x) || any_odd<false>(x[c].y) || any_odd<false>(x[c].z) || any_odd<false>(x[c].w);
+                        }
+                    }
+                    const bool some = softmax_any(odd);
+                    if (first && tid == 128 && some) s_keep = 1;
+                    if (some) {
+                        if (i > 0) wait(&bars.pv_done, i - 1);
+                        tc::fence_after_sync();
 #pragma unroll 1
                         for (int c = d0; c < d0 + kCols; c += 32) {
                             float o[32];
-                            tc::tmem_ld32(t_o + lanes + c, o);
-                            tc::tmem_ld_wait();
+                            if (first) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] *= a;
+                                for (int k = 0; k < 32; ++k) o[k] = 0.f;
+                            } else {
+                                tc::tmem_ld32(t_o + lanes + c, o);
+                                tc::tmem_ld_wait();
+                            }
+#pragma unroll 1
+                            for (int j = c_lo; j < c_hi; ++j) {
+                                const unsigned char* at = v + (c >> 6) * Sh::kHalf + j * 128;
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) {
+                                    const int d = (c & 63) + k;
+                                    const uint32_t bits = *reinterpret_cast<const uint16_t*>(at + (((d >> 3) ^ (j & 7)) << 4) + (d & 7) * 2);
+                                    if (any_odd<false>(bits)) o[k] += bf16lo(bits);
+                                }
+                            }
+                            __syncwarp();
                             tmem_st32<1>(t_o + lanes + c, o);
                         }
                         tmem_st_wait();
+                        softmax_sync();
+                        if (half < Sh::kHalves)
+                            for (int c = 0; c < 32; ++c) {
+                                uint32_t* x = reinterpret_cast<uint32_t*>(v + half * Sh::kHalf + m * 128) + c;
+                                *x = without_odd<false>(*x);
+                            }
                     }
-                    l *= a;
+                    fence_proxy_async_smem();
                 }
-                used = next;
-            }
-            if (busy) {
-                const float use = used == ninf ? 0.f : used;
-                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                wait(&bars.s_full[stage], i >> 1);
+                tc::fence_after_sync();
+                float s[kKeys];
+                float top = ninf;
+                if (busy) {
+                    tc::tmem_ld32(tmem + stage * 128 + lanes + half * kKeys, s);
+                    tc::tmem_ld32(tmem + stage * 128 + lanes + half * kKeys + 32, s + 32);
+                    tc::tmem_ld_wait();
+                    if (masked) {
+                        c_lo -= half * kKeys;
+                        c_hi -= half * kKeys;
 #pragma unroll
-                for (int c = 0; c < kKeys; c += 2) {
-                    const float e0 = fast_exp2(s[c] - use), e1 = fast_exp2(s[c + 1] - use);
-                    l4[c & 2] += e0;
-                    l4[(c & 2) + 1] += e1;
-                    // the two terms of both take the scores' places: high, then low
-                    const uint32_t hi = pack_bf16(e0, e1);
-                    s[c] = __uint_as_float(hi);
-                    s[c + 1] = __uint_as_float(pack_bf16(e0 - bf16lo(hi), e1 - bf16hi(hi)));
+                        for (int c = 0; c < kKeys; ++c)
+                            if (c < c_lo || c >= c_hi) s[c] = ninf;
+                    }
+                    float t4[4] = {ninf, ninf, ninf, ninf};
+#pragma unroll
+                    for (int c = 0; c < kKeys; ++c) t4[c & 3] = fmaxf(t4[c & 3], s[c]);
+                    top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * p.scale_log2;
                 }
-                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                tc::fence_before_sync();
+                mbar_arrive(&bars.s_empty[stage]);
+                if (softmax_any(first || top > used + 8.f)) {
+                    s_two[half][m] = top;
+                    softmax_sync();
+                    const float next = fmaxf(used, fmaxf(s_two[0][m], s_two[1][m]));
+                    if (!first) {
+                        const float a = fast_exp2(used - (next == ninf ? 0.f : next));
+                        wait(&bars.pv_done, i - 1);
+                        tc::fence_after_sync();
+                        if (busy) {
+#pragma unroll 1
+                            for (int c = d0; c < d0 + kCols; c += 32) {
+                                float o[32];
+                                tc::tmem_ld32(t_o + lanes + c, o);
+                                tc::tmem_ld_wait();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] *= a;
+                                tmem_st32<1>(t_o + lanes + c, o);
+                            }
+                            tmem_st_wait();
+                        }
+                        l *= a;
+                    }
+                    used = next;
+                }
+                if (busy) {
+                    const float use = used == ninf ? 0.f : used;
+                    float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < kKeys; c += 2) {
+                        const float e0 = fast_exp2(fmaf(s[c], p.scale_log2, -use)), e1 = fast_exp2(fmaf(s[c + 1], p.scale_log2, -use));
+                        l4[c & 2] += e0;
+                        l4[(c & 2) + 1] += e1;
+                        // the two terms of both take the scores' places: high, then low
+                        const uint32_t hi = pack_bf16(e0, e1);
+                        s[c] = __uint_as_float(hi);
+                        s[c + 1] = __uint_as_float(pack_bf16(e0 - bf16lo(hi), e1 - bf16hi(hi)));
+                    }
+                    l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                }
+                if (i > 0) wait(&bars.pv_done, i - 1);                  // the last product has read P
+                tc::fence_after_sync();
+                if (busy) {
+                    tmem_st32<2>(t_p + lanes + half * 32, s);
+                    tmem_st32<2>(t_p + lanes + 64 + half * 32, s + 1);
+                    tmem_st_wait();
+                }
+                tc::fence_before_sync();
+                mbar_arrive(&bars.p_full);
             }
-            if (i > 0) wait(&bars.pv_done, i - 1);                  // the last product has read P
-            tc::fence_after_sync();
-            if (busy) {
-                tmem_st32<2>(t_p + lanes + half * 32, s);
-                tmem_st32<2>(t_p + lanes + 64 + half * 32, s + 1);
-                tmem_st_wait();
-            }
-            tc::fence_before_sync();
-            mbar_arrive(&bars.p_full);
-
-            if (!un.last()) continue;
             // ---- the piece is done: its rows out of TMEM
             s_two[half][m] = l;
-            wait(&bars.pv_done, i);
+            wait(&bars.pv_done, i - 1);
             tc::fence_after_sync();
             softmax_sync();
             l = s_two[0][m] + s_two[1][m];
@@ -511,9 +488,9 @@ inline int tc_box(int page) {
     return b < 128 ? b : 128;
 }
 // Whether the caches can be read so: 64 columns to a box, 8 rows are the swizzle's period, and
-// rows are counted in 32 bits.
+// rows are counted in 32 bits.  The largest score is found before scaling: the scale is positive.
 inline bool tc_fits(const Args& p) {
-    return p.D >= 64 && p.D <= 128 && tc_box(p.page) >= 8 && static_cast<int64_t>(p.num_blocks) * p.Hkv * p.page <= 0x7fffffffll;
+    return p.scale_log2 > 0.f && p.D >= 64 && p.D <= 128 && tc_box(p.page) >= 8 && static_cast<int64_t>(p.num_blocks) * p.Hkv * p.page <= 0x7fffffffll;
 }
 inline bool encode_cache(CUtensorMap* map, const void* cache, const Args& p, int box) {
     auto enc = eng::tensor_map_encoder();
