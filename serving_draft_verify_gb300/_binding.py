@@ -565,6 +565,17 @@ def _on(t, dev, shape, dtype, name):
         raise ValueError(f"{name} is on another device")
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(dev, stream):
+    """Address of the stream: the given one, or the device's current one (without making an object
+    of it, which costs more than the rest of a small call)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
 def _opt(t, dev, shape, dtype, name):
     """As _on, for a tensor that may be absent; returns its address."""
     if t is None:
@@ -634,7 +645,7 @@ def dspark_plan_rows(length, rows, held, free_state, free_ring, block_table, pag
     _check("dspark_plan_rows",
            lib.dspark_plan_rows(B, page, width, nb, max_rows, length.data_ptr(), adv, rows.data_ptr(), held.data_ptr(),
                                 free_state.data_ptr(), free_ring.data_ptr(), block_table.data_ptr(), width,
-                                *[out[k].data_ptr() for k in _PLAN_OUT], ws.data_ptr(), _nbytes(ws), _stream(stream)))
+                                *[out[k].data_ptr() for k in _PLAN_OUT], ws.data_ptr(), _nbytes(ws), _stream_of(dev, stream)))
     return out
 
 
@@ -676,7 +687,7 @@ def dspark_write_kv(k, v, slot, k_cache, v_cache, k_scale=None, v_scale=None, wo
     _check("dspark_write_kv",
            lib.dspark_write_kv(n, Hkv, D, page, nb, dt, code, k.data_ptr(), ks, v.data_ptr(), vs, slot.data_ptr(), ksc,
                                vsc, k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(), _nbytes(ws),
-                               _stream(stream)))
+                               _stream_of(dev, stream)))
 
 
 def dspark_paged_attention(q, row_offset, length, block_table, k_cache, v_cache, max_rows, scale=None, window=0,
@@ -711,7 +722,7 @@ def dspark_paged_attention(q, row_offset, length, block_table, k_cache, v_cache,
                                       qs, row_offset.data_ptr(), length.data_ptr(), block_table.data_ptr(), width,
                                       k_cache.data_ptr(), v_cache.data_ptr(), ksc, vsc,
                                       D ** -0.5 if scale is None else float(scale), int(window),
-                                      out["out"].data_ptr(), lse, ws.data_ptr(), _nbytes(ws), _stream(stream)))
+                                      out["out"].data_ptr(), lse, ws.data_ptr(), _nbytes(ws), _stream_of(dev, stream)))
     return out
 
 
@@ -746,5 +757,5 @@ def dspark_adjust_logits(logits, history=None, prompt_len=None, history_len=None
                _opt(presence, dev, (B,), f32, "presence"), _opt(bias_token, dev, (B, n_bias), i32, "bias_token"),
                _opt(bias_value, dev, (B, n_bias), f32, "bias_value"), n_bias,
                _opt(mask_row, dev, (B, R), i32, "mask_row"), _opt(mask, dev, (n_mask, words), i32, "mask"), n_mask,
-               words, out.data_ptr(), ws.data_ptr(), _nbytes(ws), _stream(stream)))
+               words, out.data_ptr(), ws.data_ptr(), _nbytes(ws), _stream_of(dev, stream)))
     return out

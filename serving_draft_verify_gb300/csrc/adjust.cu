@@ -13,7 +13,8 @@
 // one request: it counts that piece's tokens of the history in shared memory once
 // and then streams the piece of every wanted row, adding one draft token between
 // rows.  One 32-bit word per token holds the count, the prompt bit and the index of
-// the token's bias; a word of zero means the token passes unchanged.
+// the token's bias; a flag for each 16 bytes of a row says whether any of its words is
+// not zero, so that a row's pass is a copy with the mask's bits but for the few that are.
 #include "common.cuh"
 #include "host_common.h"
 
@@ -41,12 +42,11 @@ struct AdjustArgs {
     StatusBlock* status;
 };
 
-// One step of the definition for a token that its word or its mask bit touches.
+// One step of the definition for a token that its word touches.
 struct Rules {
     float rho, f, p;
     const float* bias;
-    __device__ __forceinline__ float operator()(float x, uint32_t w, bool keep) const {
-        if (!keep) return -__uint_as_float(0x7f800000u);
+    __device__ __forceinline__ float operator()(float x, uint32_t w) const {
         const uint32_t n = w & kCountMask;
         if ((w & (kPrompt | kCountMask)) != 0) x = x > 0.f ? __fdiv_rn(x, rho) : x * rho;
         if (n != 0) {
@@ -72,6 +72,17 @@ struct Row<__nv_bfloat16> {
         uint32_t& w = i < 2 ? u.x : i < 4 ? u.y : i < 6 ? u.z : u.w;
         w = (i & 1) ? (w & 0xffffu) | (h << 16) : (w & 0xffff0000u) | h;
     }
+    // -inf in the place of each element whose bit of `keep` is 0
+    __device__ static uint32_t masked(uint32_t w, uint32_t keep) {
+        const uint32_t m = ((keep & 1u) ? 0xffffu : 0u) | ((keep & 2u) ? 0xffff0000u : 0u);
+        return (w & m) | (0xFF80FF80u & ~m);
+    }
+    __device__ static void mask(uint4& u, uint32_t keep) {
+        u.x = masked(u.x, keep);
+        u.y = masked(u.y, keep >> 2);
+        u.z = masked(u.z, keep >> 4);
+        u.w = masked(u.w, keep >> 6);
+    }
 };
 template <>
 struct Row<float> {
@@ -83,13 +94,21 @@ struct Row<float> {
         uint32_t& w = i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
         w = __float_as_uint(x);
     }
+    __device__ static void mask(uint4& u, uint32_t keep) {
+        u.x = (keep & 1u) ? u.x : 0xFF800000u;
+        u.y = (keep & 2u) ? u.y : 0xFF800000u;
+        u.z = (keep & 4u) ? u.z : 0xFF800000u;
+        u.w = (keep & 8u) ? u.w : 0xFF800000u;
+    }
 };
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
-    extern __shared__ uint32_t words[];                     // [chunk], then the biases [n_bias]
+    constexpr int kVec = Row<T>::kVec, kUnroll = 4;
+    extern __shared__ uint32_t words[];                     // [chunk], the biases [n_bias], the flags [chunk / kVec]
     float* s_bias = reinterpret_cast<float*>(words + p.chunk);
-    constexpr int kVec = Row<T>::kVec;
+    uint8_t* flags = reinterpret_cast<uint8_t*>(s_bias + p.n_bias);
+    __shared__ int s_draft[DSPARK_MAX_GAMMA], s_mask[DSPARK_MAX_GAMMA + 1];
     const int b = blockIdx.y, tid = threadIdx.x;
     const int v0 = blockIdx.x * p.chunk;
     const int nv = min(p.chunk, p.V - v0);
@@ -102,7 +121,23 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
         }
         rows = e + 1;
     }
-    for (int i = tid; i < p.chunk; i += kThreads) words[i] = 0;
+    for (int i = tid; i < p.chunk / 4; i += kThreads) reinterpret_cast<uint4*>(words)[i] = make_uint4(0, 0, 0, 0);
+    if (tid < rows) {
+        // the draft token that the row's count gains, and the row's mask
+        int t = -1;
+        if (tid > 0 && p.draft != nullptr) {
+            t = p.draft[static_cast<int64_t>(b) * (p.R - 1) + tid - 1];
+            if (t < 0 || t >= p.V) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 3);
+            t = t >= v0 && t < v0 + nv ? t - v0 : -1;
+        }
+        if (tid > 0) s_draft[tid - 1] = t;
+        int mr = p.mask_row != nullptr ? p.mask_row[static_cast<int64_t>(b) * p.R + tid] : -1;
+        if (mr < -1 || mr >= p.n_mask) {
+            set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 5);
+            mr = -1;
+        }
+        s_mask[tid] = mr;
+    }
     __syncthreads();
 
     // the history's tokens of this piece
@@ -112,16 +147,20 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
         if (tid == 0) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 2);
         hn = pn = 0;
     }
-    for (int i = tid; i < hn; i += kThreads) {
-        const int t = hist[i];
-        if (t < 0 || t >= p.V) {
-            set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 3);
-            continue;
+    for (int i0 = tid; i0 < hn; i0 += 4 * kThreads) {
+        int t[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t[j] = i0 + j * kThreads < hn ? hist[i0 + j * kThreads] : v0 - 1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * kThreads, v = t[j] - v0;
+            if (i >= hn) continue;
+            if (t[j] < 0 || t[j] >= p.V) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 3);
+            else if (v >= 0 && v < nv) {
+                if (i < pn) atomicOr(&words[v], kPrompt);
+                else atomicAdd(&words[v], 1u);
+            }
         }
-        const int v = t - v0;
-        if (v < 0 || v >= nv) continue;
-        if (i < pn) atomicOr(&words[v], kPrompt);
-        else atomicAdd(&words[v], 1u);
     }
     // the biases: the first entry of a token sums those of all its entries, in order
     for (int i = tid; i < p.n_bias; i += kThreads) {
@@ -139,39 +178,63 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
         s_bias[i] = sum;
         atomicOr(&words[v], static_cast<uint32_t>(i + 1) << kBiasShift);
     }
-    Rules rules{p.repetition != nullptr ? p.repetition[b] : 1.f, p.frequency != nullptr ? p.frequency[b] : 0.f,
-                p.presence != nullptr ? p.presence[b] : 0.f, s_bias};
+    const Rules rules{p.repetition != nullptr ? p.repetition[b] : 1.f, p.frequency != nullptr ? p.frequency[b] : 0.f,
+                      p.presence != nullptr ? p.presence[b] : 0.f, s_bias};
+    __syncthreads();
+    for (int i = tid; i < p.chunk / kVec; i += kThreads) {
+        uint32_t any = 0;
+#pragma unroll
+        for (int j = 0; j < kVec; j += 4) {
+            const uint4 w = reinterpret_cast<const uint4*>(words)[(i * kVec + j) / 4];
+            any |= w.x | w.y | w.z | w.w;
+        }
+        flags[i] = any != 0;
+    }
+    __syncthreads();
 
     for (int k = 0; k < rows; ++k) {
-        __syncthreads();
-        if (k > 0 && p.draft != nullptr) {
-            if (tid == 0) {
-                const int t = p.draft[static_cast<int64_t>(b) * (p.R - 1) + k - 1];
-                if (t < 0 || t >= p.V) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 3);
-                else if (t >= v0 && t < v0 + nv) words[t - v0] += 1;
+        if (k > 0) {
+            const int t = s_draft[k - 1];
+            if (t >= 0) {
+                __syncthreads();                            // the row before has been done with the old count
+                if (tid == 0) {
+                    words[t] += 1;
+                    flags[t / kVec] = 1;
+                }
+                __syncthreads();
             }
-            __syncthreads();
         }
         const int64_t row = static_cast<int64_t>(b) * p.R + k;
-        int mr = p.mask_row != nullptr ? p.mask_row[row] : -1;
-        if (mr < -1 || mr >= p.n_mask) {
-            if (tid == 0) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 5);
-            mr = -1;
-        }
-        const uint32_t* mask = mr >= 0 ? p.mask + mr * p.ld_mask : nullptr;
+        const int mr = s_mask[k];
+        const uint32_t* mask = mr >= 0 ? p.mask + mr * p.ld_mask + v0 / 32 : nullptr;
         const uint4* in = reinterpret_cast<const uint4*>(static_cast<const T*>(p.logits) + row * p.V + v0);
         uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * p.V + v0);
-        for (int i = tid; i < nv / kVec; i += kThreads) {
-            uint4 x = in[i];
-            uint32_t keep = 0xffffffffu;
-            if (mask != nullptr) keep = mask[(v0 + i * kVec) >> 5] >> ((v0 + i * kVec) & 31);
+        for (int i0 = tid; i0 < nv / kVec; i0 += kUnroll * kThreads) {
+            uint4 x[kUnroll];
+            uint32_t keep[kUnroll];
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                const uint32_t w = words[i * kVec + j];
-                const bool ok = ((keep >> j) & 1u) != 0;
-                if (w != 0 || !ok) Row<T>::put(x, j, rules(Row<T>::get(x, j), w, ok));
+            for (int u = 0; u < kUnroll; ++u) {
+                const int i = i0 + u * kThreads;
+                keep[u] = 0xffffffffu;
+                if (i < nv / kVec) {
+                    x[u] = __ldcs(in + i);
+                    if (mask != nullptr) keep[u] = __ldg(mask + i * kVec / 32) >> (i * kVec % 32);
+                }
             }
-            out[i] = x;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int i = i0 + u * kThreads;
+                if (i >= nv / kVec) continue;
+                if (flags[i] != 0) {
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) {
+                        const uint32_t w = words[i * kVec + j];
+                        if (w != 0) Row<T>::put(x[u], j, rules(Row<T>::get(x[u], j), w));
+                    }
+                }
+                if (mask != nullptr) Row<T>::mask(x[u], keep[u]);
+                __stcs(out + i, x[u]);
+            }
         }
     }
 }
@@ -211,14 +274,14 @@ extern "C" dspark_status_t dspark_adjust_logits(int B, int R, int V, dspark_dtyp
     clear_stale_error();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (clear_status(workspace, s) != DSPARK_OK) return DSPARK_ERR_CUDA;
-    AdjustArgs p{R,        V,     4096,          n_bias,      n_mask,      ld_history, ld_mask,
+    AdjustArgs p{R,        V,     8192,          n_bias,      n_mask,      ld_history, ld_mask,
                  logits,   ell,   history,       prompt_len,  history_len, draft,      repetition,
                  frequency, presence, bias_token, bias_value, mask_row,    mask,       out,
                  static_cast<StatusBlock*>(workspace)};
     while (p.chunk > 1024 && static_cast<int64_t>(B) * ((V + p.chunk - 1) / p.chunk) < 4 * sm_count(current_device()))
         p.chunk /= 2;
     const dim3 grid((V + p.chunk - 1) / p.chunk, B);
-    const size_t smem = p.chunk * 4 + static_cast<size_t>(n_bias) * 4;
+    const size_t smem = p.chunk * 4 + static_cast<size_t>(n_bias) * 4 + p.chunk / 4;
     if (dt == DSPARK_BF16) adjust_logits<__nv_bfloat16><<<grid, kThreads, smem, s>>>(p);
     else adjust_logits<float><<<grid, kThreads, smem, s>>>(p);
     return launch_status();

@@ -250,36 +250,13 @@ __device__ __forceinline__ bool part_done(const Args& p, const Piece& pc, const 
     return join;
 }
 
-// Joins the parts of a segment, in the order of the keys, and writes its rows.  First a
-// row's maximum and sum over the parts (s_row, M entries), then its elements: a thread has
-// four pieces of four elements and loads them from four parts at a time, since one block
-// reads all of it and waits for nothing but L2.
-template <typename T, int M, int kThreads, class Sync>
-__device__ __noinline__ void join_parts(const Args& p, Piece pc, Start st, float2* s_row, int tid,
-                                           Sync sync) {
-    constexpr int kE = 4, kC = 4;
-    const int c0 = block_of(pc.seg_first, st.total, st.grid);
-    const int c1 = block_of(pc.seg_first + pc.units - 1, st.total, st.grid);
-    const int left = pc.r.n * p.G - pc.tile * M, valid = left < M ? left : M;
+// The elements of joined rows: a thread has kE pieces of four elements and loads them from kC
+// parts at a time, since one block reads all of it and waits for nothing but L2.
+template <typename T, int M, int kThreads, int kE, int kC>
+__device__ __forceinline__ void join_elements(const Args& p, const Piece& pc, int c0, int c1, int valid,
+                                              const float2* s_row, int tid) {
     const float ninf = -__uint_as_float(0x7f800000u);
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-    for (int m = tid; m < valid; m += kThreads) {
-        float mx = ninf, l = 0.f;
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(ml + part_place(c, c == c0) * M + m).x);
-        const float use = mx == ninf ? 0.f : mx;
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const float2 x = __ldcg(ml + part_place(c, c == c0) * M + m);
-            l += x.y * fast_exp2(x.x - use);
-        }
-        s_row[m] = make_float2(use, l);
-        if (p.lse != nullptr) {
-            const int qi = pc.tile * M + m;
-            p.lse[(static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.Hq + pc.h * p.G + qi % p.G] = lse_of(mx, l);
-        }
-    }
-    sync();
     const int four = p.D / 4, total = valid * four;
     for (int e0 = tid; e0 < total; e0 += kE * kThreads) {
         float4 o[kE];
@@ -326,6 +303,48 @@ __device__ __noinline__ void join_parts(const Args& p, Piece pc, Start st, float
                                                      : make_float4(0.f, 0.f, 0.f, 0.f));
         }
     }
+}
+
+// Joins the parts of a segment and writes its rows: first every row's maximum and sum over the
+// parts (s_row, M entries), with as many lanes a row as there are to spare, then the elements.
+template <typename T, int M, int kThreads, class Sync>
+__device__ __noinline__ void join_parts(const Args& p, Piece pc, Start st, float2* s_row, int tid, Sync sync) {
+    const int c0 = block_of(pc.seg_first, st.total, st.grid);
+    const int c1 = block_of(pc.seg_first + pc.units - 1, st.total, st.grid);
+    const int left = pc.r.n * p.G - pc.tile * M, valid = left < M ? left : M;
+    const float ninf = -__uint_as_float(0x7f800000u);
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+    int lanes = 1;                                           // of a row: a power of two within a warp
+    while (lanes < 32 && 2 * lanes * valid <= kThreads) lanes *= 2;
+    for (int m0 = 0; m0 < valid; m0 += kThreads / lanes) {
+        const int m = m0 + tid / lanes;
+        const bool mine = m < valid;
+        float mx = ninf, l = 0.f;
+        if (mine) {
+#pragma unroll 4
+            for (int c = c0 + tid % lanes; c <= c1; c += lanes) mx = fmaxf(mx, __ldcg(ml + part_place(c, c == c0) * M + m).x);
+        }
+        for (int o = lanes / 2; o > 0; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float use = mx == ninf ? 0.f : mx;
+        if (mine) {
+#pragma unroll 4
+            for (int c = c0 + tid % lanes; c <= c1; c += lanes) {
+                const float2 x = __ldcg(ml + part_place(c, c == c0) * M + m);
+                l += x.y * fast_exp2(x.x - use);
+            }
+        }
+        for (int o = lanes / 2; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (mine && tid % lanes == 0) {
+            s_row[m] = make_float2(use, l);
+            if (p.lse != nullptr) {
+                const int qi = pc.tile * M + m;
+                p.lse[(static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.Hq + pc.h * p.G + qi % p.G] = lse_of(mx, l);
+            }
+        }
+    }
+    sync();
+    if (valid * p.D / 4 <= kThreads) join_elements<T, M, kThreads, 1, 16>(p, pc, c0, c1, valid, s_row, tid);
+    else join_elements<T, M, kThreads, 4, 4>(p, pc, c0, c1, valid, s_row, tid);
 }
 
 }  // namespace attn

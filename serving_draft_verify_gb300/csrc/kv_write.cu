@@ -4,9 +4,9 @@
 // 8 bits as e4m3(clamp(x / scale[head], +-448)), rounded to nearest even.  The
 // quotient is formed in float32 by an IEEE division; NaN stays NaN.
 //
-// Bound by memory: each element is read once and written once.  A thread moves
-// eight elements (one or two 16-byte loads); a block takes as many whole rows as
-// give it four such items a thread, all loads issued before the first store.
+// Bound by memory: each element is read once and written once.  A thread has one piece of eight
+// elements of a row (key or value, head, place) and moves it for four rows at a time, all loads
+// before the first store, so that the arithmetic of places is done once a thread and once a row.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -17,10 +17,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kItems = 4;
+constexpr int kMaxRows = 256;                   // of a block
 
 struct WriteArgs {
-    int64_t rows, k_stride, v_stride, slots;   // strides in elements
+    int64_t rows, k_stride, v_stride, slots;    // strides in elements
     int heads, D, page, rows_per_block, parts;  // parts: 8-element pieces of one row of one tensor
+    int lanes;                                  // threads of a row: a power of two, or all
     const void *k, *v;
     const int64_t* slot;
     const float *k_scale, *v_scale;
@@ -63,55 +65,58 @@ struct Eight<float> {
 
 template <typename T, bool kFp8>
 __global__ void __launch_bounds__(kThreads) write_kv(WriteArgs p) {
+    __shared__ int64_t s_to[kMaxRows];          // a row's first element of head 0 in the cache, -1: none
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_block;
     const int64_t left = p.rows - row0;
-    const int nrows = left < p.rows_per_block ? static_cast<int>(left) : p.rows_per_block;
-    const int per_row = 2 * p.parts, total = nrows * per_row, per_head = p.D / 8;
-    for (int i0 = threadIdx.x; i0 < total; i0 += kThreads * kItems) {
-        Eight<T> x[kItems];
-        int64_t to[kItems];
-        int head[kItems];
-        bool is_v[kItems];
-#pragma unroll
-        for (int j = 0; j < kItems; ++j) {
-            const int i = i0 + j * kThreads;
-            to[j] = -1;
-            if (i < total) {
-                const int r = i / per_row, e = i - r * per_row;
-                is_v[j] = e >= p.parts;
-                const int part = is_v[j] ? e - p.parts : e;
-                head[j] = part / per_head;
-                const int64_t slot = __ldg(p.slot + row0 + r);
-                if (slot >= p.slots) {
-                    if (e == 0) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 1);
-                } else if (slot >= 0) {
-                    const int64_t block = slot / p.page, off = slot - block * p.page;
-                    to[j] = ((block * p.heads + head[j]) * p.page + off) * p.D + (part - head[j] * per_head) * 8;
-                    const T* from = is_v[j] ? static_cast<const T*>(p.v) + (row0 + r) * p.v_stride
-                                            : static_cast<const T*>(p.k) + (row0 + r) * p.k_stride;
-                    x[j].load(from + static_cast<int64_t>(part) * 8);
-                }
-            }
+    const int n = left < p.rows_per_block ? static_cast<int>(left) : p.rows_per_block;
+    for (int r = threadIdx.x; r < n; r += kThreads) {
+        const int64_t slot = p.slot[row0 + r];
+        int64_t to = -1;
+        if (slot >= p.slots) {
+            set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 1);
+        } else if (slot >= 0) {
+            const int64_t block = (slot >> 32) == 0 ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.page) : slot / p.page;
+            to = (block * p.heads * p.page + (slot - block * p.page)) * p.D;
         }
+        s_to[r] = to;
+    }
+    __syncthreads();
+    const int groups = kThreads / p.lanes, mine = threadIdx.x / p.lanes, per_head = p.D / 8;
+    for (int e = threadIdx.x % p.lanes; e < 2 * p.parts; e += p.lanes) {
+        const bool is_v = e >= p.parts;
+        const int part = is_v ? e - p.parts : e, head = part / per_head;
+        const int64_t within = static_cast<int64_t>(head) * p.page * p.D + (part - head * per_head) * 8;
+        const int64_t stride = is_v ? p.v_stride : p.k_stride;
+        const T* from = static_cast<const T*>(is_v ? p.v : p.k) + row0 * stride + static_cast<int64_t>(part) * 8;
+        void* cache = is_v ? p.vc : p.kc;
+        const float scale = kFp8 ? __ldg((is_v ? p.v_scale : p.k_scale) + head) : 1.f;
+        for (int r0 = mine; r0 < n; r0 += kItems * groups) {
+            Eight<T> x[kItems];
+            int64_t to[kItems];
 #pragma unroll
-        for (int j = 0; j < kItems; ++j) {
-            if (to[j] < 0) continue;
-            void* cache = is_v[j] ? p.vc : p.kc;
-            if constexpr (kFp8) {
-                const float s = __ldg((is_v[j] ? p.v_scale : p.k_scale) + head[j]);
-                float f[8];
-                x[j].floats(f);
-                uint32_t w[2];
+            for (int j = 0; j < kItems; ++j) {
+                const int r = r0 + j * groups;
+                to[j] = r < n ? s_to[r] : -1;
+                if (to[j] >= 0) x[j].load(from + r * stride);
+            }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float2 lo = make_float2(__fdiv_rn(f[4 * h], s), __fdiv_rn(f[4 * h + 1], s));
-                    const float2 hi = make_float2(__fdiv_rn(f[4 * h + 2], s), __fdiv_rn(f[4 * h + 3], s));
-                    w[h] = __nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
-                           (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3)) << 16);
+            for (int j = 0; j < kItems; ++j) {
+                if (to[j] < 0) continue;
+                if constexpr (kFp8) {
+                    float f[8];
+                    x[j].floats(f);
+                    uint32_t w[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 lo = make_float2(__fdiv_rn(f[4 * h], scale), __fdiv_rn(f[4 * h + 1], scale));
+                        const float2 hi = make_float2(__fdiv_rn(f[4 * h + 2], scale), __fdiv_rn(f[4 * h + 3], scale));
+                        w[h] = __nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
+                               (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3)) << 16);
+                    }
+                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + to[j] + within) = make_uint2(w[0], w[1]);
+                } else {
+                    x[j].store(static_cast<T*>(cache) + to[j] + within);
                 }
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + to[j]) = make_uint2(w[0], w[1]);
-            } else {
-                x[j].store(static_cast<T*>(cache) + to[j]);
             }
         }
     }
@@ -152,8 +157,13 @@ extern "C" dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int pag
     p.slots = static_cast<int64_t>(num_blocks) * page;
     p.heads = Hkv, p.D = D, p.page = page;
     p.parts = static_cast<int>(width / 8);
-    const int want = kThreads * kItems / (2 * p.parts);
-    p.rows_per_block = want > 1 ? want : 1;
+    p.lanes = 1;
+    while (p.lanes < kThreads && p.lanes < 2 * p.parts) p.lanes *= 2;
+    // four rows a thread, and as many rows as threads at most; fewer where the rows would not fill the GPU
+    const int groups = kThreads / p.lanes;
+    p.rows_per_block = groups * kItems < kMaxRows ? groups * kItems : kMaxRows;
+    while (p.rows_per_block > 1 && (rows + p.rows_per_block - 1) / p.rows_per_block < 2 * sm_count(current_device()))
+        p.rows_per_block /= 2;
     p.k = k, p.v = v, p.slot = slot, p.k_scale = k_scale, p.v_scale = v_scale, p.kc = k_cache, p.vc = v_cache;
     p.status = static_cast<StatusBlock*>(workspace);
     const unsigned grid = static_cast<unsigned>((rows + p.rows_per_block - 1) / p.rows_per_block);
