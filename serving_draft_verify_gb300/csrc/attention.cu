@@ -11,31 +11,39 @@ namespace attn {
 namespace {
 
 // ------------------------------------------------------------ float32 rows ---
-// Sixteen query rows (four a warp) over 32 keys a unit, float32 throughout: a lane is
-// a key for the scores and a column for the values.
+// Sixteen query rows (four a warp) over 32 keys a unit, float32 throughout: a lane is a key
+// for the scores and a column for the values.  The next unit's keys and values are copied
+// (asynchronously, as they are stored) while this one's are computed on.
 constexpr int kSimtM = 16, kSimtKT = 32, kSimtThreads = 128;
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const void* base, int64_t i);
+// Four adjacent stored elements, and one, as float.
+template <typename C>
+__device__ __forceinline__ float4 four_of(const unsigned char* at);
 template <>
-__device__ __forceinline__ float4 load4<float>(const void* base, int64_t i) {
-    return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i));
+__device__ __forceinline__ float4 four_of<float>(const unsigned char* at) {
+    return *reinterpret_cast<const float4*>(at);
 }
 template <>
-__device__ __forceinline__ float4 load4<__nv_fp8_e4m3>(const void* base, int64_t i) {
-    const __nv_fp8x4_e4m3 u = *reinterpret_cast<const __nv_fp8x4_e4m3*>(static_cast<const uint8_t*>(base) + i);
-    return static_cast<float4>(u);
+__device__ __forceinline__ float4 four_of<__nv_fp8_e4m3>(const unsigned char* at) {
+    return static_cast<float4>(*reinterpret_cast<const __nv_fp8x4_e4m3*>(at));
+}
+template <typename C>
+constexpr int simt_row(int D) {                    // bytes of a staged row
+    return D * static_cast<int>(sizeof(C)) + 16;
+}
+template <typename C>
+constexpr size_t simt_smem(int D) {
+    return 4 * static_cast<size_t>(kSimtKT) * simt_row<C>(D) + (static_cast<size_t>(kSimtM) * D + kSimtM * kSimtKT) * 4;
 }
 
 template <typename C, int kCols>
 __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constant__ Args p) {
     constexpr int M = kSimtM, KT = kSimtKT;
     extern __shared__ float4 smem4[];
-    const int ld = p.D + 4;
-    float* s_q = reinterpret_cast<float*>(smem4);      // [M][D]
-    float* s_k = s_q + M * p.D;                        // [KT][ld]
-    float* s_v = s_k + KT * ld;                        // [KT][ld]
-    float* s_p = s_v + KT * ld;                        // [M][KT]: exp of the scores, -1 where masked
+    const int row_bytes = simt_row<C>(p.D), chunks = p.D * static_cast<int>(sizeof(C)) / 16;
+    unsigned char* s_kv = reinterpret_cast<unsigned char*>(smem4);                  // [2 stages][keys, values][KT] rows
+    float* s_q = reinterpret_cast<float*>(s_kv + 4 * KT * row_bytes);              // [M][D]
+    float* s_p = s_q + M * p.D;                        // [M][KT]: exp of the scores, -1 where masked
     __shared__ long long scratch[34];
     __shared__ float2 s_row[M];
     __shared__ int s_flag;
@@ -46,16 +54,41 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
     Walk<M, KT> walk(p, st);
     Piece pc;
     while (walk.next(pc)) {
-        __syncthreads();
-        const int valid = static_cast<int>(min(static_cast<int64_t>(M), static_cast<int64_t>(pc.r.n) * p.G - static_cast<int64_t>(pc.tile) * M));
+        const int left = pc.r.n * p.G - pc.tile * M, valid = left < M ? left : M;
+        // lane j has the place (in rows) of key j of a unit, found a unit ahead of its copy
+        auto find_rows = [&](int u) -> int64_t {
+            const int key = pc.span.lo + u * KT + lane;
+            if (u >= pc.u1 || key >= pc.span.hi) return 0;
+            const int blk = key / p.page;
+            return (static_cast<int64_t>(page_id(p, pc.b, blk)) * p.Hkv + pc.h) * p.page + (key - blk * p.page);
+        };
+        auto load = [&](int u, int64_t rows) {
+            if (u < pc.u1) {
+                const uint32_t to = smem_u32(s_kv) + ((u - pc.u0) & 1) * 2 * KT * row_bytes;
+                const int n = KT * chunks;             // a multiple of the warp's 32
+                for (int e = tid; e < n; e += kSimtThreads) {
+                    const int r = e / chunks, c = e - r * chunks;
+                    const int64_t row = __shfl_sync(0xffffffffu, rows, r);
+                    const bool real = pc.span.lo + u * KT + r < pc.span.hi;
+                    const int64_t at = real ? row * (p.D * static_cast<int>(sizeof(C))) + c * 16 : 0;
+                    copy16(to + r * row_bytes + c * 16, static_cast<const char*>(p.kc) + at, real);
+                    copy16(to + (KT + r) * row_bytes + c * 16, static_cast<const char*>(p.vc) + at, real);
+                }
+            }
+            copy_commit();
+        };
+        __syncthreads();                               // the last piece is done with the stages
+        load(pc.u0, find_rows(pc.u0));
+        int64_t rows = find_rows(pc.u0 + 1);
         const float qs = p.scale_log2 * (p.k_scale != nullptr ? p.k_scale[pc.h] : 1.f);
         for (int e = tid; e < M * p.D / 4; e += kSimtThreads) {
             const int m = e / (p.D / 4), d = (e - m * (p.D / 4)) * 4;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (m < valid) {
                 const int qi = pc.tile * M + m;
-                x = load4<float>(p.q, (static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.q_stride +
-                                      static_cast<int64_t>(pc.h * p.G + qi % p.G) * p.D + d);
+                x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.q) +
+                                                          (static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.q_stride +
+                                                          static_cast<int64_t>(pc.h * p.G + qi % p.G) * p.D + d));
             }
             *reinterpret_cast<float4*>(s_q + m * p.D + d) = make_float4(x.x * qs, x.y * qs, x.z * qs, x.w * qs);
         }
@@ -69,98 +102,93 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
         }
         for (int u = pc.u0; u < pc.u1; ++u) {
             const int k0 = pc.span.lo + u * KT;
+            load(u + 1, rows);
+            rows = find_rows(u + 2);
+            copy_wait<1>();
             __syncthreads();
-            for (int e = tid; e < KT * p.D / 4; e += kSimtThreads) {
-                const int j = e / (p.D / 4), d = (e - j * (p.D / 4)) * 4, key = k0 + j;
-                float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-                if (key < pc.span.hi) {
-                    const int blk = key / p.page;
-                    const int64_t at =
-                        ((static_cast<int64_t>(page_id(p, pc.b, blk)) * p.Hkv + pc.h) * p.page + (key - blk * p.page)) * p.D + d;
-                    k = load4<C>(p.kc, at);
-                    v = load4<C>(p.vc, at);
+            const unsigned char* s_k = s_kv + ((u - pc.u0) & 1) * 2 * KT * row_bytes;
+            const unsigned char* s_v = s_k + KT * row_bytes;
+            if (4 * w < valid) {
+                float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+                for (int d = 0; d < p.D; d += 4) {
+                    const float4 k = four_of<C>(s_k + lane * row_bytes + d * sizeof(C));
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float4 q = *reinterpret_cast<const float4*>(s_q + (4 * w + r) * p.D + d);
+                        s[r] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[r]))));
+                    }
                 }
-                *reinterpret_cast<float4*>(s_k + j * ld + d) = k;
-                *reinterpret_cast<float4*>(s_v + j * ld + d) = v;
-            }
-            __syncthreads();
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int d = 0; d < p.D; d += 4) {
-                const float4 k = *reinterpret_cast<const float4*>(s_k + lane * ld + d);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float4 q = *reinterpret_cast<const float4*>(s_q + (4 * w + r) * p.D + d);
-                    s[r] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[r]))));
+                    const int m = 4 * w + r, pos = pc.r.len + (pc.tile * M + m) / p.G, key = k0 + lane;
+                    const bool seen = m < valid && key <= pos && (p.window == 0 || key > pos - p.window);
+                    const float nm = fmaxf(mx[r], warp_max(seen ? s[r] : ninf));
+                    const float use = nm == ninf ? 0.f : nm;
+                    const float a = fast_exp2(mx[r] - use), e = seen ? fast_exp2(s[r] - use) : 0.f;
+                    mx[r] = nm;
+                    l[r] = l[r] * a + e;               // this lane's keys; the lanes' sums meet at the end
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c) o[r][c] *= a;
+                    s_p[m * KT + lane] = seen ? e : -1.f;
                 }
-            }
+                __syncwarp();
+#pragma unroll 4
+                for (int j = 0; j < KT; ++j) {
+                    float v[kCols];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int m = 4 * w + r, pos = pc.r.len + (pc.tile * M + m) / p.G, key = k0 + lane;
-                const bool seen = m < valid && key <= pos && (p.window == 0 || key > pos - p.window);
-                const float nm = fmaxf(mx[r], warp_max(seen ? s[r] : ninf));
-                const float use = nm == ninf ? 0.f : nm;
-                const float a = fast_exp2(mx[r] - use), e = seen ? fast_exp2(s[r] - use) : 0.f;
-                mx[r] = nm;
-                l[r] = l[r] * a + warp_sum(e);
+                    for (int c = 0; c < kCols; ++c)
+                        v[c] = lane + 32 * c < p.D ? static_cast<float>(reinterpret_cast<const C*>(s_v + j * row_bytes)[lane + 32 * c]) : 0.f;
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) o[r][c] *= a;
-                s_p[m * KT + lane] = seen ? e : -1.f;
-            }
-            __syncwarp();
-            for (int j = 0; j < KT; ++j) {
-                float v[kCols];
+                    for (int r = 0; r < 4; ++r) {
+                        const float e = s_p[(4 * w + r) * KT + j];
+                        // a masked key's value stays out even where it is not a number
+                        if (!(e < 0.f)) {
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) v[c] = lane + 32 * c < p.D ? s_v[j * ld + lane + 32 * c] : 0.f;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float e = s_p[(4 * w + r) * KT + j];
-                    // a masked key's value stays out even where it is not a number
-                    if (!(e < 0.f)) {
-#pragma unroll
-                        for (int c = 0; c < kCols; ++c) o[r][c] = fmaf(e, v[c], o[r][c]);
+                            for (int c = 0; c < kCols; ++c) o[r][c] = fmaf(e, v[c], o[r][c]);
+                        }
                     }
                 }
             }
+            __syncthreads();
         }
+        copy_wait<0>();
         const float vs = p.v_scale != nullptr ? p.v_scale[pc.h] : 1.f;
-        if (pc.whole()) {
+        const bool whole = pc.whole();
+        const int64_t place = part_place(blockIdx.x, pc.u0 == 0) * M;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int m = 4 * w + r;
-                if (m >= valid) continue;
-                const int qi = pc.tile * M + m, head = pc.h * p.G + qi % p.G;
-                const int64_t row = static_cast<int64_t>(pc.r.row0) + qi / p.G;
+        for (int r = 0; r < 4; ++r) {
+            const int m = 4 * w + r;
+            if (m >= valid) continue;
+            l[r] = warp_sum(l[r]);
+            const int qi = pc.tile * M + m, head = pc.h * p.G + qi % p.G;
+            const int64_t row = static_cast<int64_t>(pc.r.row0) + qi / p.G, at = place + m;
+            float* to = whole ? static_cast<float*>(p.out) + (row * p.Hq + head) * p.D : p.part_o + at * p.D;
+            const float f = !whole ? vs : l[r] != 0.f ? vs / l[r] : 0.f;
 #pragma unroll
-                for (int c = 0; c < kCols; ++c)
-                    if (lane + 32 * c < p.D)
-                        static_cast<float*>(p.out)[(row * p.Hq + head) * p.D + lane + 32 * c] = l[r] != 0.f ? o[r][c] * vs / l[r] : 0.f;
-                if (lane == 0 && p.lse != nullptr) p.lse[row * p.Hq + head] = lse_of(mx[r], l[r]);
+            for (int c = 0; c < kCols; ++c)
+                if (lane + 32 * c < p.D) to[lane + 32 * c] = whole && l[r] == 0.f ? 0.f : o[r][c] * f;
+            if (lane == 0) {
+                if (!whole) reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(mx[r], l[r]);
+                else if (p.lse != nullptr) p.lse[row * p.Hq + head] = lse_of(mx[r], l[r]);
             }
-        } else {
-            const int64_t place = part_place(blockIdx.x, pc.u0 == 0) * M;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int64_t at = place + 4 * w + r;
-#pragma unroll
-                for (int c = 0; c < kCols; ++c)
-                    if (lane + 32 * c < p.D) p.part_o[at * p.D + lane + 32 * c] = o[r][c] * vs;
-                if (lane == 0) reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(mx[r], l[r]);
-            }
-            if (part_done(p, pc, st, &s_flag, tid, [] { __syncthreads(); })) join_parts<float, M, kSimtThreads>(p, pc, st, s_row, tid, [] { __syncthreads(); });
         }
+        if (!whole && part_done(p, pc, st, &s_flag, tid, [] { __syncthreads(); }))
+            join_parts<float, M, kSimtThreads>(p, pc, st, s_row, tid, [] { __syncthreads(); });
     }
 }
 
 template <typename C, int kCols>
 dspark_status_t launch_simt(const Args& p, cudaStream_t s) {
-    const size_t smem = (static_cast<size_t>(kSimtM) * p.D + 2 * kSimtKT * (p.D + 4) + kSimtM * kSimtKT) * 4;
     static OncePerDevice once;
     if (once.run(current_device(), [] {
             return cudaFuncSetAttribute(attend_simt<C, kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (kSimtM * 256 + 2 * kSimtKT * 260 + kSimtM * kSimtKT) * 4);
+                                        static_cast<int>(simt_smem<C>(32 * kCols)));
         }) != cudaSuccess)
         return DSPARK_ERR_CUDA;
-    const int grid = grid_for(sm_count(current_device()) * (kCols <= 4 ? 4 : 2), kSimtM);
+    const size_t smem = simt_smem<C>(p.D);
+    const int per_sm = smem <= 52 * 1024 ? 4 : smem <= 108 * 1024 ? 2 : 1;
+    const int grid = grid_for(sm_count(current_device()) * per_sm, kSimtM);
     if (grid < 1) return DSPARK_ERR_CUDA;
     attend_simt<C, kCols><<<grid, kSimtThreads, smem, s>>>(p);
     return launch_status();

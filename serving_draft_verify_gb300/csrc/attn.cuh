@@ -94,6 +94,12 @@ __device__ __forceinline__ int64_t head_units(const Args& p, const Request& r) {
     return u;
 }
 
+// a / b for a >= 0, b > 0; the 64-bit division only where a needs it.
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // The block's first unit: request, and units into it; found by all threads together.
 // scratch: 34 words of 8 bytes.
 struct Start {
@@ -127,8 +133,8 @@ __device__ __forceinline__ Start find_start(const Args& p, long long* scratch) {
     s.total = total;
     s.grid = total < gridDim.x ? static_cast<int>(total) : static_cast<int>(gridDim.x);
     const int64_t c = blockIdx.x, n = s.grid;
-    s.first = c < n ? total * c / n : total;
-    s.last = c < n ? total * (c + 1) / n : total;
+    s.first = c < n ? div_pos(total * c, n) : total;
+    s.last = c < n ? div_pos(total * (c + 1), n) : total;
     if (at <= s.first && s.first < at + mine) {
         long long u = at;
         for (int b = b0; b < b1; ++b) {
@@ -149,7 +155,7 @@ __device__ __forceinline__ Start find_start(const Args& p, long long* scratch) {
 
 // The block that holds unit u of `total` over `grid` blocks.
 __device__ __forceinline__ int block_of(int64_t u, int64_t total, int grid) {
-    return static_cast<int>(((u + 1) * grid - 1) / total);
+    return static_cast<int>(div_pos((u + 1) * grid - 1, total));
 }
 
 // A piece of a segment: units [u0, u1) of the segment's `units`.
@@ -184,9 +190,9 @@ struct Walk {
             r = request_of(p, b, false);
             req_units = p.Hkv * head_units<M, KT>(p, r);
         }
-        const int64_t per_head = req_units / p.Hkv;
+        const int64_t per_head = div_pos(req_units, p.Hkv);
         int64_t into = at - req_first;
-        out.h = static_cast<int>(into / per_head);
+        out.h = static_cast<int>(div_pos(into, per_head));
         into -= out.h * per_head;
         int t = 0;
         Span sp = span_of<M, KT>(p, r, 0);

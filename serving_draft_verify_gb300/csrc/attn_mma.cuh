@@ -150,6 +150,41 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
     while (walk.next(pc)) {
         const int left = pc.r.n * p.G - pc.tile * M;
         const int valid = left < M ? left : M;
+        // ---- the first keys and values are on their way before anything else
+        const int steps = pc.u1 - pc.u0;
+        const int key0 = pc.span.lo + pc.u0 * KT + w * KS;   // this warp's first key; then every KT
+        // Where the keys of step s lie: the row (of D elements) of lane's key, or of the
+        // step's first key where a page holds the whole step.
+        auto find_rows = [&](int s) -> int64_t {
+            const int key = key0 + s * KT + (whole_pages ? 0 : lane);
+            if (s >= steps || key >= pc.span.hi || (!whole_pages && lane >= KS)) return 0;
+            const int blk = key / p.page;
+            return (static_cast<int64_t>(page_id(p, pc.b, blk)) * p.Hkv + pc.h) * p.page + (key - blk * p.page);
+        };
+        auto load = [&](int s, int64_t rows) {
+            const int first = key0 + s * KT;
+            if (s < steps && first < pc.span.hi) {
+                const uint32_t to = ring_a + (s % kStages) * Sh::kStage;
+                const char* kc = static_cast<const char*>(p.kc);
+                const char* vc = static_cast<const char*>(p.vc);
+#pragma unroll
+                for (int i = 0; i < KS * kChunks / 32; ++i) {
+                    const int e = lane + 32 * i, r = e / kChunks, c = e % kChunks;
+                    const int64_t row = whole_pages ? rows + r : __shfl_sync(0xffffffffu, rows, r);
+                    const bool real = first + r < pc.span.hi && c < real_chunks;
+                    const int64_t at = real ? row * (p.D * esize) + c * 16 : 0;
+                    const uint32_t d = to + chunk_at<kRow>(r, c);
+                    copy16(d, kc + at, real);
+                    copy16(d + KS * kRow, vc + at, real);
+                }
+            }
+            copy_commit();
+        };
+        int64_t rows = 0;
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) load(s, find_rows(s));
+        rows = find_rows(kStages - 1);
+
         // ---- the queries, 16-bit, swizzled; rows past the last are zero
         for (int e = tid; e < M * (DT / 8); e += kThreads) {
             const int m = e / (DT / 8), c = e - m * (DT / 8);
@@ -220,40 +255,6 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[mt][n][i] = 0.f;
         }
-
-        const int steps = pc.u1 - pc.u0;
-        const int key0 = pc.span.lo + pc.u0 * KT + w * KS;   // this warp's first key; then every KT
-        // Where the keys of step s lie: the row (of D elements) of lane's key, or of the
-        // step's first key where a page holds the whole step.
-        auto find_rows = [&](int s) -> int64_t {
-            const int key = key0 + s * KT + (whole_pages ? 0 : lane);
-            if (s >= steps || key >= pc.span.hi || (!whole_pages && lane >= KS)) return 0;
-            const int blk = key / p.page;
-            return (static_cast<int64_t>(page_id(p, pc.b, blk)) * p.Hkv + pc.h) * p.page + (key - blk * p.page);
-        };
-        auto load = [&](int s, int64_t rows) {
-            const int first = key0 + s * KT;
-            if (s < steps && first < pc.span.hi) {
-                const uint32_t to = ring_a + (s % kStages) * Sh::kStage;
-                const char* kc = static_cast<const char*>(p.kc);
-                const char* vc = static_cast<const char*>(p.vc);
-#pragma unroll
-                for (int i = 0; i < KS * kChunks / 32; ++i) {
-                    const int e = lane + 32 * i, r = e / kChunks, c = e % kChunks;
-                    const int64_t row = whole_pages ? rows + r : __shfl_sync(0xffffffffu, rows, r);
-                    const bool real = first + r < pc.span.hi && c < real_chunks;
-                    const int64_t at = real ? row * (p.D * esize) + c * 16 : 0;
-                    const uint32_t d = to + chunk_at<kRow>(r, c);
-                    copy16(d, kc + at, real);
-                    copy16(d + KS * kRow, vc + at, real);
-                }
-            }
-            copy_commit();
-        };
-        int64_t rows = 0;
-#pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) load(s, find_rows(s));
-        rows = find_rows(kStages - 1);
 
         const int pos_lo = pc.r.len + pc.tile * M / p.G, pos_hi = pc.span.hi - 1;   // the tile's first and last position
         for (int s = 0; s < steps; ++s) {

@@ -8,8 +8,8 @@
 //
 // One launch.  Every block runs the prefix sums over all B requests itself (they
 // are a few kilobytes that L2 holds), so no block waits for another, and keeps
-// the part that its own 512 rows need: the first row of each request marks its
-// place in shared memory and a running maximum over the marks gives every row its
+// the part that its own rows need (a thread a row): the first row of each request marks
+// its place in shared memory and a running maximum over the marks gives every row its
 // request.  A new page starts at a row of the step, so the thread of that row
 // enters it in the table; pages that go back are copied by the block that owns the
 // request's tile.  The last block to finish (a counter, nobody waits) writes the
@@ -19,8 +19,6 @@
 
 namespace dspark {
 namespace {
-
-constexpr int kT = 512;          // threads, rows and requests of one tile
 
 struct PlanArgs {
     int B, page, max_blocks, num_blocks;
@@ -58,7 +56,7 @@ __device__ __forceinline__ Ask ask_of(const PlanArgs& p, int b) {
     a.base = static_cast<int>(base);
     a.rows = static_cast<int>(rows);
     a.held = static_cast<int>(held);
-    a.need = static_cast<int>((end + p.page - 1) / p.page);
+    a.need = static_cast<int>((static_cast<uint32_t>(end) + p.page - 1) / static_cast<uint32_t>(p.page));
     return a;
 }
 
@@ -66,38 +64,47 @@ __device__ __forceinline__ Ask ask_of(const PlanArgs& p, int b) {
 struct Sums {
     unsigned long long rows, pages;      // pages: take in the low half, give in the high half
 };
-__device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_tot, Sums& total) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    Sums inc = v;
+__device__ __forceinline__ Sums warp_scan(Sums v) {          // inclusive
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long r = __shfl_up_sync(0xffffffffu, inc.rows, o);
-        const unsigned long long g = __shfl_up_sync(0xffffffffu, inc.pages, o);
+        const unsigned long long r = __shfl_up_sync(0xffffffffu, v.rows, o);
+        const unsigned long long g = __shfl_up_sync(0xffffffffu, v.pages, o);
         if (lane >= o) {
-            inc.rows += r;
-            inc.pages += g;
+            v.rows += r;
+            v.pages += g;
         }
     }
+    return v;
+}
+// warp_tot: kT / 32 + 1 entries, the last for the total
+template <int kT>
+__device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_tot, Sums& total) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const Sums inc = warp_scan(v);
     __syncthreads();                      // the last scan's totals have been read
     if (lane == 31) warp_tot[w] = inc;
     __syncthreads();
-    Sums before{0, 0};
-    total = Sums{0, 0};
-#pragma unroll
-    for (int i = 0; i < kT / 32; ++i) {
-        const Sums t = warp_tot[i];
-        if (i < w) {
-            before.rows += t.rows;
-            before.pages += t.pages;
-        }
-        total.rows += t.rows;
-        total.pages += t.pages;
+    if (w == 0) {
+        const Sums t = lane < kT / 32 ? warp_tot[lane] : Sums{0, 0};
+        const Sums all = warp_scan(t);
+        if (lane < kT / 32) warp_tot[lane] = Sums{all.rows - t.rows, all.pages - t.pages};
+        if (lane == 31) warp_tot[kT / 32] = all;
     }
+    __syncthreads();
+    const Sums before = warp_tot[w];
+    total = warp_tot[kT / 32];
     return Sums{before.rows + inc.rows - v.rows, before.pages + inc.pages - v.pages};
 }
+// x modulo cap for 0 <= x < 3 cap.
+__device__ __forceinline__ int64_t around(int64_t x, int cap) {
+    x = x >= cap ? x - cap : x;
+    return x >= cap ? x - cap : x;
+}
 
+template <int kT>
 __global__ void __launch_bounds__(kT) plan_rows(PlanArgs p) {
-    __shared__ Sums warp_tot[kT / 32];
+    __shared__ Sums warp_tot[kT / 32 + 1];
     __shared__ int s_mark[kT];            // marked row -> request + 1
     __shared__ int s_pos[kT], s_held[kT];
     __shared__ long long s_take[kT];
@@ -128,7 +135,7 @@ __global__ void __launch_bounds__(kT) plan_rows(PlanArgs p) {
         Sums v{static_cast<unsigned long long>(a.rows),
                static_cast<unsigned long long>(take) | (static_cast<unsigned long long>(give) << 32)};
         Sums tot;
-        Sums at = block_scan(v, warp_tot, tot);
+        Sums at = block_scan<kT>(v, warp_tot, tot);
         at.rows += run.rows;
         at.pages += run.pages;
         run.rows += tot.rows;
@@ -178,19 +185,19 @@ __global__ void __launch_bounds__(kT) plan_rows(PlanArgs p) {
         if (why == 0 && row < N && m >= 0) {
             req = s_mark[m] - 1;
             pos = s_pos[m] + (tid - m);
-            const int block = pos / p.page, held = s_held[m];
+            const int block = pos / p.page, off = pos - block * p.page, held = s_held[m];
             int32_t* entry = p.table + static_cast<int64_t>(req) * p.ld + block;
             int id;
             if (block >= held) {
-                id = p.ring[(head + s_take[m] + (block - held)) % cap];
-                if (pos % p.page == 0) *entry = id;
+                id = p.ring[around(head + s_take[m] + (block - held), cap)];
+                if (off == 0) *entry = id;
             } else {
                 id = *entry;
             }
             if (id < 0 || id >= cap)
                 set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 5);
             else
-                slot = static_cast<int64_t>(id) * p.page + pos % p.page;
+                slot = static_cast<int64_t>(id) * p.page + off;
         }
         p.row_request[row] = req;
         p.position[row] = pos;
@@ -202,7 +209,7 @@ __global__ void __launch_bounds__(kT) plan_rows(PlanArgs p) {
             const int need = s_gneed[e], held = s_gheld[e];
             const int32_t* from = p.table + static_cast<int64_t>(s_gb[e]) * p.ld;
             const int64_t to = static_cast<int64_t>(head) + count + s_gat[e];
-            for (int j = need + (tid & 31); j < held; j += 32) p.ring[(to + (j - need)) % cap] = from[j];
+            for (int j = need + (tid & 31); j < held; j += 32) p.ring[around(to + (j - need), cap)] = from[j];
         }
     }
 
@@ -224,7 +231,7 @@ __global__ void __launch_bounds__(kT) plan_rows(PlanArgs p) {
             own = Ask{};
             if (b < p.B) own = ask_of(p, b);
             Sums tot;
-            own_at = block_scan(Sums{static_cast<unsigned long long>(own.rows), 0}, warp_tot, tot);
+            own_at = block_scan<kT>(Sums{static_cast<unsigned long long>(own.rows), 0}, warp_tot, tot);
             own_at.rows += run.rows;
             run.rows += tot.rows;
         }
@@ -236,7 +243,7 @@ __global__ void __launch_bounds__(kT) plan_rows(PlanArgs p) {
     }
     if (tid == 0) {
         p.row_offset[p.B] = why == 0 ? static_cast<int32_t>(N) : 0;
-        p.free_out[0] = why == 0 ? static_cast<int32_t>((head + T) % cap) : head;
+        p.free_out[0] = why == 0 ? static_cast<int32_t>(around(head + T, cap)) : head;
         p.free_out[1] = why == 0 ? static_cast<int32_t>(count - T + R) : count;
     }
 }
@@ -276,9 +283,13 @@ extern "C" dspark_status_t dspark_plan_rows(int B, int page, int max_blocks, int
                rows,     held,      free_state, free_ring,      block_table, len_out, held_out,  free_state_out,
                row_offset, row_request, position, slot,         static_cast<StatusBlock*>(workspace),
                reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + kStatusBytes)};
-    const int64_t row_tiles = (max_rows + kT - 1) / kT, req_tiles = (B + kT - 1) / kT;
+    // a small step is one small block: its scans and barriers are the call's time
+    const bool small = B <= 256 && max_rows <= 256;
+    const int64_t tile = small ? 256 : 1024;
+    const int64_t row_tiles = (max_rows + tile - 1) / tile, req_tiles = (B + tile - 1) / tile;
     const int64_t grid = row_tiles > req_tiles ? row_tiles : req_tiles;
     if (grid > 1 && cudaMemsetAsync(workspace, 0, kStatusBytes + 16, s) != cudaSuccess) return DSPARK_ERR_CUDA;
-    plan_rows<<<static_cast<unsigned>(grid), kT, 0, s>>>(p);
+    if (small) plan_rows<256><<<static_cast<unsigned>(grid), 256, 0, s>>>(p);
+    else plan_rows<1024><<<static_cast<unsigned>(grid), 1024, 0, s>>>(p);
     return launch_status();
 }
