@@ -114,11 +114,11 @@ struct Row<float> {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
-    constexpr int kVec = Row<T>::kVec, kUnroll = 4;
+    constexpr int kVec = Row<T>::kVec, kUnroll = 2;
     extern __shared__ uint32_t words[];                     // [chunk], the biases [n_bias], the bits [chunk / kVec bytes]
     float* s_bias = reinterpret_cast<float*>(words + p.chunk);
     uint8_t* flags = reinterpret_cast<uint8_t*>(s_bias + p.n_bias);
-    __shared__ int s_draft[DSPARK_MAX_GAMMA], s_mask[DSPARK_MAX_GAMMA + 1];
+    __shared__ int s_draft[DSPARK_MAX_GAMMA];
     const int b = blockIdx.x, tid = threadIdx.x;
     const int v0 = blockIdx.y * p.chunk;
     const int nv = min(p.chunk, p.V - v0);
@@ -131,9 +131,38 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
         }
         rows = e + 1;
     }
+    // The stream: batches of kUnroll pieces a thread, row by row.  A batch is loaded while the one
+    // before is worked on, and the first while the history is counted.
+    const int nvec = nv / kVec;
+    struct Batch {
+        uint4 x[kUnroll];
+        uint32_t keep[kUnroll];
+        bool masked;
+    };
+    auto mask_of = [&](int k) {
+        int mr = p.mask_row != nullptr ? __ldg(p.mask_row + static_cast<int64_t>(b) * p.R + k) : -1;
+        return mr < -1 || mr >= p.n_mask ? -1 : mr;
+    };
+    int next_mask = mask_of(0);                             // of the row being loaded
+    auto load = [&](Batch& t, int k, int i0) {
+        const uint4* in = reinterpret_cast<const uint4*>(static_cast<const T*>(p.logits) + (static_cast<int64_t>(b) * p.R + k) * p.V + v0);
+        const uint32_t* mask = p.mask + next_mask * p.ld_mask + v0 / 32;
+        t.masked = next_mask >= 0;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = i0 + u * kThreads;
+            t.keep[u] = 0xffffffffu;
+            if (i < nvec) {
+                t.x[u] = __ldcs(in + i);
+                if (t.masked) t.keep[u] = __ldg(mask + i * kVec / 32) >> (i * kVec % 32);
+            }
+        }
+    };
+    Batch now, then;
+    load(then, 0, tid);
     for (int i = tid; i < p.chunk / 4; i += kThreads) reinterpret_cast<uint4*>(words)[i] = make_uint4(0, 0, 0, 0);
     if (tid < rows) {
-        // the draft token that the row's count gains, and the row's mask
+        // the draft token that the row's count gains
         int t = -1;
         if (tid > 0 && p.draft != nullptr) {
             t = p.draft[static_cast<int64_t>(b) * (p.R - 1) + tid - 1];
@@ -141,12 +170,10 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
             t = t >= v0 && t < v0 + nv ? t - v0 : -1;
         }
         if (tid > 0) s_draft[tid - 1] = t;
-        int mr = p.mask_row != nullptr ? p.mask_row[static_cast<int64_t>(b) * p.R + tid] : -1;
-        if (mr < -1 || mr >= p.n_mask) {
-            set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 5);
-            mr = -1;
+        if (p.mask_row != nullptr) {
+            const int mr = p.mask_row[static_cast<int64_t>(b) * p.R + tid];
+            if (mr < -1 || mr >= p.n_mask) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 5);
         }
-        s_mask[tid] = mr;
     }
     __syncthreads();
 
@@ -214,33 +241,25 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
                 __syncthreads();
             }
         }
-        const int64_t row = static_cast<int64_t>(b) * p.R + k;
-        const int mr = s_mask[k];
-        const uint32_t* mask = mr >= 0 ? p.mask + mr * p.ld_mask + v0 / 32 : nullptr;
-        const uint4* in = reinterpret_cast<const uint4*>(static_cast<const T*>(p.logits) + row * p.V + v0);
-        uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * p.V + v0);
-        for (int i0 = tid; i0 < nv / kVec; i0 += kUnroll * kThreads) {
-            uint4 x[kUnroll];
-            uint32_t keep[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int i = i0 + u * kThreads;
-                keep[u] = 0xffffffffu;
-                if (i < nv / kVec) {
-                    x[u] = __ldcs(in + i);
-                    if (mask != nullptr) keep[u] = __ldg(mask + i * kVec / 32) >> (i * kVec % 32);
-                }
+        uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (static_cast<int64_t>(b) * p.R + k) * p.V + v0);
+        for (int i0 = tid; i0 < nvec + tid; i0 += kUnroll * kThreads) {
+            now = then;
+            if (i0 - tid + kUnroll * kThreads < nvec) {
+                load(then, k, i0 + kUnroll * kThreads);
+            } else if (k + 1 < rows) {
+                next_mask = mask_of(k + 1);
+                load(then, k + 1, tid);
             }
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 const int i = i0 + u * kThreads;
-                if (i >= nv / kVec) continue;
+                if (i >= nvec) continue;
                 for (uint32_t set = flags[i]; set != 0; set &= set - 1) {
                     const int j = __ffs(set) - 1;
-                    Row<T>::put(x[u], j, rules(Row<T>::get(x[u], j), words[i * kVec + j]));
+                    Row<T>::put(now.x[u], j, rules(Row<T>::get(now.x[u], j), words[i * kVec + j]));
                 }
-                if (mask != nullptr) Row<T>::mask(x[u], keep[u]);
-                __stcs(out + i, x[u]);
+                if (now.masked) Row<T>::mask(now.x[u], now.keep[u]);
+                __stcs(out + i, now.x[u]);
             }
         }
     }

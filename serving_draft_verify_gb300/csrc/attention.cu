@@ -12,11 +12,11 @@ namespace {
 
 // ------------------------------------------------------------ float32 rows ---
 // Sixteen query rows (four a warp) over 32 keys a unit, float32 throughout: a lane is a key
-// for the scores and a column for the values.  The next unit's keys and values are copied
+// for the scores and has pairs of columns of the values.  The next unit's keys and values are copied
 // (asynchronously, as they are stored) while this one's are computed on.
 constexpr int kSimtM = 16, kSimtKT = 32, kSimtThreads = 128;
 
-// Four adjacent stored elements, and one, as float.
+// Four adjacent stored elements, and two, as float.
 template <typename C>
 __device__ __forceinline__ float4 four_of(const unsigned char* at);
 template <>
@@ -26,6 +26,16 @@ __device__ __forceinline__ float4 four_of<float>(const unsigned char* at) {
 template <>
 __device__ __forceinline__ float4 four_of<__nv_fp8_e4m3>(const unsigned char* at) {
     return static_cast<float4>(*reinterpret_cast<const __nv_fp8x4_e4m3*>(at));
+}
+template <typename C>
+__device__ __forceinline__ float2 two_of(const unsigned char* row, int d);
+template <>
+__device__ __forceinline__ float2 two_of<float>(const unsigned char* row, int d) {
+    return *reinterpret_cast<const float2*>(row + 4 * d);
+}
+template <>
+__device__ __forceinline__ float2 two_of<__nv_fp8_e4m3>(const unsigned char* row, int d) {
+    return static_cast<float2>(*reinterpret_cast<const __nv_fp8x2_e4m3*>(row + d));
 }
 template <typename C>
 constexpr int simt_row(int D) {                    // bytes of a staged row
@@ -133,19 +143,31 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
                     s_p[m * KT + lane] = seen ? e : -1.f;
                 }
                 __syncwarp();
-#pragma unroll 4
-                for (int j = 0; j < KT; ++j) {
-                    float v[kCols];
+                // Four keys at a time.  A masked key's value stays out even where it is not a number; only
+                // units with masked keys ask.
+                const bool masked = k0 + KT - 1 > pc.r.len + (pc.tile * M + 4 * w) / p.G ||
+                                    (p.window > 0 && k0 <= pc.r.len + (pc.tile * M + 4 * w + 3) / p.G - p.window) || 4 * w + 3 >= valid;
+#pragma unroll 1
+                for (int j = 0; j < KT; j += 4) {
+                    float4 e[4];
 #pragma unroll
-                    for (int c = 0; c < kCols; ++c)
-                        v[c] = lane + 32 * c < p.D ? static_cast<float>(reinterpret_cast<const C*>(s_v + j * row_bytes)[lane + 32 * c]) : 0.f;
+                    for (int r = 0; r < 4; ++r) e[r] = *reinterpret_cast<const float4*>(s_p + (4 * w + r) * KT + j);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float e = s_p[(4 * w + r) * KT + j];
-                        // a masked key's value stays out even where it is not a number
-                        if (!(e < 0.f)) {
+                    for (int i = 0; i < 4; ++i) {
+                        float2 v[kCols / 2];
 #pragma unroll
-                            for (int c = 0; c < kCols; ++c) o[r][c] = fmaf(e, v[c], o[r][c]);
+                        for (int c = 0; c < kCols / 2; ++c)
+                            v[c] = 2 * lane + 64 * c < p.D ? two_of<C>(s_v + (j + i) * row_bytes, 2 * lane + 64 * c) : make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float x = i == 0 ? e[r].x : i == 1 ? e[r].y : i == 2 ? e[r].z : e[r].w;
+                            if (!masked || !(x < 0.f)) {
+#pragma unroll
+                                for (int c = 0; c < kCols / 2; ++c) {
+                                    o[r][2 * c] = fmaf(x, v[c].x, o[r][2 * c]);
+                                    o[r][2 * c + 1] = fmaf(x, v[c].y, o[r][2 * c + 1]);
+                                }
+                            }
                         }
                     }
                 }
@@ -166,8 +188,10 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
             float* to = whole ? static_cast<float*>(p.out) + (row * p.Hq + head) * p.D : p.part_o + at * p.D;
             const float f = !whole ? vs : l[r] != 0.f ? vs / l[r] : 0.f;
 #pragma unroll
-            for (int c = 0; c < kCols; ++c)
-                if (lane + 32 * c < p.D) to[lane + 32 * c] = whole && l[r] == 0.f ? 0.f : o[r][c] * f;
+            for (int c = 0; c < kCols / 2; ++c)
+                if (2 * lane + 64 * c < p.D)
+                    *reinterpret_cast<float2*>(to + 2 * lane + 64 * c) =
+                        whole && l[r] == 0.f ? make_float2(0.f, 0.f) : make_float2(o[r][2 * c] * f, o[r][2 * c + 1] * f);
             if (lane == 0) {
                 if (!whole) reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(mx[r], l[r]);
                 else if (p.lse != nullptr) p.lse[row * p.Hq + head] = lse_of(mx[r], l[r]);
