@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
     unsigned char* s_kv = reinterpret_cast<unsigned char*>(smem4);                  // [2 stages][keys, values][KT] rows
     float* s_q = reinterpret_cast<float*>(s_kv + 4 * KT * row_bytes);              // [M][D]
     float* s_p = s_q + M * p.D;                        // [M][KT]: exp of the scores, -1 where masked
-    __shared__ long long scratch[34];
+    __shared__ long long scratch[38];
     __shared__ float2 s_row[M];
     __shared__ int s_flag;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;

@@ -85,13 +85,22 @@ template <int M>
 __device__ __forceinline__ int tiles_of(const Args& p, const Request& r) {
     return static_cast<int>((static_cast<int64_t>(r.n) * p.G + M - 1) / M);
 }
-// Units of one key head of a request.
+// A request with the units of one of its key heads.  One copy of the code for all that ask: a
+// block of a short call runs most of its instructions once, and fetching them is what it
+// waits for.
+struct Asked {
+    Request r;
+    int64_t units;
+};
 template <int M, int KT>
-__device__ __forceinline__ int64_t head_units(const Args& p, const Request& r) {
-    int64_t u = 0;
-    const int nt = tiles_of<M>(p, r);
-    for (int t = 0; t < nt; ++t) u += span_of<M, KT>(p, r, t).units(KT);
-    return u;
+__device__ __noinline__ Asked ask(const Args& p, int b, bool tell) {
+    Asked a;
+    a.r = request_of(p, b, tell);
+    a.units = 0;
+    const int nt = tiles_of<M>(p, a.r);
+#pragma unroll 1
+    for (int t = 0; t < nt; ++t) a.units += span_of<M, KT>(p, a.r, t).units(KT);
+    return a;
 }
 
 // a / b for a >= 0, b > 0; the 64-bit division only where a needs it.
@@ -101,12 +110,13 @@ __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
 }
 
 // The block's first unit: request, and units into it; found by all threads together.
-// scratch: 34 words of 8 bytes.
+// scratch: 38 words of 8 bytes.
 struct Start {
     int64_t total, first, last;       // units in all, and this block's [first, last)
-    int grid;                         // blocks that have units (no more than there are units)
+    int grid;                         // blocks that have units
     int b;
     int64_t into;                     // units before `first` in request b
+    Asked a;                          // request b
 };
 template <int M, int KT, int kThreads>
 __device__ __forceinline__ Start find_start(const Args& p, long long* scratch) {
@@ -114,7 +124,12 @@ __device__ __forceinline__ Start find_start(const Args& p, long long* scratch) {
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += p.Hkv * head_units<M, KT>(p, request_of(p, b, blockIdx.x == 0));
+    Asked a{};
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+        a = ask<M, KT>(p, b, blockIdx.x == 0);
+        mine += p.Hkv * a.units;
+    }
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -131,25 +146,33 @@ __device__ __forceinline__ Start find_start(const Args& p, long long* scratch) {
     const long long at = before + inc - mine;
     Start s;
     s.total = total;
-    s.grid = total < gridDim.x ? static_cast<int>(total) : static_cast<int>(gridDim.x);
+    // two units a block at least where units are short: a part costs its joining more than a unit does
+    const long long most = M >= 128 ? total : (total + 1) / 2;
+    s.grid = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
     const int64_t c = blockIdx.x, n = s.grid;
     s.first = c < n ? div_pos(total * c, n) : total;
     s.last = c < n ? div_pos(total * (c + 1), n) : total;
     if (at <= s.first && s.first < at + mine) {
         long long u = at;
-        for (int b = b0; b < b1; ++b) {
-            const long long c = p.Hkv * head_units<M, KT>(p, request_of(p, b, false));
-            if (s.first < u + c) {
-                scratch[32] = b;
-                scratch[33] = s.first - u;
-                break;
-            }
-            u += c;
+        int b = b0;
+#pragma unroll 1
+        for (; b < b1; ++b) {
+            if (b1 - b0 > 1) a = ask<M, KT>(p, b, false);
+            if (s.first < u + p.Hkv * a.units) break;
+            u += p.Hkv * a.units;
         }
+        scratch[32] = b;
+        scratch[33] = s.first - u;
+        scratch[34] = a.r.row0;
+        scratch[35] = a.r.n;
+        scratch[36] = a.r.len;
+        scratch[37] = a.units;
     }
     __syncthreads();
     s.b = static_cast<int>(scratch[32]);
     s.into = scratch[33];
+    s.a.r = Request{static_cast<int>(scratch[34]), static_cast<int>(scratch[35]), static_cast<int>(scratch[36])};
+    s.a.units = scratch[37];
     return s;
 }
 
@@ -172,31 +195,27 @@ struct Piece {
 template <int M, int KT>
 struct Walk {
     const Args& p;
-    int64_t at, last, req_first, req_units;
+    int64_t at, last, req_first, per_head;
     int b;
     Request r;
-    __device__ __forceinline__ Walk(const Args& args, const Start& s) : p(args), at(s.first), last(s.last), b(s.b) {
-        if (at < last) {
-            r = request_of(p, b, false);
-            req_first = at - s.into;
-            req_units = p.Hkv * head_units<M, KT>(p, r);
-        }
-    }
+    __device__ __forceinline__ Walk(const Args& args, const Start& s)
+        : p(args), at(s.first), last(s.last), req_first(s.first - s.into), per_head(s.a.units), b(s.b), r(s.a.r) {}
     __device__ __forceinline__ bool next(Piece& out) {
         if (at >= last) return false;
-        while (at >= req_first + req_units) {
-            req_first += req_units;
+        while (at >= req_first + p.Hkv * per_head) {
+            req_first += p.Hkv * per_head;
             if (++b >= p.B) return false;      // only where the lengths change under the call
-            r = request_of(p, b, false);
-            req_units = p.Hkv * head_units<M, KT>(p, r);
+            const Asked a = ask<M, KT>(p, b, false);
+            r = a.r;
+            per_head = a.units;
         }
-        const int64_t per_head = div_pos(req_units, p.Hkv);
         int64_t into = at - req_first;
         out.h = static_cast<int>(div_pos(into, per_head));
         into -= out.h * per_head;
         int t = 0;
         Span sp = span_of<M, KT>(p, r, 0);
         const int nt = tiles_of<M>(p, r);
+#pragma unroll 1
         while (into >= sp.units(KT) && t + 1 < nt) {
             into -= sp.units(KT);
             sp = span_of<M, KT>(p, r, ++t);
@@ -256,91 +275,39 @@ __device__ __forceinline__ bool part_done(const Args& p, const Piece& pc, const 
     return join;
 }
 
-// The elements of joined rows: a thread has kE pieces of four elements and loads them from kC
-// parts at a time, since one block reads all of it and waits for nothing but L2.
-template <typename T, int M, int kThreads, int kE, int kC>
-__device__ __forceinline__ void join_elements(const Args& p, const Piece& pc, int c0, int c1, int valid,
-                                              const float2* s_row, int tid) {
-    const float ninf = -__uint_as_float(0x7f800000u);
-    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-    const int four = p.D / 4, total = valid * four;
-    for (int e0 = tid; e0 < total; e0 += kE * kThreads) {
-        float4 o[kE];
-#pragma unroll
-        for (int k = 0; k < kE; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = c0; c <= c1; c += kC) {
-            float4 x[kC][kE];
-            float f[kC][kE];
-#pragma unroll
-            for (int i = 0; i < kC; ++i)
-#pragma unroll
-                for (int k = 0; k < kE; ++k) {
-                    const int e = e0 + k * kThreads;
-                    x[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    f[i][k] = ninf;
-                    if (c + i <= c1 && e < total) {
-                        const int64_t at = part_place(c + i, c + i == c0) * M + e / four;
-                        f[i][k] = __ldcg(ml + at).x;
-                        x[i][k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * p.D) + e % four);
-                    }
-                }
-#pragma unroll
-            for (int k = 0; k < kE; ++k) {
-                const int e = e0 + k * kThreads;
-                const float use = e < total ? s_row[e / four].x : 0.f;
-#pragma unroll
-                for (int i = 0; i < kC; ++i) {
-                    const float a = fast_exp2(f[i][k] - use);
-                    o[k].x = fmaf(x[i][k].x, a, o[k].x);
-                    o[k].y = fmaf(x[i][k].y, a, o[k].y);
-                    o[k].z = fmaf(x[i][k].z, a, o[k].z);
-                    o[k].w = fmaf(x[i][k].w, a, o[k].w);
-                }
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kE; ++k) {
-            const int e = e0 + k * kThreads;
-            if (e >= total) continue;
-            const int m = e / four, qi = pc.tile * M + m;
-            const float l = s_row[m].y, inv = l != 0.f ? 1.f / l : 0.f;
-            T* to = static_cast<T*>(p.out) + ((static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.Hq + pc.h * p.G + qi % p.G) * p.D;
-            store_four(to + (e % four) * 4, l != 0.f ? make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv)
-                                                     : make_float4(0.f, 0.f, 0.f, 0.f));
-        }
-    }
-}
-
 // Joins the parts of a segment and writes its rows: first every row's maximum and sum over the
-// parts (s_row, M entries), with as many lanes a row as there are to spare, then the elements.
+// parts (s_row, M entries), with as many lanes a row as there are to spare, then the elements,
+// four a thread from sixteen parts at a time.  The loops stay short: this code runs once a block at most, and with four pieces a thread unrolled as well it
+// took longer to fetch than to run (30 parts of 4 rows: 15,000 cycles, now 8,000).
 template <typename T, int M, int kThreads, class Sync>
 __device__ __noinline__ void join_parts(const Args& p, Piece pc, Start st, float2* s_row, int tid, Sync sync) {
     const int c0 = block_of(pc.seg_first, st.total, st.grid);
-    const int c1 = block_of(pc.seg_first + pc.units - 1, st.total, st.grid);
+    const int parts = block_of(pc.seg_first + pc.units - 1, st.total, st.grid) - c0 + 1;
     const int left = pc.r.n * p.G - pc.tile * M, valid = left < M ? left : M;
     const float ninf = -__uint_as_float(0x7f800000u);
-    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+    // part i of row m: place 2 (c0 + i), the first one's 2 c0 + 1
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + part_place(c0, false) * M;
+    const float* po = p.part_o + part_place(c0, false) * M * p.D;
     int lanes = 1;                                           // of a row: a power of two within a warp
     while (lanes < 32 && 2 * lanes * valid <= kThreads) lanes *= 2;
+#pragma unroll 1
     for (int m0 = 0; m0 < valid; m0 += kThreads / lanes) {
-        const int m = m0 + tid / lanes;
-        const bool mine = m < valid;
+        const int m = m0 + tid / lanes, own = m < valid ? parts : 0;
         float mx = ninf, l = 0.f;
-        if (mine) {
-#pragma unroll 4
-            for (int c = c0 + tid % lanes; c <= c1; c += lanes) mx = fmaxf(mx, __ldcg(ml + part_place(c, c == c0) * M + m).x);
+        auto add = [&](float m2, float l2) {
+            const float big = fmaxf(mx, m2), use = big == ninf ? 0.f : big;
+            l = l * fast_exp2(mx - use) + l2 * fast_exp2(m2 - use);
+            mx = big;
+        };
+#pragma unroll 2
+        for (int i = tid % lanes; i < own; i += lanes) {
+            const float2 x = __ldcg(ml + (i > 0 ? 2 * i : 1) * M + m);
+            add(x.x, x.y);
         }
-        for (int o = lanes / 2; o > 0; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+#pragma unroll 1
+        for (int o = lanes / 2; o > 0; o /= 2) add(__shfl_xor_sync(0xffffffffu, mx, o), __shfl_xor_sync(0xffffffffu, l, o));
         const float use = mx == ninf ? 0.f : mx;
-        if (mine) {
-#pragma unroll 4
-            for (int c = c0 + tid % lanes; c <= c1; c += lanes) {
-                const float2 x = __ldcg(ml + part_place(c, c == c0) * M + m);
-                l += x.y * fast_exp2(x.x - use);
-            }
-        }
-        for (int o = lanes / 2; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (mine && tid % lanes == 0) {
+        if (m < valid && tid % lanes == 0) {
             s_row[m] = make_float2(use, l);
             if (p.lse != nullptr) {
                 const int qi = pc.tile * M + m;
@@ -349,8 +316,40 @@ __device__ __noinline__ void join_parts(const Args& p, Piece pc, Start st, float
         }
     }
     sync();
-    if (valid * p.D / 4 <= kThreads) join_elements<T, M, kThreads, 1, 16>(p, pc, c0, c1, valid, s_row, tid);
-    else join_elements<T, M, kThreads, 4, 4>(p, pc, c0, c1, valid, s_row, tid);
+    constexpr int kC = 16;
+    const int four = p.D / 4, total = valid * four;
+#pragma unroll 1
+    for (int e = tid; e < total; e += kThreads) {
+        const int m = e / four, d = (e - m * four) * 4;
+        const float use = s_row[m].x, l = s_row[m].y, inv = l != 0.f ? 1.f / l : 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int i0 = 0; i0 < parts; i0 += kC) {
+            float4 x[kC];
+            float f[kC];
+#pragma unroll
+            for (int i = 0; i < kC; ++i) {
+                const int at = (i0 + i > 0 ? 2 * (i0 + i) : 1) * M + m;
+                f[i] = ninf;
+                x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i0 + i < parts) {
+                    f[i] = __ldcg(ml + at).x;
+                    x[i] = __ldcg(reinterpret_cast<const float4*>(po + static_cast<int64_t>(at) * p.D + d));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kC; ++i) {
+                const float a = fast_exp2(f[i] - use);
+                o.x = fmaf(x[i].x, a, o.x);
+                o.y = fmaf(x[i].y, a, o.y);
+                o.z = fmaf(x[i].z, a, o.z);
+                o.w = fmaf(x[i].w, a, o.w);
+            }
+        }
+        const int qi = pc.tile * M + m;
+        T* to = static_cast<T*>(p.out) + ((static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.Hq + pc.h * p.G + qi % p.G) * p.D;
+        store_four(to + d, l != 0.f ? make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f));
+    }
 }
 
 }  // namespace attn

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
     constexpr int kChunks = kRow / 16;                       // 16-byte chunks of a stored row
     constexpr float kShift = kFp8 ? 14.f : 0.f;              // P carries 2^kShift
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long scratch[34];
+    __shared__ long long scratch[38];
     __shared__ float s_m[kWarps][M], s_l[kWarps][M], s_qs[M];
     __shared__ float2 s_row[M];
     __shared__ int s_flag;

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     unsigned char* s_q = smem;                               // [2] tiles: [halves][128 rows][128 bytes]
     unsigned char* s_k = smem + 2 * Sh::kTile;
     unsigned char* s_v = smem + 4 * Sh::kTile;
-    __shared__ long long scratch[34];
+    __shared__ long long scratch[38];
     __shared__ __align__(8) TcBars bars;
     __shared__ uint32_t s_tmem;
     __shared__ float2 s_row[kTcM];
