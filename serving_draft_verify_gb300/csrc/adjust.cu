@@ -20,8 +20,7 @@
 // Vocabularies number frequent tokens first, so the pieces with the most set bits are the
 // first: blocks of one piece are neighbours in the launch, the first pieces start first, and
 // the light ones fill the end.
-#include "common.cuh"
-#include "host_common.h"
+#include "launch.cuh"
 
 namespace dspark {
 namespace {
@@ -126,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
     if (p.ell != nullptr) {
         const int e = p.ell[b];
         if (e < 0 || e >= p.R) {
-            if (tid == 0) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 1);
+            if (tid == 0) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 1);      // waits for the clearing too
             return;
         }
         rows = e + 1;
@@ -166,13 +165,13 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
         int t = -1;
         if (tid > 0 && p.draft != nullptr) {
             t = p.draft[static_cast<int64_t>(b) * (p.R - 1) + tid - 1];
-            if (t < 0 || t >= p.V) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 3);
+            if (t < 0 || t >= p.V) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 3);
             t = t >= v0 && t < v0 + nv ? t - v0 : -1;
         }
         if (tid > 0) s_draft[tid - 1] = t;
         if (p.mask_row != nullptr) {
             const int mr = p.mask_row[static_cast<int64_t>(b) * p.R + tid];
-            if (mr < -1 || mr >= p.n_mask) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 5);
+            if (mr < -1 || mr >= p.n_mask) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 5);
         }
     }
     __syncthreads();
@@ -181,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
     const int32_t* hist = p.history + static_cast<int64_t>(b) * p.ld_history;
     int hn = p.history_len != nullptr ? p.history_len[b] : 0, pn = p.prompt_len != nullptr ? p.prompt_len[b] : 0;
     if (hn < 0 || hn > p.ld_history || pn < 0 || pn > hn) {
-        if (tid == 0) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 2);
+        if (tid == 0) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 2);
         hn = pn = 0;
     }
     for (int i0 = tid; i0 < hn; i0 += 4 * kThreads) {
@@ -192,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
         for (int j = 0; j < 4; ++j) {
             const int i = i0 + j * kThreads, v = t[j] - v0;
             if (i >= hn) continue;
-            if (t[j] < 0 || t[j] >= p.V) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 3);
+            if (t[j] < 0 || t[j] >= p.V) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 3);
             else if (v >= 0 && v < nv) {
                 if (i < pn) atomicOr(&words[v], kPrompt);
                 else atomicAdd(&words[v], 1u);
@@ -204,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
         const int32_t* tok = p.bias_token + static_cast<int64_t>(b) * p.n_bias;
         const float* val = p.bias_value + static_cast<int64_t>(b) * p.n_bias;
         const int t = tok[i], v = t - v0;
-        if (t < -1 || t >= p.V) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 4);
+        if (t < -1 || t >= p.V) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 4);
         if (t < 0 || v < 0 || v >= nv) continue;
         bool first = true;
         for (int j = 0; j < i && first; ++j) first = tok[j] != t;
@@ -263,6 +262,7 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
             }
         }
     }
+    if (blockIdx.x == 0) head_cleared();
 }
 
 }  // namespace
@@ -299,7 +299,6 @@ extern "C" dspark_status_t dspark_adjust_logits(int B, int R, int V, dspark_dtyp
     if (a != o && a < o + bytes && o < a + bytes) return DSPARK_ERR_INVALID_ARGUMENT;
     clear_stale_error();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (clear_status(workspace, s) != DSPARK_OK) return DSPARK_ERR_CUDA;
     AdjustArgs p{R,        V,     8192,          n_bias,      n_mask,      ld_history, ld_mask,
                  logits,   ell,   history,       prompt_len,  history_len, draft,      repetition,
                  frequency, presence, bias_token, bias_value, mask_row,    mask,       out,
@@ -308,7 +307,6 @@ extern "C" dspark_status_t dspark_adjust_logits(int B, int R, int V, dspark_dtyp
         p.chunk /= 2;
     const dim3 grid(B, (V + p.chunk - 1) / p.chunk);
     const size_t smem = p.chunk * 4 + static_cast<size_t>(n_bias) * 4 + p.chunk / 4;
-    if (dt == DSPARK_BF16) adjust_logits<__nv_bfloat16><<<grid, kThreads, smem, s>>>(p);
-    else adjust_logits<float><<<grid, kThreads, smem, s>>>(p);
-    return launch_status();
+    return launch_cleared(workspace, kStatusBytes, dt == DSPARK_BF16 ? adjust_logits<__nv_bfloat16> : adjust_logits<float>,
+                          grid, kThreads, smem, s, p);
 }

@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
         if (!whole && part_done(p, pc, st, &s_flag, tid, [] { __syncthreads(); }))
             join_parts<float, M, kSimtThreads>(p, pc, st, s_row, tid, [] { __syncthreads(); });
     }
+    if (blockIdx.x == 0) head_cleared();
 }
 
 template <typename C, int kCols>
@@ -214,8 +215,7 @@ dspark_status_t launch_simt(const Args& p, cudaStream_t s) {
     const int per_sm = smem <= 52 * 1024 ? 4 : smem <= 108 * 1024 ? 2 : 1;
     const int grid = grid_for(sm_count(current_device()) * per_sm, kSimtM);
     if (grid < 1) return DSPARK_ERR_CUDA;
-    attend_simt<C, kCols><<<grid, kSimtThreads, smem, s>>>(p);
-    return launch_status();
+    return launch_cleared(p.status, kHeadBytes, attend_simt<C, kCols>, dim3(grid), kSimtThreads, smem, s, p);
 }
 template <typename C>
 dspark_status_t launch_f32(const Args& p, cudaStream_t s) {
@@ -276,8 +276,7 @@ extern "C" dspark_status_t dspark_paged_attention(
     if (workspace_bytes < dspark_paged_attention_workspace_size(D)) return DSPARK_ERR_WORKSPACE_TOO_SMALL;
     clear_stale_error();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(workspace, 0, kStatusBytes + attn::kCounterBytes, s) != cudaSuccess) return DSPARK_ERR_CUDA;
-    if (rows == 0) return DSPARK_OK;
+    if (rows == 0) return clear_status(workspace, s);
     attn::Args p{};
     p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.D = D, p.page = page, p.max_blocks = max_blocks;
     p.num_blocks = num_blocks, p.max_rows = max_rows, p.window = window, p.rows = rows, p.ld_table = ld_table;

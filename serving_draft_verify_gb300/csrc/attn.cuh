@@ -19,8 +19,7 @@
 // who came last.
 #pragma once
 
-#include "common.cuh"
-#include "host_common.h"
+#include "launch.cuh"
 
 namespace dspark {
 namespace attn {
@@ -45,6 +44,8 @@ constexpr int kMaxGrid = 1024;
 constexpr size_t kCounterBytes = kMaxGrid * 4;
 constexpr int kMaxPartRows = 40960;         // query rows of all places: 2 grid M of any launch
 
+constexpr size_t kHeadBytes = kStatusBytes + kCounterBytes;      // what starts at zero
+
 // Blocks of a launch: as many as can be resident, so that the even division is one wave.
 inline int grid_for(int resident, int M) {
     int n = resident < kMaxGrid ? resident : kMaxGrid;
@@ -55,14 +56,14 @@ struct Request {
     int row0, n, len;                 // first row, rows, keys before the step
 };
 // What the lengths say about request b; an inconsistent one has no rows.
-__device__ __forceinline__ Request request_of(const Args& p, int b, bool tell) {
+__device__ __forceinline__ Request request_of(const Args& p, int b, bool report) {
     Request r;
     r.row0 = p.row_offset[b];
     const int64_t n = static_cast<int64_t>(p.row_offset[b + 1]) - r.row0;
     r.len = p.length[b];
     const int64_t cap = static_cast<int64_t>(p.max_blocks) * p.page;
     const bool ok = n >= 0 && n <= p.max_rows && r.row0 >= 0 && r.row0 + n <= p.rows && r.len >= 0 && r.len + n <= cap;
-    if (!ok && tell) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 1);
+    if (!ok && report) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 1);
     r.n = ok ? static_cast<int>(n) : 0;
     return r;
 }
@@ -93,9 +94,9 @@ struct Asked {
     int64_t units;
 };
 template <int M, int KT>
-__device__ __noinline__ Asked ask(const Args& p, int b, bool tell) {
+__device__ __noinline__ Asked ask(const Args& p, int b, bool report) {
     Asked a;
-    a.r = request_of(p, b, tell);
+    a.r = request_of(p, b, report);
     a.units = 0;
     const int nt = tiles_of<M>(p, a.r);
 #pragma unroll 1
@@ -243,7 +244,7 @@ __device__ __forceinline__ int64_t part_place(int block, bool starts) { return 2
 __device__ __forceinline__ int page_id(const Args& p, int b, int j) {
     int id = __ldg(p.table + static_cast<int64_t>(b) * p.ld_table + j);
     if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks)) {
-        set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 2);
+        tell(p.status, DSPARK_ERR_DEVICE_CHECK, 2);
         id = 0;
     }
     return id;
@@ -268,7 +269,10 @@ __device__ __forceinline__ bool part_done(const Args& p, const Piece& pc, const 
     const int c1 = block_of(pc.seg_first + pc.units - 1, st.total, st.grid);
     __threadfence();
     sync();
-    if (tid == 0) *s_flag = atomicAdd(&p.counters[c0], 1u) == static_cast<unsigned>(c1 - c0);
+    if (tid == 0) {
+        head_cleared();
+        *s_flag = atomicAdd(&p.counters[c0], 1u) == static_cast<unsigned>(c1 - c0);
+    }
     sync();
     const bool join = *s_flag != 0;
     if (join) __threadfence();

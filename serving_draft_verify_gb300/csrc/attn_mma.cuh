@@ -517,6 +517,7 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
         if (!whole && part_done(p, pc, st, &s_flag, tid, [] { __syncthreads(); })) join_parts<__nv_bfloat16, M, kThreads>(p, pc, st, s_row, tid, [] { __syncthreads(); });
         __syncthreads();
     }
+    if (blockIdx.x == 0) head_cleared();
 }
 
 template <bool kFp8, int MT, int DT>
@@ -530,8 +531,7 @@ dspark_status_t launch_mma(const Args& p, cudaStream_t s) {
         return DSPARK_ERR_CUDA;
     const int grid = grid_for(sm_count(dev) * Sh::kPerSm, Sh::M);
     if (grid < 1) return DSPARK_ERR_CUDA;
-    attend_mma<kFp8, MT, DT><<<grid, Sh::kThreads, Sh::kSmem, s>>>(p);
-    return launch_status();
+    return launch_cleared(p.status, kHeadBytes, attend_mma<kFp8, MT, DT>, dim3(grid), Sh::kThreads, Sh::kSmem, s, p);
 }
 
 }  // namespace attn

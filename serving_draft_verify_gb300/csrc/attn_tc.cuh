@@ -99,7 +99,7 @@ __device__ __noinline__ void long_wait(uint64_t* bar, uint32_t parity, volatile 
     if (*dead) return;
     if (!mbar_wait(bar, parity)) {
         *dead = 1;
-        set_status(status, DSPARK_ERR_TIMEOUT, 1);
+        tell(status, DSPARK_ERR_TIMEOUT, 1);
     }
 }
 
@@ -479,6 +479,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, 512);
     }
+    if (blockIdx.x == 0) head_cleared();
 }
 
 // Rows of a TMA box: the largest power of two that divides the page, so that a box lies on one
@@ -517,8 +518,7 @@ dspark_status_t launch_tc(const Args& p, cudaStream_t s) {
     if (!encode_cache(&km, p.kc, p, box) || !encode_cache(&vm, p.vc, p, box)) return DSPARK_ERR_CUDA;
     const int grid = grid_for(sm_count(dev), kTcM);
     if (grid < 1) return DSPARK_ERR_CUDA;
-    attend_tc<DT><<<grid, kTcThreads, TcShape<DT>::kSmem, s>>>(p, km, vm, box);
-    return launch_status();
+    return launch_cleared(p.status, kHeadBytes, attend_tc<DT>, dim3(grid), kTcThreads, TcShape<DT>::kSmem, s, p, km, vm, box);
 }
 
 }  // namespace attn

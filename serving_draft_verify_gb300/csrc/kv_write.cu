@@ -9,8 +9,7 @@
 // before the first store, so that the arithmetic of places is done once a thread and once a row.
 #include <cuda_fp8.h>
 
-#include "common.cuh"
-#include "host_common.h"
+#include "launch.cuh"
 
 namespace dspark {
 namespace {
@@ -73,7 +72,7 @@ __global__ void __launch_bounds__(kThreads) write_kv(WriteArgs p) {
         const int64_t slot = p.slot[row0 + r];
         int64_t to = -1;
         if (slot >= p.slots) {
-            set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 1);
+            tell(p.status, DSPARK_ERR_DEVICE_CHECK, 1);
         } else if (slot >= 0) {
             const int64_t block = (slot >> 32) == 0 ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.page) : slot / p.page;
             to = (block * p.heads * p.page + (slot - block * p.page)) * p.D;
@@ -120,6 +119,7 @@ __global__ void __launch_bounds__(kThreads) write_kv(WriteArgs p) {
             }
         }
     }
+    if (blockIdx.x == 0) head_cleared();
 }
 
 }  // namespace
@@ -150,8 +150,7 @@ extern "C" dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int pag
     if (workspace_bytes < dspark_write_kv_workspace_size()) return DSPARK_ERR_WORKSPACE_TOO_SMALL;
     clear_stale_error();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (clear_status(workspace, s) != DSPARK_OK) return DSPARK_ERR_CUDA;
-    if (rows == 0) return DSPARK_OK;
+    if (rows == 0) return clear_status(workspace, s);
     WriteArgs p{};
     p.rows = rows, p.k_stride = k_stride, p.v_stride = v_stride;
     p.slots = static_cast<int64_t>(num_blocks) * page;
@@ -167,12 +166,8 @@ extern "C" dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int pag
     p.k = k, p.v = v, p.slot = slot, p.k_scale = k_scale, p.v_scale = v_scale, p.kc = k_cache, p.vc = v_cache;
     p.status = static_cast<StatusBlock*>(workspace);
     const unsigned grid = static_cast<unsigned>((rows + p.rows_per_block - 1) / p.rows_per_block);
-    if (dt == DSPARK_BF16) {
-        if (cache_dt == DSPARK_E4M3) write_kv<__nv_bfloat16, true><<<grid, kThreads, 0, s>>>(p);
-        else write_kv<__nv_bfloat16, false><<<grid, kThreads, 0, s>>>(p);
-    } else {
-        if (cache_dt == DSPARK_E4M3) write_kv<float, true><<<grid, kThreads, 0, s>>>(p);
-        else write_kv<float, false><<<grid, kThreads, 0, s>>>(p);
-    }
-    return launch_status();
+    const bool fp8 = cache_dt == DSPARK_E4M3;
+    void (*kernel)(WriteArgs) = dt == DSPARK_BF16 ? (fp8 ? write_kv<__nv_bfloat16, true> : write_kv<__nv_bfloat16, false>)
+                                                  : (fp8 ? write_kv<float, true> : write_kv<float, false>);
+    return launch_cleared(workspace, kStatusBytes, kernel, dim3(grid), kThreads, 0, s, p);
 }

@@ -14,8 +14,7 @@
 // enters it in the table; pages that go back are copied by the block that owns the
 // request's tile.  The last block to finish (a counter, nobody waits) writes the
 // per-request state, so the state may be updated in place.
-#include "common.cuh"
-#include "host_common.h"
+#include "launch.cuh"
 
 namespace dspark {
 namespace {
@@ -169,7 +168,7 @@ __global__ void __launch_bounds__(kT) plan_rows(PlanArgs p) {
     else if (T > count) why = 3;
     else if (count + R > cap) why = 1;
     else if (N > p.room) why = 4;
-    if (why != 0 && blockIdx.x == 0 && tid == 0) set_status(p.status, DSPARK_ERR_DEVICE_CHECK, why);
+    if (why != 0 && blockIdx.x == 0 && tid == 0) tell(p.status, DSPARK_ERR_DEVICE_CHECK, why);
 
     // the block's rows
     const int64_t row = r0 + tid;
@@ -195,7 +194,7 @@ __global__ void __launch_bounds__(kT) plan_rows(PlanArgs p) {
                 id = *entry;
             }
             if (id < 0 || id >= cap)
-                set_status(p.status, DSPARK_ERR_DEVICE_CHECK, 5);
+                tell(p.status, DSPARK_ERR_DEVICE_CHECK, 5);
             else
                 slot = static_cast<int64_t>(id) * p.page + off;
         }
@@ -217,7 +216,10 @@ __global__ void __launch_bounds__(kT) plan_rows(PlanArgs p) {
     if (gridDim.x > 1) {
         __threadfence();
         __syncthreads();
-        if (tid == 0) s_last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
+        if (tid == 0) {
+            head_cleared();
+            s_last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
+        }
         __syncthreads();
         if (!s_last) return;
         __threadfence();
@@ -288,8 +290,11 @@ extern "C" dspark_status_t dspark_plan_rows(int B, int page, int max_blocks, int
     const int64_t tile = small ? 256 : 1024;
     const int64_t row_tiles = (max_rows + tile - 1) / tile, req_tiles = (B + tile - 1) / tile;
     const int64_t grid = row_tiles > req_tiles ? row_tiles : req_tiles;
-    if (grid > 1 && cudaMemsetAsync(workspace, 0, kStatusBytes + 16, s) != cudaSuccess) return DSPARK_ERR_CUDA;
-    if (small) plan_rows<256><<<static_cast<unsigned>(grid), 256, 0, s>>>(p);
-    else plan_rows<1024><<<static_cast<unsigned>(grid), 1024, 0, s>>>(p);
+    if (grid > 1) {
+        if (small) return launch_cleared(workspace, kStatusBytes + 16, plan_rows<256>, dim3(static_cast<unsigned>(grid)), 256, 0, s, p);
+        return launch_cleared(workspace, kStatusBytes + 16, plan_rows<1024>, dim3(static_cast<unsigned>(grid)), 1024, 0, s, p);
+    }
+    if (small) plan_rows<256><<<1, 256, 0, s>>>(p);
+    else plan_rows<1024><<<1, 1024, 0, s>>>(p);
     return launch_status();
 }
