@@ -576,12 +576,16 @@ def _stream_of(dev, stream):
     return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
-def _opt(t, dev, shape, dtype, name):
-    """As _on, for a tensor that may be absent; returns its address."""
-    if t is None:
-        return None
-    _on(t, dev, shape, dtype, name)
-    return t.data_ptr()
+def _check_all(dev, wanted):
+    """Every (tensor, shape, type, name) as _on checks it; absent (None) ones pass.  One loop, as a
+    small call's time is its checks."""
+    for t, shape, dtype, name in wanted:
+        if t is not None and (t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
+            _on(t, dev, shape, dtype, name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _heads(t, dev, dtype, name):
@@ -596,11 +600,11 @@ def _heads(t, dev, dtype, name):
     return s[0] if n > 1 else heads * D
 
 
-def _scratch(nbytes, like, workspace, stream, *made):
-    """The workspace (allocated here if None).  Memory that this call allocated and that work on
+def _scratch(size, like, workspace, stream, *made):
+    """The workspace (allocated here, of size() bytes, if None).  Memory that this call allocated and that work on
     another stream than the current one uses is tied to that stream."""
     if workspace is None:
-        workspace = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=like.device)
+        workspace = torch.empty(max(int(size()), 256), dtype=torch.uint8, device=like.device)
         made = (*made, workspace)
     elif workspace.get_device() != like.get_device():
         raise ValueError("workspace is on another device")
@@ -626,26 +630,28 @@ def dspark_plan_rows(length, rows, held, free_state, free_ring, block_table, pag
     nb, = free_ring.shape
     width = block_table.shape[1]
     i32 = torch.int32
-    _on(length, dev, (B,), i32, "length")
-    _on(rows, dev, (B,), i32, "rows")
-    _on(held, dev, (B,), i32, "held")
-    _on(free_state, dev, (2,), i32, "free_state")
-    _on(free_ring, dev, (nb,), i32, "free_ring")
-    _on(block_table, dev, (B, width), i32, "block_table")
-    adv = _opt(advance, dev, (B,), i32, "advance")
     made = ()
     if out is None:
         new = lambda n, t=i32: torch.empty(n, dtype=t, device=length.device)  # noqa: E731
         out = dict(length=new(B), held=new(B), free_state=new(2), row_offset=new(B + 1), row_request=new(max_rows),
                    position=new(max_rows), slot=new(max_rows, torch.int64))
         made = tuple(out.values())
-    for k, n in zip(_PLAN_OUT, (B, B, 2, B + 1, max_rows, max_rows, max_rows)):
-        _on(out[k], dev, (n,), torch.int64 if k == "slot" else i32, k)
-    ws = _scratch(lib.dspark_plan_rows_workspace_size(B, max_rows), length, workspace, stream, *made)
+    o_len, o_held, o_free, o_off, o_req, o_pos, o_slot = [out[k] for k in _PLAN_OUT]
+    per, rowwise = (B,), (max_rows,)
+    _check_all(dev, ((length, per, i32, "length"), (rows, per, i32, "rows"), (held, per, i32, "held"),
+                     (advance, per, i32, "advance"), (free_state, (2,), i32, "free_state"),
+                     (free_ring, (nb,), i32, "free_ring"), (block_table, (B, width), i32, "block_table"),
+                     (o_len, per, i32, "out length"), (o_held, per, i32, "out held"),
+                     (o_free, (2,), i32, "out free_state"), (o_off, (B + 1,), i32, "row_offset"),
+                     (o_req, rowwise, i32, "row_request"), (o_pos, rowwise, i32, "position"),
+                     (o_slot, rowwise, torch.int64, "slot")))
+    ws = _scratch(lambda: lib.dspark_plan_rows_workspace_size(B, max_rows), length, workspace, stream, *made)
     _check("dspark_plan_rows",
-           lib.dspark_plan_rows(B, page, width, nb, max_rows, length.data_ptr(), adv, rows.data_ptr(), held.data_ptr(),
-                                free_state.data_ptr(), free_ring.data_ptr(), block_table.data_ptr(), width,
-                                *[out[k].data_ptr() for k in _PLAN_OUT], ws.data_ptr(), _nbytes(ws), _stream_of(dev, stream)))
+           lib.dspark_plan_rows(B, page, width, nb, max_rows, length.data_ptr(), _addr(advance), rows.data_ptr(),
+                                held.data_ptr(), free_state.data_ptr(), free_ring.data_ptr(), block_table.data_ptr(),
+                                width, o_len.data_ptr(), o_held.data_ptr(), o_free.data_ptr(), o_off.data_ptr(),
+                                o_req.data_ptr(), o_pos.data_ptr(), o_slot.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                _stream_of(dev, stream)))
     return out
 
 
@@ -655,13 +661,12 @@ def _cache_code(k_cache, v_cache, k_scale, v_scale, dev, dtype):
     if len(shape) != 4:
         raise ValueError("caches have the shape [num_blocks, Hkv, page, D]")
     t = k_cache.dtype
-    _on(k_cache, dev, shape, t, "k_cache")
-    _on(v_cache, dev, shape, t, "v_cache")
+    _check_all(dev, ((k_cache, shape, t, "k_cache"), (v_cache, shape, t, "v_cache")))
     if t is torch.float8_e4m3fn:
         if k_scale is None or v_scale is None:
             raise ValueError("8-bit caches need k_scale and v_scale")
-        return DSPARK_E4M3, _opt(k_scale, dev, (shape[1],), torch.float32, "k_scale"), \
-            _opt(v_scale, dev, (shape[1],), torch.float32, "v_scale")
+        _check_all(dev, ((k_scale, shape[1:2], torch.float32, "k_scale"), (v_scale, shape[1:2], torch.float32, "v_scale")))
+        return DSPARK_E4M3, k_scale.data_ptr(), v_scale.data_ptr()
     if t is not dtype:
         raise TypeError(f"caches of {t} for rows of {dtype}")
     if k_scale is not None or v_scale is not None:
@@ -683,10 +688,10 @@ def dspark_write_kv(k, v, slot, k_cache, v_cache, k_scale=None, v_scale=None, wo
         raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} for caches of {Hkv} heads of {D}")
     _on(slot, dev, (n,), torch.int64, "slot")
     code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, k.dtype)
-    ws = _scratch(lib.dspark_write_kv_workspace_size(), k_cache, workspace, stream)
+    ws = _scratch(lib.dspark_write_kv_workspace_size, k_cache, workspace, stream)
     _check("dspark_write_kv",
            lib.dspark_write_kv(n, Hkv, D, page, nb, dt, code, k.data_ptr(), ks, v.data_ptr(), vs, slot.data_ptr(), ksc,
-                               vsc, k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(), _nbytes(ws),
+                               vsc, k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(), ws.nbytes,
                                _stream_of(dev, stream)))
 
 
@@ -705,24 +710,23 @@ def dspark_paged_attention(q, row_offset, length, block_table, k_cache, v_cache,
     if qd != D:
         raise ValueError(f"q has heads of {qd}, the caches of {D}")
     width = block_table.shape[1]
-    _on(row_offset, dev, (B + 1,), torch.int32, "row_offset")
-    _on(length, dev, (B,), torch.int32, "length")
-    _on(block_table, dev, (B, width), torch.int32, "block_table")
     code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, q.dtype)
     made = ()
     if out is None:
         out = dict(out=torch.empty((n, Hq, D), dtype=q.dtype, device=q.device),
                    lse=torch.empty((n, Hq), dtype=torch.float32, device=q.device))
         made = tuple(out.values())
-    _on(out["out"], dev, (n, Hq, D), q.dtype, "out")
-    lse = _opt(out.get("lse"), dev, (n, Hq), torch.float32, "lse")
-    ws = _scratch(lib.dspark_paged_attention_workspace_size(D), q, workspace, stream, *made)
+    o, lse = out["out"], out.get("lse")
+    _check_all(dev, ((row_offset, (B + 1,), torch.int32, "row_offset"), (length, (B,), torch.int32, "length"),
+                     (block_table, (B, width), torch.int32, "block_table"), (o, (n, Hq, D), q.dtype, "out"),
+                     (lse, (n, Hq), torch.float32, "lse")))
+    ws = _scratch(lambda: lib.dspark_paged_attention_workspace_size(D), q, workspace, stream, *made)
     _check("dspark_paged_attention",
            lib.dspark_paged_attention(B, n, max_rows, Hq, Hkv, D, page, width, nb, _dtype_code(q), code, q.data_ptr(),
                                       qs, row_offset.data_ptr(), length.data_ptr(), block_table.data_ptr(), width,
                                       k_cache.data_ptr(), v_cache.data_ptr(), ksc, vsc,
                                       D ** -0.5 if scale is None else float(scale), int(window),
-                                      out["out"].data_ptr(), lse, ws.data_ptr(), _nbytes(ws), _stream_of(dev, stream)))
+                                      o.data_ptr(), _addr(lse), ws.data_ptr(), ws.nbytes, _stream_of(dev, stream)))
     return out
 
 
@@ -738,7 +742,6 @@ def dspark_adjust_logits(logits, history=None, prompt_len=None, history_len=None
     dev = _device_of(logits, "logits")
     B, R, V = logits.shape
     i32, f32 = torch.int32, torch.float32
-    _on(logits, dev, (B, R, V), logits.dtype, "logits")
     width = history.shape[1] if history is not None else 0
     n_bias = bias_token.shape[1] if bias_token is not None else 0
     n_mask, words = mask.shape if mask is not None else (0, (V + 31) // 32)
@@ -746,16 +749,19 @@ def dspark_adjust_logits(logits, history=None, prompt_len=None, history_len=None
     if out is None:
         out = torch.empty_like(logits)
         made = (out,)
-    _on(out, dev, (B, R, V), logits.dtype, "out")
-    ws = _scratch(lib.dspark_adjust_logits_workspace_size(), logits, workspace, stream, *made)
+    per, whole = (B,), (B, R, V)
+    _check_all(dev, ((logits, whole, logits.dtype, "logits"), (out, whole, logits.dtype, "out"), (ell, per, i32, "ell"),
+                     (history, (B, width), i32, "history"), (prompt_len, per, i32, "prompt_len"),
+                     (history_len, per, i32, "history_len"), (draft, (B, R - 1), i32, "draft"),
+                     (repetition, per, f32, "repetition"), (frequency, per, f32, "frequency"),
+                     (presence, per, f32, "presence"), (bias_token, (B, n_bias), i32, "bias_token"),
+                     (bias_value, (B, n_bias), f32, "bias_value"), (mask_row, (B, R), i32, "mask_row"),
+                     (mask, (n_mask, words), i32, "mask")))
+    ws = _scratch(lib.dspark_adjust_logits_workspace_size, logits, workspace, stream, *made)
     _check("dspark_adjust_logits",
-           lib.dspark_adjust_logits(
-               B, R, V, _dtype_code(logits), logits.data_ptr(), _opt(ell, dev, (B,), i32, "ell"),
-               _opt(history, dev, (B, width), i32, "history"), width, _opt(prompt_len, dev, (B,), i32, "prompt_len"),
-               _opt(history_len, dev, (B,), i32, "history_len"), _opt(draft, dev, (B, R - 1), i32, "draft"),
-               _opt(repetition, dev, (B,), f32, "repetition"), _opt(frequency, dev, (B,), f32, "frequency"),
-               _opt(presence, dev, (B,), f32, "presence"), _opt(bias_token, dev, (B, n_bias), i32, "bias_token"),
-               _opt(bias_value, dev, (B, n_bias), f32, "bias_value"), n_bias,
-               _opt(mask_row, dev, (B, R), i32, "mask_row"), _opt(mask, dev, (n_mask, words), i32, "mask"), n_mask,
-               words, out.data_ptr(), ws.data_ptr(), _nbytes(ws), _stream_of(dev, stream)))
+           lib.dspark_adjust_logits(B, R, V, _dtype_code(logits), logits.data_ptr(), _addr(ell), _addr(history), width,
+                                    _addr(prompt_len), _addr(history_len), _addr(draft), _addr(repetition),
+                                    _addr(frequency), _addr(presence), _addr(bias_token), _addr(bias_value), n_bias,
+                                    _addr(mask_row), _addr(mask), n_mask, words, out.data_ptr(), ws.data_ptr(),
+                                    ws.nbytes, _stream_of(dev, stream)))
     return out

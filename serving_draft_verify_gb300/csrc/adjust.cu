@@ -121,11 +121,18 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
     const int b = blockIdx.x, tid = threadIdx.x;
     const int v0 = blockIdx.y * p.chunk;
     const int nv = min(p.chunk, p.V - v0);
+    // Every block of a request sees the same errors; the first piece's tells them.  Where there is one
+    // request that block clears the status as well, and nothing has to come before.
+    StatusBlock* status = blockIdx.y == 0 ? p.status : nullptr;
+    if (gridDim.x == 1 && blockIdx.y == 0) {
+        if (tid < 4) reinterpret_cast<uint32_t*>(status)[tid] = 0;
+        __syncthreads();
+    }
     int rows = p.R;
     if (p.ell != nullptr) {
         const int e = p.ell[b];
         if (e < 0 || e >= p.R) {
-            if (tid == 0) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 1);      // waits for the clearing too
+            if (tid == 0) tell(status, DSPARK_ERR_DEVICE_CHECK, 1);        // waits for the clearing too
             return;
         }
         rows = e + 1;
@@ -165,13 +172,13 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
         int t = -1;
         if (tid > 0 && p.draft != nullptr) {
             t = p.draft[static_cast<int64_t>(b) * (p.R - 1) + tid - 1];
-            if (t < 0 || t >= p.V) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 3);
+            if (t < 0 || t >= p.V) tell(status, DSPARK_ERR_DEVICE_CHECK, 3);
             t = t >= v0 && t < v0 + nv ? t - v0 : -1;
         }
         if (tid > 0) s_draft[tid - 1] = t;
         if (p.mask_row != nullptr) {
             const int mr = p.mask_row[static_cast<int64_t>(b) * p.R + tid];
-            if (mr < -1 || mr >= p.n_mask) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 5);
+            if (mr < -1 || mr >= p.n_mask) tell(status, DSPARK_ERR_DEVICE_CHECK, 5);
         }
     }
     __syncthreads();
@@ -180,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
     const int32_t* hist = p.history + static_cast<int64_t>(b) * p.ld_history;
     int hn = p.history_len != nullptr ? p.history_len[b] : 0, pn = p.prompt_len != nullptr ? p.prompt_len[b] : 0;
     if (hn < 0 || hn > p.ld_history || pn < 0 || pn > hn) {
-        if (tid == 0) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 2);
+        if (tid == 0) tell(status, DSPARK_ERR_DEVICE_CHECK, 2);
         hn = pn = 0;
     }
     for (int i0 = tid; i0 < hn; i0 += 4 * kThreads) {
@@ -191,7 +198,7 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
         for (int j = 0; j < 4; ++j) {
             const int i = i0 + j * kThreads, v = t[j] - v0;
             if (i >= hn) continue;
-            if (t[j] < 0 || t[j] >= p.V) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 3);
+            if (t[j] < 0 || t[j] >= p.V) tell(status, DSPARK_ERR_DEVICE_CHECK, 3);
             else if (v >= 0 && v < nv) {
                 if (i < pn) atomicOr(&words[v], kPrompt);
                 else atomicAdd(&words[v], 1u);
@@ -203,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
         const int32_t* tok = p.bias_token + static_cast<int64_t>(b) * p.n_bias;
         const float* val = p.bias_value + static_cast<int64_t>(b) * p.n_bias;
         const int t = tok[i], v = t - v0;
-        if (t < -1 || t >= p.V) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 4);
+        if (t < -1 || t >= p.V) tell(status, DSPARK_ERR_DEVICE_CHECK, 4);
         if (t < 0 || v < 0 || v >= nv) continue;
         bool first = true;
         for (int j = 0; j < i && first; ++j) first = tok[j] != t;
@@ -307,6 +314,11 @@ extern "C" dspark_status_t dspark_adjust_logits(int B, int R, int V, dspark_dtyp
         p.chunk /= 2;
     const dim3 grid(B, (V + p.chunk - 1) / p.chunk);
     const size_t smem = p.chunk * 4 + static_cast<size_t>(n_bias) * 4 + p.chunk / 4;
+    if (B == 1) {
+        if (dt == DSPARK_BF16) adjust_logits<__nv_bfloat16><<<grid, kThreads, smem, s>>>(p);
+        else adjust_logits<float><<<grid, kThreads, smem, s>>>(p);
+        return launch_status();
+    }
     return launch_cleared(workspace, kStatusBytes, dt == DSPARK_BF16 ? adjust_logits<__nv_bfloat16> : adjust_logits<float>,
                           grid, kThreads, smem, s, p);
 }

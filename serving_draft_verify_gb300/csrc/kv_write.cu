@@ -14,7 +14,6 @@
 namespace dspark {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kItems = 4;
 constexpr int kMaxRows = 256;                   // of a block
 
@@ -62,12 +61,16 @@ struct Eight<float> {
     }
 };
 
-template <typename T, bool kFp8>
+template <typename T, bool kFp8, int kThreads>
 __global__ void __launch_bounds__(kThreads) write_kv(WriteArgs p) {
     __shared__ int64_t s_to[kMaxRows];          // a row's first element of head 0 in the cache, -1: none
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_block;
     const int64_t left = p.rows - row0;
     const int n = left < p.rows_per_block ? static_cast<int>(left) : p.rows_per_block;
+    if (gridDim.x == 1) {                       // alone: no clearing came before
+        if (threadIdx.x < 4) reinterpret_cast<uint32_t*>(p.status)[threadIdx.x] = 0;
+        __syncthreads();
+    }
     for (int r = threadIdx.x; r < n; r += kThreads) {
         const int64_t slot = p.slot[row0 + r];
         int64_t to = -1;
@@ -156,18 +159,32 @@ extern "C" dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int pag
     p.slots = static_cast<int64_t>(num_blocks) * page;
     p.heads = Hkv, p.D = D, p.page = page;
     p.parts = static_cast<int>(width / 8);
+    // Few rows (64 KB, what 1024 threads move in one go) are one block, which clears the status itself.
+    // Otherwise four rows a thread, and fewer where the rows would not fill the GPU.
+    const bool one = rows <= kMaxRows && rows * 2 * p.parts <= 1024 * kItems;
+    const int threads = one ? 1024 : 256;
     p.lanes = 1;
-    while (p.lanes < kThreads && p.lanes < 2 * p.parts) p.lanes *= 2;
-    // four rows a thread, and as many rows as threads at most; fewer where the rows would not fill the GPU
-    const int groups = kThreads / p.lanes;
-    p.rows_per_block = groups * kItems < kMaxRows ? groups * kItems : kMaxRows;
-    while (p.rows_per_block > 1 && (rows + p.rows_per_block - 1) / p.rows_per_block < 2 * sm_count(current_device()))
+    while (p.lanes < threads && p.lanes < 2 * p.parts) p.lanes *= 2;
+    const int groups = threads / p.lanes;
+    p.rows_per_block = one ? kMaxRows : groups * kItems < kMaxRows ? groups * kItems : kMaxRows;
+    while (!one && p.rows_per_block > 1 && (rows + p.rows_per_block - 1) / p.rows_per_block < 2 * sm_count(current_device()))
         p.rows_per_block /= 2;
     p.k = k, p.v = v, p.slot = slot, p.k_scale = k_scale, p.v_scale = v_scale, p.kc = k_cache, p.vc = v_cache;
     p.status = static_cast<StatusBlock*>(workspace);
     const unsigned grid = static_cast<unsigned>((rows + p.rows_per_block - 1) / p.rows_per_block);
-    const bool fp8 = cache_dt == DSPARK_E4M3;
-    void (*kernel)(WriteArgs) = dt == DSPARK_BF16 ? (fp8 ? write_kv<__nv_bfloat16, true> : write_kv<__nv_bfloat16, false>)
-                                                  : (fp8 ? write_kv<float, true> : write_kv<float, false>);
-    return launch_cleared(workspace, kStatusBytes, kernel, dim3(grid), kThreads, 0, s, p);
+    const bool bf16 = dt == DSPARK_BF16, fp8 = cache_dt == DSPARK_E4M3;
+    if (grid == 1) {
+        // (also rows that are one block of the other kind: it clears the status as well)
+        if (one) {
+            if (bf16) (fp8 ? write_kv<__nv_bfloat16, true, 1024> : write_kv<__nv_bfloat16, false, 1024>)<<<1, 1024, 0, s>>>(p);
+            else (fp8 ? write_kv<float, true, 1024> : write_kv<float, false, 1024>)<<<1, 1024, 0, s>>>(p);
+        } else {
+            if (bf16) (fp8 ? write_kv<__nv_bfloat16, true, 256> : write_kv<__nv_bfloat16, false, 256>)<<<1, 256, 0, s>>>(p);
+            else (fp8 ? write_kv<float, true, 256> : write_kv<float, false, 256>)<<<1, 256, 0, s>>>(p);
+        }
+        return launch_status();
+    }
+    void (*kernel)(WriteArgs) = bf16 ? (fp8 ? write_kv<__nv_bfloat16, true, 256> : write_kv<__nv_bfloat16, false, 256>)
+                                     : (fp8 ? write_kv<float, true, 256> : write_kv<float, false, 256>);
+    return launch_cleared(workspace, kStatusBytes, kernel, dim3(grid), 256, 0, s, p);
 }
