@@ -68,6 +68,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// The bits of x, or 0: a choice among registers (an index would move the array to memory).
+__device__ __forceinline__ uint32_t bits_if(bool yes, float x) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tselp.b32 %0, %1, 0, p;\n\t}"
+                 : "=r"(r)
+                 : "r"(__float_as_uint(x)), "r"(yes ? 1u : 0u));
+    return r;
+}
 // 16 bytes to shared memory, or 16 zero bytes; wait until at most n groups are outstanding.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
@@ -185,7 +193,8 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
         for (int s = 0; s < kStages - 1; ++s) load(s, find_rows(s));
         rows = find_rows(kStages - 1);
 
-        // ---- the queries, 16-bit, swizzled; rows past the last are zero
+        // ---- the queries, 16-bit, swizzled; rows past the last are zero.  A negative scale's sign is theirs.
+        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
         for (int e = tid; e < M * (DT / 8); e += kThreads) {
             const int m = e / (DT / 8), c = e - m * (DT / 8);
             uint4 x = make_uint4(0, 0, 0, 0);
@@ -195,6 +204,7 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
                                                          (static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.q_stride +
                                                          static_cast<int64_t>(pc.h * p.G + qi % p.G) * p.D + c * 8));
             }
+            x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
             *reinterpret_cast<uint4*>(s_q + chunk_at<2 * DT>(m, c)) = x;
         }
         if constexpr (kFp8) {
@@ -226,7 +236,7 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
                     if (i < DT / 2)
                         *reinterpret_cast<uint32_t*>(s_q + chunk_at<2 * DT>(m, to >> 2) + (to & 3) * 4) = own[k];
                 }
-                if (lane == 0) s_qs[m] = scalbnf(p.scale_log2 * p.k_scale[pc.h], -ex);
+                if (lane == 0) s_qs[m] = scalbnf(fabsf(p.scale_log2) * p.k_scale[pc.h], -ex);
             }
         }
         __syncthreads();
@@ -246,7 +256,7 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                sc[mt][r] = kFp8 ? s_qs[mt * 16 + g + 8 * r] : p.scale_log2;
+                sc[mt][r] = fmaxf(kFp8 ? s_qs[mt * 16 + g + 8 * r] : fabsf(p.scale_log2), 1.17549435e-38f);   // -inf times it is -inf
                 mx[mt][r] = ninf;
                 l[mt][r] = 0.f;
             }
@@ -295,7 +305,8 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
                     }
                 }
             }
-            // ---- scores in units of log 2; hidden keys at -inf
+            // ---- scores; hidden keys at -inf.  Their scale (to units of log 2) is not negative, so the
+            // largest is found before scaling and the scaling is part of the exponent's addition.
             const bool masked = first + KS - 1 > pos_lo || (p.window > 0 && first <= pos_hi - p.window);
             uint32_t hidden[MT][2];                          // bit 2n + i: key 8n + 2t + i is hidden from row g (+ 8)
             float nm[MT][2];
@@ -312,22 +323,21 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const int key = first + 8 * n + 2 * t + i;
-                                if (key > pos || key >= pc.span.hi || (p.window > 0 && key <= pos - p.window))
+                                if (key > pos || key >= pc.span.hi || (p.window > 0 && key <= pos - p.window)) {
                                     hidden[mt][r] |= 1u << (2 * n + i);
+                                    sv[mt][n][2 * r + i] = ninf;
+                                }
                             }
                     }
-                    float mm = mx[mt][r];
+                    float m2[2] = {ninf, ninf};
 #pragma unroll
                     for (int n = 0; n < 2 * kSub; ++n)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            float& x = sv[mt][n][2 * r + i];
-                            x *= sc[mt][r];
-                            if (hidden[mt][r] >> (2 * n + i) & 1u) x = ninf;
-                            mm = fmaxf(mm, x);
-                        }
+                        for (int i = 0; i < 2; ++i) m2[i] = fmaxf(m2[i], sv[mt][n][2 * r + i]);
+                    float mm = fmaxf(m2[0], m2[1]);
                     mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 1));
                     mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 2));
+                    mm = fmaxf(mx[mt][r], mm == ninf ? ninf : mm * sc[mt][r]);
                     nm[mt][r] = mm;
                     moved |= mm != mx[mt][r];
                 }
@@ -355,7 +365,8 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
                     const float use = (mx[mt][r] == ninf ? 0.f : mx[mt][r]) - kShift;
 #pragma unroll
                     for (int n = 0; n < 2 * kSub; ++n) {
-                        const float e0 = fast_exp2(sv[mt][n][2 * r] - use), e1 = fast_exp2(sv[mt][n][2 * r + 1] - use);
+                        const float e0 = fast_exp2(fmaf(sv[mt][n][2 * r], sc[mt][r], -use));
+                        const float e1 = fast_exp2(fmaf(sv[mt][n][2 * r + 1], sc[mt][r], -use));
                         l[mt][r] += e0 + e1;
                         sv[mt][n][2 * r] = e0;
                         sv[mt][n][2 * r + 1] = e1;
@@ -385,11 +396,10 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
                             bool in[2];
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
-                                float mine = 0.f;
+                                uint32_t mine = 0;
 #pragma unroll
-                                for (int n = 0; n < 2 * kSub; ++n)
-                                    if (n == (j >> 3)) mine = (j & 1) ? sv[mt][n][2 * r + 1] : sv[mt][n][2 * r];
-                                e[r] = __shfl_sync(0xffffffffu, mine, src);
+                                for (int k = 0; k < 4 * kSub; ++k) mine |= bits_if(k == 2 * (j >> 3) + (j & 1), sv[mt][k >> 1][2 * r + (k & 1)]);
+                                e[r] = __uint_as_float(__shfl_sync(0xffffffffu, mine, src));
                                 in[r] = !(__shfl_sync(0xffffffffu, hidden[mt][r], src) >> (2 * (j >> 3) + (j & 1)) & 1u);
                             }
 #pragma unroll
