@@ -10,6 +10,11 @@ namespace dspark {
 namespace attn {
 namespace {
 
+// 64 requests of up to 4000 keys, 32 heads on 8: 9 rows a request (36 query rows) 196 us on the warp-level
+// instructions and 203 on tcgen05, 12 rows 206 and 205, 17 rows 307 and 240.  Short caches favour the
+// former longer (256 requests of up to 500 keys, 17 rows: 285 and 311), but the lengths are on the device.
+constexpr int kWide = 48;
+
 // ------------------------------------------------------------ float32 rows ---
 // Sixteen query rows (four a warp) over 32 keys a unit, float32 throughout: a lane is a key
 // for the scores and has pairs of columns of the values.  The next unit's keys and values are copied
@@ -224,17 +229,15 @@ dspark_status_t launch_f32(const Args& p, cudaStream_t s) {
     return launch_simt<C, 8>(p, s);
 }
 
-// bf16 rows: the instructions take 16 query rows at a time, two such tiles where a request has
-// more than 16 (and the output rows still fit the registers).
+// bf16 rows: sixteen query rows at a time on the warp-level instructions, or 128 on tcgen05 where a
+// request may have more rows than kWide.
 template <bool kFp8>
 dspark_status_t launch_bf16(const Args& p, cudaStream_t s) {
-    const int64_t most = static_cast<int64_t>(p.max_rows) * p.G;
     if constexpr (!kFp8)
-        if (most > 32 && tc_fits(p)) return p.D <= 64 ? launch_tc<64>(p, s) : launch_tc<128>(p, s);
-    const bool two = most > 16;
-    if (p.D <= 64) return two ? launch_mma<kFp8, 2, 64>(p, s) : launch_mma<kFp8, 1, 64>(p, s);
-    if (p.D <= 128) return two ? launch_mma<kFp8, 2, 128>(p, s) : launch_mma<kFp8, 1, 128>(p, s);
-    return launch_mma<kFp8, 1, 256>(p, s);
+        if (static_cast<int64_t>(p.max_rows) * p.G > kWide && tc_fits(p)) return p.D <= 64 ? launch_tc<64>(p, s) : launch_tc<128>(p, s);
+    if (p.D <= 64) return launch_mma<kFp8, 64>(p, s);
+    if (p.D <= 128) return launch_mma<kFp8, 128>(p, s);
+    return launch_mma<kFp8, 256>(p, s);
 }
 
 }  // namespace

@@ -1,5 +1,6 @@
-// Attention of few query rows a request (plain decoding, short drafts): up to 32 query
-// rows of a key head at a time on the warp-level tensor instructions.
+// Attention of few query rows a request (plain decoding, short drafts): 16 query rows of a
+// key head at a time on the warp-level tensor instructions (tiles of 32 rows held twice the
+// registers and were slower than two tiles of 16 wherever both were measured).
 //
 // Bound by the cache's bytes, so the kernel is built around keeping loads in flight.
 // The four warps of a block share nothing in the loop: warp w takes keys w KS .. w KS + KS - 1
@@ -86,10 +87,10 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
 
-template <bool kFp8, int MT, int DT>
+template <bool kFp8, int DT>
 struct MmaShape {
     static constexpr int kThreads = 128, kWarps = 4;
-    static constexpr int M = 16 * MT;
+    static constexpr int M = 16;
     static constexpr int KS = kFp8 ? 32 : 16;               // keys of a warp's step
     static constexpr int KT = KS * kWarps;                  // keys of a unit
     static constexpr int kRow = kFp8 ? DT : 2 * DT;         // bytes of a stored row
@@ -100,7 +101,7 @@ struct MmaShape {
     static constexpr int kQBytes = M * DT * 2;
     static constexpr int kSmem = kWarps * kWarpBytes + kQBytes;
     static constexpr int kPerSm = kSmem > 113 * 1024 ? 1 : 2;
-    static constexpr bool kQReg = MT * DT <= 128;
+    static constexpr bool kQReg = DT <= 128;
     static_assert(M * kLd * 4 <= kWarpBytes, "a warp's result fits its ring");
 };
 
@@ -129,9 +130,9 @@ __device__ __forceinline__ uint32_t without_odd(uint32_t u) {
     return u;
 }
 
-template <bool kFp8, int MT, int DT>
-__global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_mma(const __grid_constant__ Args p) {
-    using Sh = MmaShape<kFp8, MT, DT>;
+template <bool kFp8, int DT>
+__global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(const __grid_constant__ Args p) {
+    using Sh = MmaShape<kFp8, DT>;
     constexpr int M = Sh::M, KS = Sh::KS, KT = Sh::KT, kRow = Sh::kRow, kStages = Sh::kStages;
     constexpr int kThreads = Sh::kThreads, kWarps = Sh::kWarps;
     constexpr int kSub = KS / 16;                            // 16-key blocks of a step
@@ -188,29 +189,30 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
             }
             copy_commit();
         };
-        int64_t rows = 0;
-#pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) load(s, find_rows(s));
-        rows = find_rows(kStages - 1);
-
-        // ---- the queries, 16-bit, swizzled; rows past the last are zero.  A negative scale's sign is theirs.
-        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+        // The queries first (16-bit, swizzled, rows past the last zero): they arrive with the first keys.
         for (int e = tid; e < M * (DT / 8); e += kThreads) {
-            const int m = e / (DT / 8), c = e - m * (DT / 8);
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (m < valid && c * 8 < p.D) {
-                const int qi = pc.tile * M + m;
-                x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                         (static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.q_stride +
-                                                         static_cast<int64_t>(pc.h * p.G + qi % p.G) * p.D + c * 8));
-            }
-            x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-            *reinterpret_cast<uint4*>(s_q + chunk_at<2 * DT>(m, c)) = x;
+            const int m = e / (DT / 8), c = e - m * (DT / 8), qi = pc.tile * M + m;
+            const bool real = m < valid && c * 8 < p.D;
+            const int64_t at = real ? (static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.q_stride +
+                                          static_cast<int64_t>(pc.h * p.G + qi % p.G) * p.D + c * 8
+                                    : 0;
+            copy16(q_a + chunk_at<2 * DT>(m, c), static_cast<const __nv_bfloat16*>(p.q) + at, real);
+        }
+        int64_t ahead[kStages];
+#pragma unroll
+        for (int s = 0; s < kStages; ++s) ahead[s] = find_rows(s);
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) load(s, ahead[s]);
+        int64_t rows = ahead[kStages - 1];
+        copy_wait<kStages - 2>();
+        __syncthreads();
+        if (p.scale_log2 < 0.f) {                            // a negative scale's sign is the queries'
+            for (int e = tid; e < M * DT / 2; e += kThreads) reinterpret_cast<uint32_t*>(s_q)[e] ^= 0x80008000u;
+            __syncthreads();
         }
         if constexpr (kFp8) {
             // rows to f16: the largest element comes to 2^10 .. 2^11, and the columns of every
             // 16 into the order in which ldmatrix hands out the keys' bytes
-            __syncthreads();
             for (int m = w; m < M; m += kWarps) {
                 float big = 0.f;
                 for (int i = lane; i < DT / 2; i += 32) {
@@ -238,33 +240,28 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
                 }
                 if (lane == 0) s_qs[m] = scalbnf(fabsf(p.scale_log2) * p.k_scale[pc.h], -ex);
             }
+            __syncthreads();
         }
-        __syncthreads();
-        uint32_t qf[Sh::kQReg ? MT : 1][Sh::kQReg ? DT / 16 : 1][4];
-        auto load_q = [&](int mt, int ks, uint32_t* a) {
-            ldsm4(a, q_a + chunk_at<2 * DT>(mt * 16 + (lane & 15), 2 * ks + (lane >> 4)));
+        uint32_t qf[Sh::kQReg ? DT / 16 : 1][4];
+        auto load_q = [&](int ks, uint32_t* a) {
+            ldsm4(a, q_a + chunk_at<2 * DT>(lane & 15, 2 * ks + (lane >> 4)));
         };
         if constexpr (Sh::kQReg) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int ks = 0; ks < DT / 16; ++ks) load_q(mt, ks, qf[mt][ks]);
+            for (int ks = 0; ks < DT / 16; ++ks) load_q(ks, qf[ks]);
         }
-        float sc[MT][2], mx[MT][2], l[MT][2];
-        float o[MT][DT / 8][4];
+        float sc[2], mx[2], l[2];
+        float o[DT / 8][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                sc[mt][r] = fmaxf(kFp8 ? s_qs[mt * 16 + g + 8 * r] : fabsf(p.scale_log2), 1.17549435e-38f);   // -inf times it is -inf
-                mx[mt][r] = ninf;
-                l[mt][r] = 0.f;
-            }
-#pragma unroll
-            for (int n = 0; n < DT / 8; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[mt][n][i] = 0.f;
+        for (int r = 0; r < 2; ++r) {
+            sc[r] = fmaxf(kFp8 ? s_qs[g + 8 * r] : fabsf(p.scale_log2), 1.17549435e-38f);   // -inf times it is -inf
+            mx[r] = ninf;
+            l[r] = 0.f;
         }
+#pragma unroll
+        for (int n = 0; n < DT / 8; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
 
         const int pos_lo = pc.r.len + pc.tile * M / p.G, pos_hi = pc.span.hi - 1;   // the tile's first and last position
         for (int s = 0; s < steps; ++s) {
@@ -277,109 +274,98 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
             const uint32_t k_a = ring_a + (s % kStages) * Sh::kStage, v_a = k_a + KS * kRow;
 
             // ---- S = Q K^T
-            float sv[MT][2 * kSub][4];
+            float sv[2 * kSub][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int n = 0; n < 2 * kSub; ++n)
 #pragma unroll
-                for (int n = 0; n < 2 * kSub; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sv[mt][n][i] = 0.f;
+                for (int i = 0; i < 4; ++i) sv[n][i] = 0.f;
 #pragma unroll
             for (int ks = 0; ks < DT / 16; ++ks) {
                 uint32_t kf[4];
                 if constexpr (kFp8) ldsm4(kf, k_a + chunk_at<kRow>(lane, ks));
                 else ldsm4(kf, k_a + chunk_at<kRow>((lane & 7) + (lane >> 4) * 8, 2 * ks + ((lane >> 3) & 1)));
+                uint32_t qa[4];
+                const uint32_t* a = qa;
+                if constexpr (Sh::kQReg) a = qf[ks];
+                else load_q(ks, qa);
+                if constexpr (kFp8) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    uint32_t qa[4];
-                    const uint32_t* a = qa;
-                    if constexpr (Sh::kQReg) a = qf[mt][ks];
-                    else load_q(mt, ks, qa);
-                    if constexpr (kFp8) {
-#pragma unroll
-                        for (int n = 0; n < 4; ++n)
-                            mma16816<true>(sv[mt][n], a, e4m3x2_f16x2(kf[n]), e4m3x2_f16x2(kf[n] >> 16));
-                    } else {
-                        mma16816<false>(sv[mt][0], a, kf[0], kf[1]);
-                        mma16816<false>(sv[mt][1], a, kf[2], kf[3]);
-                    }
+                    for (int n = 0; n < 4; ++n)
+                        mma16816<true>(sv[n], a, e4m3x2_f16x2(kf[n]), e4m3x2_f16x2(kf[n] >> 16));
+                } else {
+                    mma16816<false>(sv[0], a, kf[0], kf[1]);
+                    mma16816<false>(sv[1], a, kf[2], kf[3]);
                 }
             }
             // ---- scores; hidden keys at -inf.  Their scale (to units of log 2) is not negative, so the
             // largest is found before scaling and the scaling is part of the exponent's addition.
             const bool masked = first + KS - 1 > pos_lo || (p.window > 0 && first <= pos_hi - p.window);
-            uint32_t hidden[MT][2];                          // bit 2n + i: key 8n + 2t + i is hidden from row g (+ 8)
-            float nm[MT][2];
+            uint32_t hidden[2];                          // bit 2n + i: key 8n + 2t + i is hidden from row g (+ 8)
+            float nm[2];
             bool moved = false;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    hidden[mt][r] = 0;
-                    if (masked) {
-                        const int pos = pc.r.len + (pc.tile * M + mt * 16 + g + 8 * r) / p.G;
-#pragma unroll
-                        for (int n = 0; n < 2 * kSub; ++n)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int key = first + 8 * n + 2 * t + i;
-                                if (key > pos || key >= pc.span.hi || (p.window > 0 && key <= pos - p.window)) {
-                                    hidden[mt][r] |= 1u << (2 * n + i);
-                                    sv[mt][n][2 * r + i] = ninf;
-                                }
-                            }
-                    }
-                    float m2[2] = {ninf, ninf};
+            for (int r = 0; r < 2; ++r) {
+                hidden[r] = 0;
+                if (masked) {
+                    const int pos = pc.r.len + (pc.tile * M + g + 8 * r) / p.G;
 #pragma unroll
                     for (int n = 0; n < 2 * kSub; ++n)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) m2[i] = fmaxf(m2[i], sv[mt][n][2 * r + i]);
-                    float mm = fmaxf(m2[0], m2[1]);
-                    mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 1));
-                    mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 2));
-                    mm = fmaxf(mx[mt][r], mm == ninf ? ninf : mm * sc[mt][r]);
-                    nm[mt][r] = mm;
-                    moved |= mm != mx[mt][r];
+                        for (int i = 0; i < 2; ++i) {
+                            const int key = first + 8 * n + 2 * t + i;
+                            if (key > pos || key >= pc.span.hi || (p.window > 0 && key <= pos - p.window)) {
+                                hidden[r] |= 1u << (2 * n + i);
+                                sv[n][2 * r + i] = ninf;
+                            }
+                        }
                 }
+                float m2[2] = {ninf, ninf};
+#pragma unroll
+                for (int n = 0; n < 2 * kSub; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) m2[i] = fmaxf(m2[i], sv[n][2 * r + i]);
+                float mm = fmaxf(m2[0], m2[1]);
+                mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 1));
+                mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 2));
+                mm = fmaxf(mx[r], mm == ninf ? ninf : mm * sc[r]);
+                nm[r] = mm;
+                moved |= mm != mx[r];
+            }
             if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float a = fast_exp2(mx[mt][r] - (nm[mt][r] == ninf ? 0.f : nm[mt][r]));
-                        l[mt][r] *= a;
-                        mx[mt][r] = nm[mt][r];
-#pragma unroll
-                        for (int n = 0; n < DT / 8; ++n) {
-                            o[mt][n][2 * r] *= a;
-                            o[mt][n][2 * r + 1] *= a;
-                        }
-                    }
-            }
-            // ---- P
-            uint32_t ph[MT][kSub][4], pl[kFp8 ? 1 : MT][kSub][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float use = (mx[mt][r] == ninf ? 0.f : mx[mt][r]) - kShift;
+                    const float a = fast_exp2(mx[r] - (nm[r] == ninf ? 0.f : nm[r]));
+                    l[r] *= a;
+                    mx[r] = nm[r];
 #pragma unroll
-                    for (int n = 0; n < 2 * kSub; ++n) {
-                        const float e0 = fast_exp2(fmaf(sv[mt][n][2 * r], sc[mt][r], -use));
-                        const float e1 = fast_exp2(fmaf(sv[mt][n][2 * r + 1], sc[mt][r], -use));
-                        l[mt][r] += e0 + e1;
-                        sv[mt][n][2 * r] = e0;
-                        sv[mt][n][2 * r + 1] = e1;
-                        const int at = (n & 1) * 2 + r;
-                        if constexpr (kFp8) {
-                            ph[mt][n >> 1][at] = pack_f16(e0, e1);
-                        } else {
-                            const uint32_t h = pack_bf16(e0, e1);
-                            ph[mt][n >> 1][at] = h;
-                            pl[mt][n >> 1][at] = pack_bf16(e0 - bf16lo(h), e1 - bf16hi(h));
-                        }
+                    for (int n = 0; n < DT / 8; ++n) {
+                        o[n][2 * r] *= a;
+                        o[n][2 * r + 1] *= a;
                     }
                 }
+            }
+            // ---- P
+            uint32_t ph[kSub][4], pl[kSub][4];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float use = (mx[r] == ninf ? 0.f : mx[r]) - kShift;
+#pragma unroll
+                for (int n = 0; n < 2 * kSub; ++n) {
+                    const float e0 = fast_exp2(fmaf(sv[n][2 * r], sc[r], -use));
+                    const float e1 = fast_exp2(fmaf(sv[n][2 * r + 1], sc[r], -use));
+                    l[r] += e0 + e1;
+                    sv[n][2 * r] = e0;
+                    sv[n][2 * r + 1] = e1;
+                    const int at = (n & 1) * 2 + r;
+                    if constexpr (kFp8) {
+                        ph[n >> 1][at] = pack_f16(e0, e1);
+                    } else {
+                        const uint32_t h = pack_bf16(e0, e1);
+                        ph[n >> 1][at] = h;
+                        pl[n >> 1][at] = pack_bf16(e0 - bf16lo(h), e1 - bf16hi(h));
+                    }
+                }
+            }
             // ---- O += P V.  A hidden key's P is 0, which keeps its value out as long as that is
             // finite.  Steps with hidden keys look: values that are not finite are added here, to
             // the rows that see them, and become 0 for the product.
@@ -390,31 +376,28 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
                 if (__any_sync(0xffffffffu, odd)) {
                     for (int j = 0; j < KS; ++j) {
                         const int src = g * 4 + ((j & 7) >> 1);
+                        float e[2];
+                        bool in[2];
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            float e[2];
-                            bool in[2];
+                        for (int r = 0; r < 2; ++r) {
+                            uint32_t mine = 0;
 #pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                uint32_t mine = 0;
+                            for (int k = 0; k < 4 * kSub; ++k) mine |= bits_if(k == 2 * (j >> 3) + (j & 1), sv[k >> 1][2 * r + (k & 1)]);
+                            e[r] = __uint_as_float(__shfl_sync(0xffffffffu, mine, src));
+                            in[r] = !(__shfl_sync(0xffffffffu, hidden[r], src) >> (2 * (j >> 3) + (j & 1)) & 1u);
+                        }
 #pragma unroll
-                                for (int k = 0; k < 4 * kSub; ++k) mine |= bits_if(k == 2 * (j >> 3) + (j & 1), sv[mt][k >> 1][2 * r + (k & 1)]);
-                                e[r] = __uint_as_float(__shfl_sync(0xffffffffu, mine, src));
-                                in[r] = !(__shfl_sync(0xffffffffu, hidden[mt][r], src) >> (2 * (j >> 3) + (j & 1)) & 1u);
-                            }
+                        for (int n = 0; n < DT / 8; ++n) {
 #pragma unroll
-                            for (int n = 0; n < DT / 8; ++n) {
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    // column of accumulator i of tile n, as the products below leave it
-                                    const int d = kFp8 ? (n >> 1) * 16 + 4 * t + 2 * i + (n & 1) : n * 8 + 2 * t + i;
-                                    const unsigned char* at = vb + chunk_at<kRow>(j, d * esize / 16) + d * esize % 16;
-                                    const uint32_t bits = kFp8 ? *at : *reinterpret_cast<const uint16_t*>(at);
-                                    if (any_odd<kFp8>(bits)) {
-                                        const float v = kFp8 ? __uint_as_float(0x7fffffffu) : bf16lo(bits);
-                                        if (in[0]) o[mt][n][i] = fmaf(e[0], v, o[mt][n][i]);
-                                        if (in[1]) o[mt][n][2 + i] = fmaf(e[1], v, o[mt][n][2 + i]);
-                                    }
+                            for (int i = 0; i < 2; ++i) {
+                                // column of accumulator i of tile n, as the products below leave it
+                                const int d = kFp8 ? (n >> 1) * 16 + 4 * t + 2 * i + (n & 1) : n * 8 + 2 * t + i;
+                                const unsigned char* at = vb + chunk_at<kRow>(j, d * esize / 16) + d * esize % 16;
+                                const uint32_t bits = kFp8 ? *at : *reinterpret_cast<const uint16_t*>(at);
+                                if (any_odd<kFp8>(bits)) {
+                                    const float v = kFp8 ? __uint_as_float(0x7fffffffu) : bf16lo(bits);
+                                    if (in[0]) o[n][i] = fmaf(e[0], v, o[n][i]);
+                                    if (in[1]) o[n][2 + i] = fmaf(e[1], v, o[n][2 + i]);
                                 }
                             }
                         }
@@ -440,25 +423,20 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
                         od[i] = e4m3x2_f16x2(x >> 16);
                     }
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int b = 0; b < kSub; ++b) {
-                            mma16816<true>(o[mt][2 * c], ph[mt][b], ev[2 * b], ev[2 * b + 1]);
-                            mma16816<true>(o[mt][2 * c + 1], ph[mt][b], od[2 * b], od[2 * b + 1]);
-                        }
+                    for (int b = 0; b < kSub; ++b) {
+                        mma16816<true>(o[2 * c], ph[b], ev[2 * b], ev[2 * b + 1]);
+                        mma16816<true>(o[2 * c + 1], ph[b], od[2 * b], od[2 * b + 1]);
+                    }
                 }
             } else {
 #pragma unroll
                 for (int c = 0; c < DT / 8; c += 2) {
                     uint32_t vf[4];
                     ldsm4_t(vf, v_a + chunk_at<kRow>(lane & 15, c + (lane >> 4)));
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        mma16816<false>(o[mt][c], ph[mt][0], vf[0], vf[1]);
-                        mma16816<false>(o[mt][c + 1], ph[mt][0], vf[2], vf[3]);
-                        mma16816<false>(o[mt][c], pl[mt][0], vf[0], vf[1]);
-                        mma16816<false>(o[mt][c + 1], pl[mt][0], vf[2], vf[3]);
-                    }
+                    mma16816<false>(o[c], ph[0], vf[0], vf[1]);
+                    mma16816<false>(o[c + 1], ph[0], vf[2], vf[3]);
+                    mma16816<false>(o[c], pl[0], vf[0], vf[1]);
+                    mma16816<false>(o[c + 1], pl[0], vf[2], vf[3]);
                 }
             }
         }
@@ -468,80 +446,93 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, MT, DT>::kPerSm)) attend_
         // ---- the four warps' results join
         float* mine = reinterpret_cast<float*>(ring);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int r = 0; r < 2; ++r) {
+            float sum = l[r];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            const int m = g + 8 * r;
+            if (t == 0) {
+                s_m[w][m] = mx[r];
+                s_l[w][m] = sum;
+            }
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float sum = l[mt][r];
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                const int m = mt * 16 + g + 8 * r;
-                if (t == 0) {
-                    s_m[w][m] = mx[mt][r];
-                    s_l[w][m] = sum;
-                }
-#pragma unroll
-                for (int n = 0; n < DT / 8; ++n) {
-                    if constexpr (kFp8) {
-                        if ((n & 1) == 0)
-                            *reinterpret_cast<float4*>(mine + m * Sh::kLd + n * 8 + 4 * t) =
-                                make_float4(o[mt][n][2 * r], o[mt][n + 1][2 * r], o[mt][n][2 * r + 1], o[mt][n + 1][2 * r + 1]);
-                    } else {
-                        *reinterpret_cast<float2*>(mine + m * Sh::kLd + n * 8 + 2 * t) =
-                            make_float2(o[mt][n][2 * r], o[mt][n][2 * r + 1]);
-                    }
+            for (int n = 0; n < DT / 8; ++n) {
+                if constexpr (kFp8) {
+                    if ((n & 1) == 0)
+                        *reinterpret_cast<float4*>(mine + m * Sh::kLd + n * 8 + 4 * t) =
+                            make_float4(o[n][2 * r], o[n + 1][2 * r], o[n][2 * r + 1], o[n + 1][2 * r + 1]);
+                } else {
+                    *reinterpret_cast<float2*>(mine + m * Sh::kLd + n * 8 + 2 * t) =
+                        make_float2(o[n][2 * r], o[n][2 * r + 1]);
                 }
             }
         }
         __syncthreads();
-        const float vs = kFp8 ? p.v_scale[pc.h] : 1.f;
         const bool whole = pc.whole();
-        const int64_t place = part_place(blockIdx.x, pc.u0 == 0) * M;
-        const int pairs = p.D / 2;
-        for (int e = tid; e < valid * pairs; e += kThreads) {
-            const int m = e / pairs, d = (e - m * pairs) * 2;
-            float big = ninf, sum = 0.f, x = 0.f, y = 0.f;
+        if (tid < M) {
+            // a row's maximum and sum, and each warp's factor in its output (the values' scale and, where
+            // this is the whole, the sum with it)
+            float big = ninf, sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) big = fmaxf(big, s_m[i][m]);
-            const float use = big == ninf ? 0.f : big;
+            for (int i = 0; i < kWarps; ++i) big = fmaxf(big, s_m[i][tid]);
+            const float use = big == ninf ? 0.f : big, vs = kFp8 ? p.v_scale[pc.h] : 1.f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) sum += s_l[i][tid] * fast_exp2(s_m[i][tid] - use);
+            const float f = !whole ? vs : sum != 0.f ? vs / sum : 0.f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) s_m[i][tid] = f * fast_exp2(s_m[i][tid] - use);
+            if (tid < valid) {
+                if (!whole) {
+                    reinterpret_cast<float2*>(p.part_ml)[part_place(blockIdx.x, pc.u0 == 0) * M + tid] = make_float2(big - kShift, sum);
+                } else if (p.lse != nullptr) {
+                    const int qi = pc.tile * M + tid;
+                    p.lse[(static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.Hq + pc.h * p.G + qi % p.G] = lse_of(big - kShift, sum);
+                }
+            }
+        }
+        __syncthreads();
+        const int four = p.D / 4;
+        float* part = p.part_o + part_place(blockIdx.x, pc.u0 == 0) * M * p.D;
+#pragma unroll 2
+        for (int e = tid; e < valid * four; e += kThreads) {
+            const int m = e / four, d = (e - m * four) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) {
-                const float f = fast_exp2(s_m[i][m] - use);
-                const float2 v = *reinterpret_cast<const float2*>(smem + i * Sh::kWarpBytes + (m * Sh::kLd + d) * 4);
-                sum += s_l[i][m] * f;
-                x = fmaf(v.x, f, x);
-                y = fmaf(v.y, f, y);
+                const float f = s_m[i][m];
+                const float4 v = *reinterpret_cast<const float4*>(smem + i * Sh::kWarpBytes + (m * Sh::kLd + d) * 4);
+                x.x = fmaf(v.x, f, x.x);
+                x.y = fmaf(v.y, f, x.y);
+                x.z = fmaf(v.z, f, x.z);
+                x.w = fmaf(v.w, f, x.w);
             }
             if (whole) {
                 const int qi = pc.tile * M + m, head = pc.h * p.G + qi % p.G;
                 const int64_t row = static_cast<int64_t>(pc.r.row0) + qi / p.G;
-                const float inv = sum != 0.f ? vs / sum : 0.f;
-                *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + (row * p.Hq + head) * p.D + d) =
-                    sum != 0.f ? pack_bf16(x * inv, y * inv) : 0u;
-                if (d == 0 && p.lse != nullptr) p.lse[row * p.Hq + head] = lse_of(big - kShift, sum);
+                store_four(static_cast<__nv_bfloat16*>(p.out) + (row * p.Hq + head) * p.D + d, x);
             } else {
-                const int64_t at = place + m;
-                *reinterpret_cast<float2*>(p.part_o + at * p.D + d) = make_float2(x * vs, y * vs);
-                if (d == 0) reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(big - kShift, sum);
+                store_four(part + m * p.D + d, x);
             }
         }
-        if (!whole && part_done(p, pc, st, &s_flag, tid, [] { __syncthreads(); })) join_parts<__nv_bfloat16, M, kThreads>(p, pc, st, s_row, tid, [] { __syncthreads(); });
+        if (!whole && part_done(p, pc, st, &s_flag, tid, [] { __syncthreads(); })) 
+            join_parts<__nv_bfloat16, M, kThreads>(p, pc, st, s_row, tid, [] { __syncthreads(); });
         __syncthreads();
     }
     if (blockIdx.x == 0) head_cleared();
 }
 
-template <bool kFp8, int MT, int DT>
+template <bool kFp8, int DT>
 dspark_status_t launch_mma(const Args& p, cudaStream_t s) {
-    using Sh = MmaShape<kFp8, MT, DT>;
+    using Sh = MmaShape<kFp8, DT>;
     static OncePerDevice once;
     const int dev = current_device();
     if (once.run(dev, [] {
-            return cudaFuncSetAttribute(attend_mma<kFp8, MT, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+            return cudaFuncSetAttribute(attend_mma<kFp8, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
         }) != cudaSuccess)
         return DSPARK_ERR_CUDA;
     const int grid = grid_for(sm_count(dev) * Sh::kPerSm, Sh::M);
     if (grid < 1) return DSPARK_ERR_CUDA;
-    return launch_cleared(p.status, kHeadBytes, attend_mma<kFp8, MT, DT>, dim3(grid), Sh::kThreads, Sh::kSmem, s, p);
+    return launch_cleared(p.status, kHeadBytes, attend_mma<kFp8, DT>, dim3(grid), Sh::kThreads, Sh::kSmem, s, p);
 }
 
 }  // namespace attn
