@@ -220,14 +220,16 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
                     big = fmaxf(big, fmaxf(fabsf(bf16lo(u)), fabsf(bf16hi(u))));
                 }
                 big = warp_max(big);
-                int ex = 0;
-                if (big > 0.f && big < __uint_as_float(0x7f800000u)) ex = 10 - ilogbf(big);
+                // 2^up and 2^-up by their exponent bits (up stays where both are normal numbers)
+                int up = 0;
+                if (big > 0.f && big < __uint_as_float(0x7f800000u)) up = min(10 - (static_cast<int>(__float_as_uint(big) >> 23) - 127), 126);
+                const float grow = __uint_as_float(static_cast<uint32_t>(127 + up) << 23), back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
                 uint32_t own[DT / 64 > 0 ? (DT + 63) / 64 : 1];
 #pragma unroll
                 for (int k = 0; k < (DT + 63) / 64; ++k) {
                     const int i = lane + 32 * k;             // pair i: columns 2i, 2i + 1
                     const uint32_t u = i < DT / 2 ? *reinterpret_cast<const uint32_t*>(s_q + chunk_at<2 * DT>(m, i >> 2) + (i & 3) * 4) : 0u;
-                    own[k] = pack_f16(scalbnf(bf16lo(u), ex), scalbnf(bf16hi(u), ex));
+                    own[k] = pack_f16(bf16lo(u) * grow, bf16hi(u) * grow);
                 }
                 __syncwarp();
 #pragma unroll
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
                     if (i < DT / 2)
                         *reinterpret_cast<uint32_t*>(s_q + chunk_at<2 * DT>(m, to >> 2) + (to & 3) * 4) = own[k];
                 }
-                if (lane == 0) s_qs[m] = scalbnf(fabsf(p.scale_log2) * p.k_scale[pc.h], -ex);
+                if (lane == 0) s_qs[m] = fabsf(p.scale_log2) * p.k_scale[pc.h] * back;
             }
             __syncthreads();
         }
