@@ -7,6 +7,8 @@
 // Bound by memory: each element is read once and written once.  A thread has one piece of eight
 // elements of a row (key or value, head, place) and moves it for four rows at a time, all loads
 // before the first store, so that the arithmetic of places is done once a thread and once a row.
+// 16384 rows of 8 heads of 128: bf16 24 us (134 MB, 5.6 TB/s), to 8 bits 25 us (100 MB); with two
+// rows at a time 37 and 33 us, with eight 24 and 27, with blocks of 256 threads 28 to 8 bits.
 #include <cuda_fp8.h>
 
 #include "launch.cuh"
@@ -169,7 +171,7 @@ extern "C" dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int pag
     // Few rows (64 KB, what 1024 threads move in one go) are one block, which clears the status itself.
     // Otherwise four rows a thread, and fewer where the rows would not fill the GPU.
     const bool one = rows <= kMaxRows && rows * 2 * p.parts <= 1024 * kItems;
-    const int threads = one ? 1024 : 256;
+    const int threads = one ? 1024 : 128;
     p.lanes = 1;
     while (p.lanes < threads && p.lanes < 2 * p.parts) p.lanes *= 2;
     const int groups = threads / p.lanes;
@@ -186,12 +188,12 @@ extern "C" dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int pag
             if (bf16) (fp8 ? write_kv<__nv_bfloat16, true, 1024> : write_kv<__nv_bfloat16, false, 1024>)<<<1, 1024, 0, s>>>(p);
             else (fp8 ? write_kv<float, true, 1024> : write_kv<float, false, 1024>)<<<1, 1024, 0, s>>>(p);
         } else {
-            if (bf16) (fp8 ? write_kv<__nv_bfloat16, true, 256> : write_kv<__nv_bfloat16, false, 256>)<<<1, 256, 0, s>>>(p);
-            else (fp8 ? write_kv<float, true, 256> : write_kv<float, false, 256>)<<<1, 256, 0, s>>>(p);
+            if (bf16) (fp8 ? write_kv<__nv_bfloat16, true, 128> : write_kv<__nv_bfloat16, false, 128>)<<<1, 128, 0, s>>>(p);
+            else (fp8 ? write_kv<float, true, 128> : write_kv<float, false, 128>)<<<1, 128, 0, s>>>(p);
         }
         return launch_status();
     }
-    void (*kernel)(WriteArgs) = bf16 ? (fp8 ? write_kv<__nv_bfloat16, true, 256> : write_kv<__nv_bfloat16, false, 256>)
-                                     : (fp8 ? write_kv<float, true, 256> : write_kv<float, false, 256>);
-    return launch_cleared(workspace, kStatusBytes, kernel, dim3(grid), 256, 0, s, p);
+    void (*kernel)(WriteArgs) = bf16 ? (fp8 ? write_kv<__nv_bfloat16, true, 128> : write_kv<__nv_bfloat16, false, 128>)
+                                     : (fp8 ? write_kv<float, true, 128> : write_kv<float, false, 128>);
+    return launch_cleared(workspace, kStatusBytes, kernel, dim3(grid), 128, 0, s, p);
 }
