@@ -318,6 +318,38 @@ def test_hidden_keys_may_hold_anything(dsv, dtype, rows, Hq, D):
     assert torch.isnan(got["out"][rows - 1]).all() and torch.isnan(got["lse"][rows - 1]).all()
 
 
+@pytest.mark.parametrize("rows,Hq,D", [(4, 8, 64), (3, 32, 128), (17, 32, 128)])
+def test_hidden_keys_of_an_8_bit_cache(dsv, rows, Hq, D):
+    c = _attend_case(12, [(37, rows), (64, rows)], Hq, 4, D, 16, "bf16", "e4m3", 0)
+    want, _ = _run_attend(dsv, c)
+    nan = torch.tensor(0x7F, dtype=torch.uint8, device="cuda")
+    for b, last in enumerate([37 + rows - 1, 64 + rows - 1]):
+        blk = c["block_table"][b, last // 16]
+        c["k_cache"].view(torch.uint8)[blk, :, last % 16] = nan
+        c["v_cache"].view(torch.uint8)[blk, :, last % 16] = nan
+    got, _ = _run_attend(dsv, c)
+    keep = [i for i in range(2 * rows) if i % rows != rows - 1]
+    assert torch.equal(got["out"][keep], want["out"][keep]) and torch.equal(got["lse"][keep], want["lse"][keep])
+    assert torch.isnan(got["out"][rows - 1]).all()
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS, ids=["-".join(k) for k in KINDS])
+@pytest.mark.parametrize("scale", [-0.25, 0.0, 1.5])
+def test_attention_scales(dsv, dtype, cache, scale):
+    c = _attend_case(17, [(70, 4), (3, 1), (0, 17)], 16, 4, 64, 16, dtype, cache, 40)
+    out, code = _run_attend(dsv, c, scale=scale)
+    assert code[0] == 0
+    _check_attend(out, _oracle(c, scale), dtype, 64)
+
+
+@pytest.mark.parametrize("page", [3, 12, 16])
+def test_attention_of_many_rows_on_any_page(dsv, page):
+    c = _attend_case(18, [(150, 30), (0, 20), (301, 7)], 8, 2, 128, page, "bf16", "bf16", 0)
+    out, code = _run_attend(dsv, c)
+    assert code[0] == 0
+    _check_attend(out, _oracle(c), "bf16", 128)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_extreme_scores(dsv, dtype):
     """Scores of the type's range, and keys that score -inf."""
