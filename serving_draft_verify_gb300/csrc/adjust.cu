@@ -55,7 +55,10 @@ struct Rules {
     const float* bias;
     __device__ __forceinline__ float operator()(float x, uint32_t w) const {
         const uint32_t n = w & kCountMask;
-        if ((w & (kPrompt | kCountMask)) != 0) x = x > 0.f ? __fdiv_rn(x, rho) : x * rho;
+        if ((w & (kPrompt | kCountMask)) != 0) {
+            if (x > 0.f) x = __fdiv_rn(x, rho);
+            else x *= rho;
+        }
         if (n != 0) {
             x = __fsub_rn(x, __fmul_rn(f, static_cast<float>(n)));
             x -= p;
@@ -167,8 +170,8 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
             }
         }
     };
-    Batch now, then;
-    load(then, 0, tid);
+    Batch one, two;                                         // by turns
+    load(one, 0, tid);
     for (int i = tid; i < p.chunk / 4; i += kThreads) reinterpret_cast<uint4*>(words)[i] = make_uint4(0, 0, 0, 0);
     if (tid < rows) {
         // the draft token that the row's count gains
@@ -253,9 +256,19 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
     }
     __syncthreads();
 
-    for (int k = 0; k < rows; ++k) {
-        if (k > 0) {
-            const int t = s_draft[k - 1];
+    // A batch's work, once the next one's loads are on their way; false after the last.
+    int k = 0, i0 = tid;
+    auto work = [&](Batch& now, Batch& then) -> bool {
+        const int at = i0, row = k;
+        i0 += kUnroll * kThreads;
+        if (i0 - tid >= nvec) {
+            i0 = tid;
+            ++k;
+            if (k < rows) next_mask = mask_of(k);
+        }
+        if (k < rows) load(then, k, i0);
+        if (at == tid && row > 0) {
+            const int t = s_draft[row - 1];
             if (t >= 0) {
                 __syncthreads();                            // the row before has been done with the old count
                 if (tid == 0) {
@@ -265,27 +278,22 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(AdjustArgs p) {
                 __syncthreads();
             }
         }
-        uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (static_cast<int64_t>(b) * p.R + k) * p.V + v0);
-        for (int i0 = tid; i0 < nvec + tid; i0 += kUnroll * kThreads) {
-            now = then;
-            if (i0 - tid + kUnroll * kThreads < nvec) {
-                load(then, k, i0 + kUnroll * kThreads);
-            } else if (k + 1 < rows) {
-                next_mask = mask_of(k + 1);
-                load(then, k + 1, tid);
-            }
+        uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (static_cast<int64_t>(b) * p.R + row) * p.V + v0);
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int i = i0 + u * kThreads;
-                if (i >= nvec) continue;
-                for (uint32_t set = flags[i]; set != 0; set &= set - 1) {
-                    const int j = __ffs(set) - 1;
-                    Row<T>::put(now.x[u], j, rules(Row<T>::get(now.x[u], j), words[i * kVec + j]));
-                }
-                if (now.masked) Row<T>::mask(now.x[u], now.keep[u]);
-                __stcs(out + i, now.x[u]);
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = at + u * kThreads;
+            if (i >= nvec) continue;
+            // what the mask hides needs no rules
+            for (uint32_t set = flags[i] & now.keep[u]; set != 0; set &= set - 1) {
+                const int j = __ffs(set) - 1;
+                Row<T>::put(now.x[u], j, rules(Row<T>::get(now.x[u], j), words[i * kVec + j]));
             }
+            if (now.masked) Row<T>::mask(now.x[u], now.keep[u]);
+            __stcs(out + i, now.x[u]);
         }
+        return k < rows;
+    };
+    while (work(one, two) && work(two, one)) {
     }
     if (blockIdx.x == 0) head_cleared();
 }
