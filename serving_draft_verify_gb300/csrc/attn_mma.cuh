@@ -81,6 +81,9 @@ __device__ __forceinline__ uint32_t bits_if(bool yes, float x) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async16_at(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int n>
 __device__ __forceinline__ void copy_wait() {
@@ -152,6 +155,7 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
     const int esize = kFp8 ? 1 : 2;
     const int real_chunks = p.D * esize / 16;
     const bool whole_pages = p.page % KS == 0;               // a step's keys lie on one page
+    const bool adjacent = whole_pages && p.D == DT;          // and fill the stored rows
 
     const Start st = find_start<M, KT, kThreads>(p, scratch);
     Walk<M, KT> walk(p, st);
@@ -176,15 +180,29 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
                 const uint32_t to = ring_a + (s % kStages) * Sh::kStage;
                 const char* kc = static_cast<const char*>(p.kc);
                 const char* vc = static_cast<const char*>(p.vc);
+                if (adjacent && first + KS <= pc.span.hi) {
+                    // the step's rows are one run of bytes: 16 a lane, 512 on each time
+                    const int64_t at = rows * kRow + lane * 16;
+                    kc += at;
+                    vc += at;
 #pragma unroll
-                for (int i = 0; i < KS * kChunks / 32; ++i) {
-                    const int e = lane + 32 * i, r = e / kChunks, c = e % kChunks;
-                    const int64_t row = whole_pages ? rows + r : __shfl_sync(0xffffffffu, rows, r);
-                    const bool real = first + r < pc.span.hi && c < real_chunks;
-                    const int64_t at = real ? row * (p.D * esize) + c * 16 : 0;
-                    const uint32_t d = to + chunk_at<kRow>(r, c);
-                    copy16(d, kc + at, real);
-                    copy16(d + KS * kRow, vc + at, real);
+                    for (int i = 0; i < KS * kChunks / 32; ++i) {
+                        const int e = lane + 32 * i;
+                        const uint32_t d = to + chunk_at<kRow>(e / kChunks, e % kChunks);
+                        cp_async16_at(d, kc + 512 * i);
+                        cp_async16_at(d + KS * kRow, vc + 512 * i);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < KS * kChunks / 32; ++i) {
+                        const int e = lane + 32 * i, r = e / kChunks, c = e % kChunks;
+                        const int64_t row = whole_pages ? rows + r : __shfl_sync(0xffffffffu, rows, r);
+                        const bool real = first + r < pc.span.hi && c < real_chunks;
+                        const int64_t at = real ? row * (p.D * esize) + c * 16 : 0;
+                        const uint32_t d = to + chunk_at<kRow>(r, c);
+                        copy16(d, kc + at, real);
+                        copy16(d + KS * kRow, vc + at, real);
+                    }
                 }
             }
             copy_commit();
