@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
     const uint32_t q_a = smem_u32(s_q);
     const int esize = kFp8 ? 1 : 2;
     const int real_chunks = p.D * esize / 16;
-    const bool whole_pages = p.page % KS == 0;               // a step's keys lie on one page
+    const bool whole_pages = p.page % 16 == 0;               // 16 keys (a step's or half of it) lie on one page
     const bool adjacent = whole_pages && p.D == DT;          // and fill the stored rows
 
     const Start st = find_start<M, KT, kThreads>(p, scratch);
@@ -166,10 +166,10 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
         // ---- the first keys and values are on their way before anything else
         const int steps = pc.u1 - pc.u0;
         const int key0 = pc.span.lo + pc.u0 * KT + w * KS;   // this warp's first key; then every KT
-        // Where the keys of step s lie: the row (of D elements) of lane's key, or of the
-        // step's first key where a page holds the whole step.
+        // Where the keys of step s lie: the row (of D elements) of lane's key, or of the first of
+        // its 16 where a page holds them.
         auto find_rows = [&](int s) -> int64_t {
-            const int key = key0 + s * KT + (whole_pages ? 0 : lane);
+            const int key = key0 + s * KT + (whole_pages ? lane & (KS - 16) : lane);
             if (s >= steps || key >= pc.span.hi || (!whole_pages && lane >= KS)) return 0;
             const int blk = key / p.page;
             return (static_cast<int64_t>(page_id(p, pc.b, blk)) * p.Hkv + pc.h) * p.page + (key - blk * p.page);
@@ -180,23 +180,29 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
                 const uint32_t to = ring_a + (s % kStages) * Sh::kStage;
                 const char* kc = static_cast<const char*>(p.kc);
                 const char* vc = static_cast<const char*>(p.vc);
-                if (adjacent && first + KS <= pc.span.hi) {
-                    // the step's rows are one run of bytes: 16 a lane, 512 on each time
-                    const int64_t at = rows * kRow + lane * 16;
-                    kc += at;
-                    vc += at;
+                int64_t run[kSub];                           // the first rows of the step's sixteens
 #pragma unroll
-                    for (int i = 0; i < KS * kChunks / 32; ++i) {
-                        const int e = lane + 32 * i;
-                        const uint32_t d = to + chunk_at<kRow>(e / kChunks, e % kChunks);
-                        cp_async16_at(d, kc + 512 * i);
-                        cp_async16_at(d + KS * kRow, vc + 512 * i);
+                for (int b = 0; b < kSub; ++b) run[b] = kSub == 1 ? rows : __shfl_sync(0xffffffffu, rows, 16 * b);
+                if (adjacent && first + KS <= pc.span.hi) {
+                    // sixteen rows are one run of bytes: 16 a lane, 512 on each time
+                    constexpr int kIn = 16 * kChunks / 32;
+#pragma unroll
+                    for (int b = 0; b < kSub; ++b) {
+                        const int64_t at = run[b] * kRow + lane * 16;
+#pragma unroll
+                        for (int i = 0; i < kIn; ++i) {
+                            const int e = lane + 32 * (kIn * b + i);
+                            const uint32_t d = to + chunk_at<kRow>(e / kChunks, e % kChunks);
+                            cp_async16_at(d, kc + at + 512 * i);
+                            cp_async16_at(d + KS * kRow, vc + at + 512 * i);
+                        }
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < KS * kChunks / 32; ++i) {
                         const int e = lane + 32 * i, r = e / kChunks, c = e % kChunks;
-                        const int64_t row = whole_pages ? rows + r : __shfl_sync(0xffffffffu, rows, r);
+                        const int64_t mine = __shfl_sync(0xffffffffu, rows, whole_pages ? r & (KS - 16) : r);
+                        const int64_t row = whole_pages ? mine + (r & 15) : mine;
                         const bool real = first + r < pc.span.hi && c < real_chunks;
                         const int64_t at = real ? row * (p.D * esize) + c * 16 : 0;
                         const uint32_t d = to + chunk_at<kRow>(r, c);
