@@ -2,6 +2,8 @@
 // attn.cuh has the mathematics, the division of the work and the joining.
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "attn.cuh"
 #include "attn_mma.cuh"
 #include "attn_tc.cuh"
@@ -16,7 +18,7 @@ namespace {
 constexpr int kWide = 48;
 
 // ------------------------------------------------------------ float32 rows ---
-// Sixteen query rows (four a warp) over 32 keys a unit, float32 throughout: a lane is a key
+// Sixteen query rows (up to four a warp) over 32 keys a unit, float32 throughout: a lane is a key
 // for the scores and has pairs of columns of the values.  The next unit's keys and values are copied
 // (asynchronously, as they are stored) while this one's are computed on.
 constexpr int kSimtM = 16, kSimtKT = 32, kSimtThreads = 128;
@@ -123,21 +125,25 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
             __syncthreads();
             const unsigned char* s_k = s_kv + ((u - pc.u0) & 1) * 2 * KT * row_bytes;
             const unsigned char* s_v = s_k + KT * row_bytes;
-            if (4 * w < valid) {
-                float s[4] = {0.f, 0.f, 0.f, 0.f};
+            // The warp's rows are w, w + 4, ...: a tile with few rows has them spread over the warps.
+            auto compute = [&](auto count) {
+                constexpr int R = decltype(count)::value;
+                float s[R] = {};
 #pragma unroll 4
                 for (int d = 0; d < p.D; d += 4) {
                     const float4 k = four_of<C>(s_k + lane * row_bytes + d * sizeof(C));
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float4 q = *reinterpret_cast<const float4*>(s_q + (4 * w + r) * p.D + d);
+                    for (int r = 0; r < R; ++r) {
+                        const float4 q = *reinterpret_cast<const float4*>(s_q + (w + 4 * r) * p.D + d);
                         s[r] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[r]))));
                     }
                 }
+                bool masked = false;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int m = 4 * w + r, pos = pc.r.len + (pc.tile * M + m) / p.G, key = k0 + lane;
+                for (int r = 0; r < R; ++r) {
+                    const int m = w + 4 * r, pos = pc.r.len + (pc.tile * M + m) / p.G, key = k0 + lane;
                     const bool seen = m < valid && key <= pos && (p.window == 0 || key > pos - p.window);
+                    masked |= !seen;
                     const float nm = fmaxf(mx[r], warp_max(seen ? s[r] : ninf));
                     const float use = nm == ninf ? 0.f : nm;
                     const float a = fast_exp2(mx[r] - use), e = seen ? fast_exp2(s[r] - use) : 0.f;
@@ -147,16 +153,15 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
                     for (int c = 0; c < kCols; ++c) o[r][c] *= a;
                     s_p[m * KT + lane] = seen ? e : -1.f;
                 }
-                __syncwarp();
                 // Four keys at a time.  A masked key's value stays out even where it is not a number; only
                 // units with masked keys ask.
-                const bool masked = k0 + KT - 1 > pc.r.len + (pc.tile * M + 4 * w) / p.G ||
-                                    (p.window > 0 && k0 <= pc.r.len + (pc.tile * M + 4 * w + 3) / p.G - p.window) || 4 * w + 3 >= valid;
+                masked = __any_sync(0xffffffffu, masked);
+                __syncwarp();
 #pragma unroll 1
                 for (int j = 0; j < KT; j += 4) {
-                    float4 e[4];
+                    float4 e[R];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) e[r] = *reinterpret_cast<const float4*>(s_p + (4 * w + r) * KT + j);
+                    for (int r = 0; r < R; ++r) e[r] = *reinterpret_cast<const float4*>(s_p + (w + 4 * r) * KT + j);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float2 v[kCols / 2];
@@ -164,7 +169,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
                         for (int c = 0; c < kCols / 2; ++c)
                             v[c] = 2 * lane + 64 * c < p.D ? two_of<C>(s_v + (j + i) * row_bytes, 2 * lane + 64 * c) : make_float2(0.f, 0.f);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
+                        for (int r = 0; r < R; ++r) {
                             const float x = i == 0 ? e[r].x : i == 1 ? e[r].y : i == 2 ? e[r].z : e[r].w;
                             if (!masked || !(x < 0.f)) {
 #pragma unroll
@@ -176,7 +181,11 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
                         }
                     }
                 }
-            }
+            };
+            const int rows_of_warp = (valid - w + 3) / 4;
+            if (rows_of_warp > 2) compute(std::integral_constant<int, 4>{});
+            else if (rows_of_warp == 2) compute(std::integral_constant<int, 2>{});
+            else if (rows_of_warp == 1) compute(std::integral_constant<int, 1>{});
             __syncthreads();
         }
         copy_wait<0>();
@@ -185,7 +194,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
         const int64_t place = part_place(blockIdx.x, pc.u0 == 0) * M;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int m = 4 * w + r;
+            const int m = w + 4 * r;
             if (m >= valid) continue;
             l[r] = warp_sum(l[r]);
             const int qi = pc.tile * M + m, head = pc.h * p.G + qi % p.G;
