@@ -13,6 +13,11 @@
 //   P = 2^(S - m), rescaling the output only in steps where a maximum moved,
 //   O += P V     P's accumulator layout is the A operand's layout.
 //
+// Three blocks an SM (168 registers, rings of two steps of 8 KB a warp): with three steps and two
+// blocks, fixed latencies left the 8-bit caches at half the speed of their bytes (64 requests of
+// 4000 keys: 87 us, now 74; bf16 112 and 110, of 500 keys 100 and 87).  64 requests of up to 16384
+// keys, one row each, bf16: 6.4 - 6.7 TB/s, which is what a copy reaches.
+//
 // bf16 caches: P goes in as two bf16 terms (high + low: 16 bits of P), which costs a second
 // product but no bytes.  8-bit caches: stored values are exact in f16, so both products
 // run in f16; Q's rows are scaled by a power of two into f16's range, P carries a factor
@@ -98,13 +103,13 @@ struct MmaShape {
     static constexpr int KT = KS * kWarps;                  // keys of a unit
     static constexpr int kRow = kFp8 ? DT : 2 * DT;         // bytes of a stored row
     static constexpr int kStage = 2 * KS * kRow;            // keys, then values
-    static constexpr int kStages = DT <= 64 ? 6 : 3;
+    static constexpr int kStages = DT <= 64 ? 4 : DT <= 128 ? 2 : 3;
     static constexpr int kWarpBytes = kStage * kStages;     // also holds a warp's result at the end
     static constexpr int kLd = DT + 8;                      // row of that result, floats
     static constexpr int kQBytes = M * DT * 2;
     static constexpr int kSmem = kWarps * kWarpBytes + kQBytes;
-    static constexpr int kPerSm = kSmem > 113 * 1024 ? 1 : 2;
-    static constexpr bool kQReg = DT <= 128;
+    static constexpr int kPerSm = kSmem > 113 * 1024 ? 1 : 3;
+    static constexpr bool kQReg = DT <= 64;              // the queries' fragments stay in registers
     static_assert(M * kLd * 4 <= kWarpBytes, "a warp's result fits its ring");
 };
 
