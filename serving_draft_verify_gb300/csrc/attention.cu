@@ -12,10 +12,12 @@ namespace dspark {
 namespace attn {
 namespace {
 
-// 64 requests of up to 4000 keys, 32 heads on 8: 9 rows a request (36 query rows) 196 us on the warp-level
-// instructions and 203 on tcgen05, 12 rows 206 and 205, 17 rows 307 and 240.  Short caches favour the
-// former longer (256 requests of up to 500 keys, 17 rows: 285 and 311), but the lengths are on the device.
-constexpr int kWide = 48;
+// Query rows of a key head above which tcgen05 takes over.  32 heads on 8, us on the warp-level
+// instructions and on tcgen05: 64 requests of up to 4000 keys, 12 rows a request (48 query rows) 188 and
+// 205, 16 rows 229 and 222, 17 rows 284 and 240; 128 requests of up to 6000 keys, 17 rows 723 and 498.
+// Short caches favour the former longer (256 requests of up to 500 keys, 16 rows: 242 and 302), but the
+// lengths are on the device.
+constexpr int kWide = 64;
 
 // ------------------------------------------------------------ float32 rows ---
 // Sixteen query rows (up to four a warp) over 32 keys a unit, float32 throughout: a lane is a key
