@@ -551,6 +551,16 @@ def dspark_verify_ex(t_logits, U, W1, W2, x0, x, lse_d, logp_d, ell, temperature
 
 
 # --------------------------------------------- the target model's side of a round ---
+_CODES = {torch.bfloat16: DSPARK_BF16, torch.float32: DSPARK_F32}
+
+
+def _code_of(dtype):
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
 def _device_of(t, name):
     dev = t.get_device()
     if dev < 0:
@@ -671,7 +681,7 @@ def _cache_code(k_cache, v_cache, k_scale, v_scale, dev, dtype):
         raise TypeError(f"caches of {t} for rows of {dtype}")
     if k_scale is not None or v_scale is not None:
         raise ValueError("only 8-bit caches have scales")
-    return (DSPARK_BF16 if t is torch.bfloat16 else DSPARK_F32), None, None
+    return _code_of(t), None, None
 
 
 def dspark_write_kv(k, v, slot, k_cache, v_cache, k_scale=None, v_scale=None, workspace=None, stream=None):
@@ -681,7 +691,7 @@ def dspark_write_kv(k, v, slot, k_cache, v_cache, k_scale=None, v_scale=None, wo
     lib = load()
     dev = _device_of(k_cache, "k_cache")
     nb, Hkv, page, D = k_cache.shape
-    dt = _dtype_code(k, v)
+    dt = _code_of(k.dtype)
     ks, vs = _heads(k, dev, k.dtype, "k"), _heads(v, dev, k.dtype, "v")
     n = k.shape[0]
     if k.shape != (n, Hkv, D) or v.shape != (n, Hkv, D):
@@ -722,7 +732,7 @@ def dspark_paged_attention(q, row_offset, length, block_table, k_cache, v_cache,
                      (lse, (n, Hq), torch.float32, "lse")))
     ws = _scratch(lambda: lib.dspark_paged_attention_workspace_size(D), q, workspace, stream, *made)
     _check("dspark_paged_attention",
-           lib.dspark_paged_attention(B, n, max_rows, Hq, Hkv, D, page, width, nb, _dtype_code(q), code, q.data_ptr(),
+           lib.dspark_paged_attention(B, n, max_rows, Hq, Hkv, D, page, width, nb, _code_of(q.dtype), code, q.data_ptr(),
                                       qs, row_offset.data_ptr(), length.data_ptr(), block_table.data_ptr(), width,
                                       k_cache.data_ptr(), v_cache.data_ptr(), ksc, vsc,
                                       D ** -0.5 if scale is None else float(scale), int(window),
@@ -759,7 +769,7 @@ def dspark_adjust_logits(logits, history=None, prompt_len=None, history_len=None
                      (mask, (n_mask, words), i32, "mask")))
     ws = _scratch(lib.dspark_adjust_logits_workspace_size, logits, workspace, stream, *made)
     _check("dspark_adjust_logits",
-           lib.dspark_adjust_logits(B, R, V, _dtype_code(logits), logits.data_ptr(), _addr(ell), _addr(history), width,
+           lib.dspark_adjust_logits(B, R, V, _code_of(logits.dtype), logits.data_ptr(), _addr(ell), _addr(history), width,
                                     _addr(prompt_len), _addr(history_len), _addr(draft), _addr(repetition),
                                     _addr(frequency), _addr(presence), _addr(bias_token), _addr(bias_value), n_bias,
                                     _addr(mask_row), _addr(mask), n_mask, words, out.data_ptr(), ws.data_ptr(),

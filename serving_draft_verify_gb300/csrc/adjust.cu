@@ -33,7 +33,7 @@ constexpr int kBiasShift = 21;
 constexpr int kMaxBias = (1 << (32 - kBiasShift)) - 1;      // 2047
 constexpr int kMaxHistory = static_cast<int>(kCountMask) - DSPARK_MAX_GAMMA;
 constexpr int kThreads = 256;
-constexpr int kPieceBytes = 16384;          // of a row, at most: half and a quarter of it measured slower
+constexpr int kPieceBytes = 16384;          // of a row, at most (256 requests, bf16: 314 us; with half of it 338)
 
 struct AdjustArgs {
     int R, V, chunk, n_bias, n_mask;
