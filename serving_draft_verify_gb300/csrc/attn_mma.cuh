@@ -18,7 +18,7 @@
 // 4000 keys: 87 us, now 74; bf16 112 and 110, of 500 keys 100 and 87).  64 requests of up to 16384
 // keys, one row each, bf16: 352 us for 2.4 GB, 6.8 TB/s, which is what a copy reaches.
 //
-// bf16 caches: P goes in as two bf16 terms (high + low: 16 bits of P), which costs a second
+// bf16 caches: P goes in as two bf16 terms (split_bf16: 15 bits of P at least), which costs a second
 // product but no bytes.  8-bit caches: stored values are exact in f16, so both products
 // run in f16; Q's rows are scaled by a power of two into f16's range, P carries a factor
 // 2^14 that the sum carries too and is rounded to 11 bits (half a step of 2^-12, below the
@@ -68,6 +68,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+// Two weights as two bf16 terms each.  The high one is cut off, not rounded, so that the rest is never
+// negative, and 2^-23 of the weight goes on top of the rest, so that it is not zero either: a visible
+// value of +-inf then meets two positive factors (0 inf and inf - inf are not numbers).  The rest
+// is below 2^-7 of the weight and is rounded by at most 2^-8 of itself, together 2^-15, which the
+// output's own rounding of 2^-8 covers.  (Below 2^-103 the rest leaves bf16's normal numbers.)
+__device__ __forceinline__ void split_bf16(float e0, float e1, uint32_t& high, uint32_t& low) {
+    constexpr float kOnTop = 1.f + 0x1p-23f;
+    high = __byte_perm(__float_as_uint(e0), __float_as_uint(e1), 0x7632);
+    low = pack_bf16(fmaf(e0, kOnTop, -bf16lo(high)), fmaf(e1, kOnTop, -bf16hi(high)));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t r;
@@ -391,9 +401,7 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
                     if constexpr (kFp8) {
                         ph[n >> 1][at] = pack_f16(e0, e1);
                     } else {
-                        const uint32_t h = pack_bf16(e0, e1);
-                        ph[n >> 1][at] = h;
-                        pl[n >> 1][at] = pack_bf16(e0 - bf16lo(h), e1 - bf16hi(h));
+                        split_bf16(e0, e1, ph[n >> 1][at], pl[n >> 1][at]);
                     }
                 }
             }

@@ -14,7 +14,7 @@
 //               MN-major operand);
 //   warp 3      values like the keys, and before a piece's its queries, into the other of two buffers;
 //   warps 4-11  two threads a query row, each with half of a unit's keys: P = 2^(S - m) as two
-//               bf16 terms (high + low, so that 16 bits of P count) into TMEM, the sum, and half of
+//               bf16 terms (split_bf16, so that 15 bits of P count) into TMEM, the sum, and half of
 //               the output's columns at the end.
 // The output in TMEM is rescaled only where a maximum has grown by more than 2^8 over the one
 // in use (the factor stays in P and the sum alike until then), so the two threads of a row
@@ -414,9 +414,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         l4[c & 2] += e0;
                         l4[(c & 2) + 1] += e1;
                         // the two terms of both take the scores' places: high, then low
-                        const uint32_t hi = pack_bf16(e0, e1);
-                        s[c] = __uint_as_float(hi);
-                        s[c + 1] = __uint_as_float(pack_bf16(e0 - bf16lo(hi), e1 - bf16hi(hi)));
+                        uint32_t high, low;
+                        split_bf16(e0, e1, high, low);
+                        s[c] = __uint_as_float(high);
+                        s[c + 1] = __uint_as_float(low);
                     }
                     l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
                 }

@@ -1,0 +1,60 @@
+"""Edges of the target model's side of a round.  The bounds of attention are those of
+test_gpu_target.py's text.
+"""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_target import _attend_case, _check_attend, _oracle, _run_attend, dsv  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ attend ---
+# lens, Hq, Hkv, D: 17 rows of groups of four and more go to 128-row tiles, the others to 16-row ones
+VISIBLE = [([(900, 1), (130, 1)], 8, 4, 64), ([(900, 4), (130, 4)], 8, 4, 128), ([(900, 2)], 4, 4, 256),
+           ([(900, 17), (130, 17)], 32, 8, 128), ([(900, 17)], 16, 2, 64), ([(9000, 1)], 8, 2, 128),
+           ([(9000, 17)], 32, 8, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,Hq,Hkv,D", VISIBLE)
+def test_infinite_values_at_visible_keys(dsv, lens, Hq, Hkv, D, dtype):  # noqa: F811
+    """A weight is positive, so a value of +-inf makes its column +-inf wherever its key stands, both
+    signs make it NaN, and the other columns stay as they are."""
+    c = _attend_case(31, lens, Hq, Hkv, D, 16, dtype, dtype, 0)
+    inf = float("inf")
+    for b, (n, r) in enumerate(lens):
+        places = [0, 5, n // 3, n // 2 + 1, n - 70, n - 1, n, n + r - 1]
+        for i, p in enumerate(places):
+            blk = int(c["block_table"][b, p // 16])
+            c["v_cache"][blk, :, p % 16, 3 * i] = -inf if i & 1 else inf
+        for p, x in ((n // 4, inf), (n // 4 + 1, -inf)):
+            c["v_cache"][int(c["block_table"][b, p // 16]), :, p % 16, 31] = x
+    out, code = _run_attend(dsv, c)
+    assert code[0] == 0
+    with np.errstate(invalid="ignore"):
+        ref = _oracle(c)
+    odd = ~np.isfinite(ref["out"])
+    assert np.isposinf(ref["out"]).any() and np.isneginf(ref["out"]).any() and np.isnan(ref["out"]).any()
+    got = out["out"].double().cpu().numpy()
+    np.testing.assert_array_equal(got[odd], ref["out"][odd])
+    rest = dict(ref, out=np.where(odd, 0.0, ref["out"]), weight=np.where(odd, 0.0, ref["weight"]))
+    _check_attend(dict(out, out=torch.from_numpy(np.where(odd, 0.0, got))), rest, dtype, D)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_hidden_values_in_later_units(dsv, value):  # noqa: F811
+    """Pieces of several units of 128 keys, the last row's value (in the last of them) not finite."""
+    rows, B = 17, 20
+    lens = [(900 + 13 * b, rows) for b in range(B)]
+    c = _attend_case(32, lens, 32, 8, 128, 16, "bf16", "bf16", 0)
+    want, _ = _run_attend(dsv, c)
+    for b, (n, _r) in enumerate(lens):
+        last = n + rows - 1
+        c["v_cache"][int(c["block_table"][b, last // 16]), :, last % 16] = value
+    got, _ = _run_attend(dsv, c)
+    keep = [i for i in range(B * rows) if i % rows != rows - 1]
+    assert torch.equal(got["out"][keep], want["out"][keep]) and torch.equal(got["lse"], want["lse"])
+    last = got["out"][rows - 1::rows].float()
+    assert torch.isnan(last).all() if value != value else torch.isposinf(last).all()
