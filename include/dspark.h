@@ -476,7 +476,8 @@ dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int page, int num_
  * hq / (Hq / Hkv):
  *   s_j = scale q . k_j,  lse = ln sum_j exp(s_j),  out = sum_j exp(s_j - lse) v_j
  * in float32, out rounded once to `dt`.  Keys and values a row does not see have no
- * part in it, whatever they hold; pages past the last position are not read.
+ * part in it, whatever they hold.  Table entries of pages past the last position, and with a
+ * window of pages wholly before position len[b] - window + 1, are not read.
  *   q: row i at i * q_stride elements, Hq heads of D adjacent elements in `dt`, 16-byte
  *   aligned rows; out [rows][Hq][D] in `dt`; lse [rows][Hq] float32 or NULL.
  *   rows: what q and out have room for (row_offset[B] or more; the rest is not

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
         // lane j has the place (in rows) of key j of a unit, found a unit ahead of its copy
         auto find_rows = [&](int u) -> int64_t {
             const int key = pc.span.lo + u * KT + lane;
-            if (u >= pc.u1 || key >= pc.span.hi) return 0;
+            if (u >= pc.u1 || key < pc.span.seen || key >= pc.span.hi) return 0;
             const int blk = key / p.page;
             return (static_cast<int64_t>(page_id(p, pc.b, blk)) * p.Hkv + pc.h) * p.page + (key - blk * p.page);
         };
@@ -88,7 +88,8 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
                 for (int e = tid; e < n; e += kSimtThreads) {
                     const int r = e / chunks, c = e - r * chunks;
                     const int64_t row = __shfl_sync(0xffffffffu, rows, r);
-                    const bool real = pc.span.lo + u * KT + r < pc.span.hi;
+                    const int key = pc.span.lo + u * KT + r;
+                    const bool real = key >= pc.span.seen && key < pc.span.hi;
                     const int64_t at = real ? row * (p.D * static_cast<int>(sizeof(C))) + c * 16 : 0;
                     copy16(to + r * row_bytes + c * 16, static_cast<const char*>(p.kc) + at, real);
                     copy16(to + (KT + r) * row_bytes + c * 16, static_cast<const char*>(p.vc) + at, real);

@@ -67,9 +67,10 @@ __device__ __forceinline__ Request request_of(const Args& p, int b, bool report)
     r.n = ok ? static_cast<int>(n) : 0;
     return r;
 }
-// The keys [lo, hi) that tile t of a request's query rows can see, and its units.
+// The keys [seen, hi) that tile t of a request's query rows can see, and its units.  Nothing is read
+// for the keys from lo to seen: pages that a window has left behind may be gone.
 struct Span {
-    int lo, hi;                       // lo on a unit's border
+    int lo, hi, seen;                 // lo: the unit's border at or before seen
     __device__ __forceinline__ int units(int KT) const { return hi > lo ? (hi - lo + KT - 1) / KT : 1; }
 };
 template <int M, int KT>
@@ -78,8 +79,8 @@ __device__ __forceinline__ Span span_of(const Args& p, const Request& r, int t) 
     const int last = (min(static_cast<int64_t>(t + 1) * M, static_cast<int64_t>(r.n) * p.G) - 1) / p.G;
     Span s;
     s.hi = r.len + last + 1;
-    const int lo = p.window > 0 ? max(0, r.len + first - p.window + 1) : 0;
-    s.lo = lo / KT * KT;
+    s.seen = p.window > 0 ? max(0, r.len + first - p.window + 1) : 0;
+    s.lo = s.seen / KT * KT;
     return s;
 }
 template <int M>

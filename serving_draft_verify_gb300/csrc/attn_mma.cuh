@@ -185,20 +185,20 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
         // its 16 where a page holds them.
         auto find_rows = [&](int s) -> int64_t {
             const int key = key0 + s * KT + (whole_pages ? lane & (KS - 16) : lane);
-            if (s >= steps || key >= pc.span.hi || (!whole_pages && lane >= KS)) return 0;
+            if (s >= steps || key + (whole_pages ? 15 : 0) < pc.span.seen || key >= pc.span.hi || (!whole_pages && lane >= KS)) return 0;
             const int blk = key / p.page;
             return (static_cast<int64_t>(page_id(p, pc.b, blk)) * p.Hkv + pc.h) * p.page + (key - blk * p.page);
         };
         auto load = [&](int s, int64_t rows) {
             const int first = key0 + s * KT;
-            if (s < steps && first < pc.span.hi) {
+            if (s < steps && first < pc.span.hi && first + KS > pc.span.seen) {
                 const uint32_t to = ring_a + (s % kStages) * Sh::kStage;
                 const char* kc = static_cast<const char*>(p.kc);
                 const char* vc = static_cast<const char*>(p.vc);
                 int64_t run[kSub];                           // the first rows of the step's sixteens
 #pragma unroll
                 for (int b = 0; b < kSub; ++b) run[b] = kSub == 1 ? rows : __shfl_sync(0xffffffffu, rows, 16 * b);
-                if (adjacent && first + KS <= pc.span.hi) {
+                if (adjacent && first >= pc.span.seen && first + KS <= pc.span.hi) {
                     // sixteen rows are one run of bytes: 16 a lane, 512 on each time
                     constexpr int kIn = 16 * kChunks / 32;
 #pragma unroll
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
                         const int e = lane + 32 * i, r = e / kChunks, c = e % kChunks;
                         const int64_t mine = __shfl_sync(0xffffffffu, rows, whole_pages ? r & (KS - 16) : r);
                         const int64_t row = whole_pages ? mine + (r & 15) : mine;
-                        const bool real = first + r < pc.span.hi && c < real_chunks;
+                        const bool real = first + r >= pc.span.seen && first + r < pc.span.hi && c < real_chunks;
                         const int64_t at = real ? row * (p.D * esize) + c * 16 : 0;
                         const uint32_t d = to + chunk_at<kRow>(r, c);
                         copy16(d, kc + at, real);
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
             load(s + kStages - 1, rows);
             rows = find_rows(s + kStages);
             const int first = key0 + s * KT;
-            if (first >= pc.span.hi) continue;
+            if (first >= pc.span.hi || first + KS <= pc.span.seen) continue;
             const uint32_t k_a = ring_a + (s % kStages) * Sh::kStage, v_a = k_a + KS * kRow;
 
             // ---- S = Q K^T

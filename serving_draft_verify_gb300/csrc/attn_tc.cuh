@@ -196,23 +196,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 fence_proxy_async_smem();
                 mbar_arrive(&bars.q_full[n & 1]);
             }
-            const int hi = pc.span.hi, b = pc.b, h = pc.h;
+            const int hi = pc.span.hi, seen = pc.span.seen, b = pc.b, h = pc.h;
             int k0 = pc.span.lo + pc.u0 * kTcKT;
 #pragma unroll 1
             for (int u = pc.u0; u < pc.u1; ++u, ++i, k0 += kTcKT) {
-                const int stage = i & 1, boxes = (min(kTcKT, hi - k0) + box - 1) / box;
+                // boxes wholly before the first key that the tile sees stay away: the softmax makes those
+                // values 0, as it does those past the last key
+                const int stage = i & 1, before = max(seen - k0, 0) / box, boxes = (min(kTcKT, hi - k0) + box - 1) / box - before;
                 // lane l finds the row of box l; lane 0 issues them all (an instruction that several
                 // lanes issue goes lane by lane, at several times the cost)
                 int y = 0;
                 if (lane < boxes) {
-                    const int key = k0 + lane * box, blk = key / p.page;
+                    const int key = k0 + (before + lane) * box, blk = key / p.page;
                     y = (page_id(p, b, blk) * p.Hkv + h) * p.page + (key - blk * p.page);
                 }
                 if (lane == 0) {
                     wait(&empty[stage], (i >> 1) + 1);
                     if (!s_dead) mbar_arrive_expect_tx(&full[stage], boxes * box * 128 * Sh::kHalves);
                 }
-                unsigned char* to = ring + stage * Sh::kTile;
+                unsigned char* to = ring + stage * Sh::kTile + before * box * 128;
 #pragma unroll 1
                 for (int j = 0; j < boxes; ++j, to += box * 128) {
                     const int yj = __shfl_sync(0xffffffffu, y, j);
@@ -304,15 +306,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (masked) {
                     c_hi = min(min(pos, pos_hi) + 1 - k0, kTcKT);
                     if (p.window > 0) c_lo = max(pos - p.window + 1 - k0, 0);
-                    // Values at keys past the last one, and values that are not finite at keys that only
-                    // some rows see, must not meet the product (0 times them is not 0).  The former become
-                    // 0; the latter are added here to the rows that see them and become 0 too.
+                    // Values at keys past the last one or before the first, and values that are not finite at
+                    // keys that only some rows see, must not meet the product (0 times them is not 0).  The
+                    // former become 0; the latter are added here to the rows that see them and become 0 too.
                     wait(&bars.v_full[stage], i >> 1);
                     unsigned char* v = s_v + stage * Sh::kTile;
                     bool odd = false;
                     if (half < Sh::kHalves) {
                         uint4* x = reinterpret_cast<uint4*>(v + half * Sh::kHalf + m * 128);
-                        if (k0 + m > pos_hi) {
+                        if (k0 + m > pos_hi || k0 + m < pc.span.seen) {
 #pragma unroll
                             for (int c = 0; c < 8; ++c) x[c] = make_uint4(0, 0, 0, 0);
                         } else {

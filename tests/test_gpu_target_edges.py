@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_target import _attend_case, _check_attend, _oracle, _run_attend, dsv  # noqa: F401
+from tests.test_gpu_target import KINDS, _attend_case, _check_attend, _oracle, _run_attend, dsv  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +58,30 @@ def test_hidden_values_in_later_units(dsv, value):  # noqa: F811
     assert torch.equal(got["out"][keep], want["out"][keep]) and torch.equal(got["lse"], want["lse"])
     last = got["out"][rows - 1::rows].float()
     assert torch.isnan(last).all() if value != value else torch.isposinf(last).all()
+
+
+WINDOWS = [  # lens, Hq, Hkv, D, page, window
+    ([(500, 1), (37, 1)], 8, 2, 128, 16, 100), ([(500, 4), (70, 3)], 8, 2, 64, 16, 33), ([(300, 3)], 4, 2, 48, 5, 41),
+    ([(90, 2)], 4, 4, 32, 1, 7), ([(1000, 3)], 8, 4, 64, 256, 300), ([(700, 17), (140, 17)], 32, 8, 128, 16, 130),
+    ([(700, 17)], 16, 2, 64, 8, 65), ([(1100, 17)], 32, 8, 128, 32, 500), ([(600, 2)], 4, 1, 256, 24, 200),
+    ([(5000, 4)], 8, 2, 128, 16, 1500)]
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS, ids=["-".join(k) for k in KINDS])
+@pytest.mark.parametrize("lens,Hq,Hkv,D,page,window", WINDOWS)
+def test_pages_before_the_window_may_be_gone(dsv, lens, Hq, Hkv, D, page, window, dtype, cache):  # noqa: F811
+    if cache == "e4m3" and D % 16:
+        pytest.skip("8-bit heads are multiples of 16")
+    c = _attend_case(33, lens, Hq, Hkv, D, page, dtype, cache, window)
+    want, code = _run_attend(dsv, c)
+    assert code[0] == 0
+    _check_attend(want, _oracle(c), dtype, D)
+    gone = 0
+    for b, (n, _r) in enumerate(lens):
+        first = max(0, n - window + 1)                       # the first key that any row of the step sees
+        c["block_table"][b, :first // page] = -1
+        gone += first // page
+    assert gone > 0
+    got, code = _run_attend(dsv, c)
+    assert code[0] == 0
+    assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
