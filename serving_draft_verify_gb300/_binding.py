@@ -610,17 +610,28 @@ def _heads(t, dev, dtype, name):
     return s[0] if n > 1 else heads * D
 
 
-def _scratch(size, like, workspace, stream, *made):
-    """The workspace (allocated here, of size() bytes, if None).  Memory that this call allocated and that work on
-    another stream than the current one uses is tied to that stream."""
+def _made_on(stream, make):
+    """make()'s dict of tensors, from the memory of the stream that writes them: what the current stream
+    has freed it may still have to read.  The caller may use them on the current stream."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        made = make()
+    for t in made.values():
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return made
+
+
+def _scratch(size, like, workspace, stream):
+    """The workspace; if None, size() bytes of the memory of the stream that uses it."""
     if workspace is None:
-        workspace = torch.empty(max(int(size()), 256), dtype=torch.uint8, device=like.device)
-        made = (*made, workspace)
-    elif workspace.get_device() != like.get_device():
+        make = lambda: torch.empty(max(int(size()), 256), dtype=torch.uint8, device=like.device)  # noqa: E731
+        if stream is None:
+            return make()
+        with torch.cuda.stream(stream):
+            return make()
+    if workspace.get_device() != like.get_device():
         raise ValueError("workspace is on another device")
-    if stream is not None:
-        for t in made:
-            t.record_stream(stream)
     return workspace
 
 
@@ -640,12 +651,11 @@ def dspark_plan_rows(length, rows, held, free_state, free_ring, block_table, pag
     nb, = free_ring.shape
     width = block_table.shape[1]
     i32 = torch.int32
-    made = ()
     if out is None:
         new = lambda n, t=i32: torch.empty(n, dtype=t, device=length.device)  # noqa: E731
-        out = dict(length=new(B), held=new(B), free_state=new(2), row_offset=new(B + 1), row_request=new(max_rows),
-                   position=new(max_rows), slot=new(max_rows, torch.int64))
-        made = tuple(out.values())
+        out = _made_on(stream, lambda: dict(length=new(B), held=new(B), free_state=new(2), row_offset=new(B + 1),
+                                            row_request=new(max_rows), position=new(max_rows),
+                                            slot=new(max_rows, torch.int64)))
     o_len, o_held, o_free, o_off, o_req, o_pos, o_slot = [out[k] for k in _PLAN_OUT]
     per, rowwise = (B,), (max_rows,)
     _check_all(dev, ((length, per, i32, "length"), (rows, per, i32, "rows"), (held, per, i32, "held"),
@@ -655,7 +665,7 @@ def dspark_plan_rows(length, rows, held, free_state, free_ring, block_table, pag
                      (o_free, (2,), i32, "out free_state"), (o_off, (B + 1,), i32, "row_offset"),
                      (o_req, rowwise, i32, "row_request"), (o_pos, rowwise, i32, "position"),
                      (o_slot, rowwise, torch.int64, "slot")))
-    ws = _scratch(lambda: lib.dspark_plan_rows_workspace_size(B, max_rows), length, workspace, stream, *made)
+    ws = _scratch(lambda: lib.dspark_plan_rows_workspace_size(B, max_rows), length, workspace, stream)
     _check("dspark_plan_rows",
            lib.dspark_plan_rows(B, page, width, nb, max_rows, length.data_ptr(), _addr(advance), rows.data_ptr(),
                                 held.data_ptr(), free_state.data_ptr(), free_ring.data_ptr(), block_table.data_ptr(),
@@ -721,16 +731,14 @@ def dspark_paged_attention(q, row_offset, length, block_table, k_cache, v_cache,
         raise ValueError(f"q has heads of {qd}, the caches of {D}")
     width = block_table.shape[1]
     code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, q.dtype)
-    made = ()
     if out is None:
-        out = dict(out=torch.empty((n, Hq, D), dtype=q.dtype, device=q.device),
-                   lse=torch.empty((n, Hq), dtype=torch.float32, device=q.device))
-        made = tuple(out.values())
+        out = _made_on(stream, lambda: dict(out=torch.empty((n, Hq, D), dtype=q.dtype, device=q.device),
+                                            lse=torch.empty((n, Hq), dtype=torch.float32, device=q.device)))
     o, lse = out["out"], out.get("lse")
     _check_all(dev, ((row_offset, (B + 1,), torch.int32, "row_offset"), (length, (B,), torch.int32, "length"),
                      (block_table, (B, width), torch.int32, "block_table"), (o, (n, Hq, D), q.dtype, "out"),
                      (lse, (n, Hq), torch.float32, "lse")))
-    ws = _scratch(lambda: lib.dspark_paged_attention_workspace_size(D), q, workspace, stream, *made)
+    ws = _scratch(lambda: lib.dspark_paged_attention_workspace_size(D), q, workspace, stream)
     _check("dspark_paged_attention",
            lib.dspark_paged_attention(B, n, max_rows, Hq, Hkv, D, page, width, nb, _code_of(q.dtype), code, q.data_ptr(),
                                       qs, row_offset.data_ptr(), length.data_ptr(), block_table.data_ptr(), width,
@@ -755,10 +763,8 @@ def dspark_adjust_logits(logits, history=None, prompt_len=None, history_len=None
     width = history.shape[1] if history is not None else 0
     n_bias = bias_token.shape[1] if bias_token is not None else 0
     n_mask, words = mask.shape if mask is not None else (0, (V + 31) // 32)
-    made = ()
     if out is None:
-        out = torch.empty_like(logits)
-        made = (out,)
+        out = _made_on(stream, lambda: dict(out=torch.empty_like(logits)))["out"]
     per, whole = (B,), (B, R, V)
     _check_all(dev, ((logits, whole, logits.dtype, "logits"), (out, whole, logits.dtype, "out"), (ell, per, i32, "ell"),
                      (history, (B, width), i32, "history"), (prompt_len, per, i32, "prompt_len"),
@@ -767,7 +773,7 @@ def dspark_adjust_logits(logits, history=None, prompt_len=None, history_len=None
                      (presence, per, f32, "presence"), (bias_token, (B, n_bias), i32, "bias_token"),
                      (bias_value, (B, n_bias), f32, "bias_value"), (mask_row, (B, R), i32, "mask_row"),
                      (mask, (n_mask, words), i32, "mask")))
-    ws = _scratch(lib.dspark_adjust_logits_workspace_size, logits, workspace, stream, *made)
+    ws = _scratch(lib.dspark_adjust_logits_workspace_size, logits, workspace, stream)
     _check("dspark_adjust_logits",
            lib.dspark_adjust_logits(B, R, V, _code_of(logits.dtype), logits.data_ptr(), _addr(ell), _addr(history), width,
                                     _addr(prompt_len), _addr(history_len), _addr(draft), _addr(repetition),

@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_target import KINDS, _attend_case, _check_attend, _oracle, _run_attend, dsv  # noqa: F401
+from tests.test_gpu_target import (KINDS, _attend_case, _check_attend, _gpu, _oracle, _plan_case, _run_attend,
+                                   dsv)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +86,39 @@ def test_pages_before_the_window_may_be_gone(dsv, lens, Hq, Hkv, D, page, window
     got, code = _run_attend(dsv, c)
     assert code[0] == 0
     assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+
+
+# --------------------------------------------------- streams ---
+def _sleep(ms=50):
+    torch.cuda._sleep(int(ms * 2e6))
+
+
+@pytest.mark.parametrize("call", ["plan", "attend", "adjust"])
+def test_memory_made_for_another_stream(dsv, call):  # noqa: F811
+    """Memory that the current stream has still to read is not what a call on another stream writes."""
+    side = torch.cuda.Stream()
+    if call == "plan":
+        c = _plan_case(71, 2000, 16, 40, 9, 17)
+        g = {k: _gpu(v) for k, v in c.items() if isinstance(v, np.ndarray)}
+        run = lambda s: dsv.dspark_plan_rows(g["length"], g["rows"], g["held"], g["free_state"], g["free_ring"],  # noqa: E731
+                                             g["block_table"], 16, c["max_rows"], advance=g["advance"], stream=s)["slot"]
+        size, dtype = (c["max_rows"],), torch.int64
+    elif call == "attend":
+        c = _attend_case(72, [(300, 64), (20, 2)], 8, 2, 128, 16, "bf16", "bf16", 0)
+        args = {k: c[k] for k in ("q", "row_offset", "length", "block_table", "k_cache", "v_cache", "max_rows")}
+        run = lambda s: dsv.dspark_paged_attention(**args, stream=s)["out"]  # noqa: E731
+        size, dtype = c["q"].shape, torch.bfloat16
+    else:
+        x = torch.randn((4, 3, 40000), device="cuda")
+        run = lambda s: dsv.dspark_adjust_logits(x, stream=s)  # noqa: E731
+        size, dtype = x.shape, torch.float32
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    old = torch.full(size, 77, dtype=dtype, device="cuda")
+    later = torch.zeros_like(old)
+    _sleep()
+    later.copy_(old)
+    del old                                              # its memory is free for the current stream's next use
+    out = run(side)
+    torch.cuda.synchronize()
+    assert (later == 77).all() and not (out == 77).all()
