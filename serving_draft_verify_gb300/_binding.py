@@ -562,9 +562,13 @@ def _code_of(dtype):
 
 
 def _device_of(t, name):
+    """The device index of the call's first tensor.  The library launches on the current device and takes
+    its streams from there, so tensors of another one are refused."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
     return dev
 
 
