@@ -34,7 +34,7 @@ struct PlanArgs {
     uint32_t* ticket;
 };
 
-// What one request asks for; `bad` is the detail code of an inconsistent one.
+// What one request asks for; `bad` is 1 or 2, the detail code of an inconsistent one.
 struct Ask {
     int base, rows, held, need;
     uint32_t bad;
@@ -125,14 +125,14 @@ __global__ void __launch_bounds__(kT) plan_rows(PlanArgs p) {
     const int head = p.free_state[0], count = p.free_state[1];
     const int tiles = (p.B + kT - 1) / kT;
     Sums run{0, 0};
-    uint32_t bad = 0;
+    uint32_t bad = 0;                     // bit d - 1: a request of this thread is refused with detail d
     Ask own{};                            // this thread's request of the last tile, kept for the state write
     Sums own_at{0, 0};
     for (int t = 0; t < tiles; ++t) {
         const int b = t * kT + tid;
         Ask a{};
         if (b < p.B) a = ask_of(p, b);
-        if (a.bad != 0) bad = a.bad;
+        bad |= a.bad;
         const int take = a.need > a.held ? a.need - a.held : 0, give = a.held > a.need ? a.held - a.need : 0;
         Sums v{static_cast<unsigned long long>(a.rows),
                static_cast<unsigned long long>(take) | (static_cast<unsigned long long>(give) << 32)};
@@ -164,10 +164,10 @@ __global__ void __launch_bounds__(kT) plan_rows(PlanArgs p) {
     const int64_t T = static_cast<int64_t>(run.pages & 0xffffffffu), R = static_cast<int64_t>(run.pages >> 32);
     // all or nothing: every block comes to the same verdict
     const int cap = p.num_blocks;
-    if (head < 0 || head >= cap || count < 0 || count > cap) bad = bad > 1u ? bad : 1u;
+    if (head < 0 || head >= cap || count < 0 || count > cap) bad |= 1u;
     uint32_t why = 0;
-    if (__syncthreads_or(bad == 1u)) why = 1;
-    else if (__syncthreads_or(bad == 2u)) why = 2;
+    if (__syncthreads_or(bad & 1u)) why = 1;
+    else if (__syncthreads_or(bad & 2u)) why = 2;
     else if (T > count) why = 3;
     else if (count + R > cap) why = 1;
     else if (N > p.room) why = 4;

@@ -5,8 +5,9 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import target
 from tests.test_gpu_target import (KINDS, _attend_case, _check_attend, _gpu, _oracle, _plan_case, _run_attend,
-                                   dsv)  # noqa: F401
+                                   _run_plan, _same_plan, dsv)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -86,6 +87,21 @@ def test_pages_before_the_window_may_be_gone(dsv, lens, Hq, Hkv, D, page, window
     got, code = _run_attend(dsv, c)
     assert code[0] == 0
     assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+
+
+# -------------------------------------------------------------------- plan ---
+@pytest.mark.parametrize("B,first,second", [(1500, 3, 1027), (1500, 1027, 3), (9, 1, 2), (2100, 2049, 1025)])
+def test_plan_tells_the_first_reason(dsv, B, first, second):  # noqa: F811
+    """An inconsistent request (detail 1) and a full table (2) in one step: 1, whichever comes first."""
+    c = _plan_case(41, B, 8, 20, 4, 17, finish=0.0)
+    c["length"][first] = -1
+    c["rows"][second] = 8 * 20 + 1
+    c["max_rows"] = int(c["rows"].sum()) + 1
+    want = target.plan_rows(**c)
+    assert want["detail"] == 1
+    got, code, why = _run_plan(dsv, c)
+    assert (code, why) == (6, 1)
+    _same_plan(got, want)
 
 
 # --------------------------------------------------- streams ---
