@@ -434,9 +434,9 @@ dspark_status_t dspark_training_loss(int64_t rows, int V, dspark_dtype_t dt,
  *   first rows; and for row i: row_request[i], position[i] (base + its place in the
  *   request) int32 and slot[i] int64, i < max_rows, with -1 in the rows past the
  *   last.
- * All or nothing: where a request's numbers are not consistent (detail 1: negative,
- * more rows than its pages hold, or a ring that cannot hold what is given back), a
- * table is full (2), the free pages do not suffice (3) or there are more than max_rows
+ * All or nothing: where a request's numbers are not consistent (detail 1: len, advance,
+ * rows or held negative, more rows than its pages hold, or a ring that cannot hold what is
+ * given back), a table is full (2), the free pages do not suffice (3) or there are more than max_rows
  * rows (4), the status is DSPARK_ERR_DEVICE_CHECK, the state outputs repeat the inputs,
  * row_offset is all zero, the rows are all -1 and no page moves.  A page id outside
  * [0, num_blocks) (5) gives that row slot -1.

@@ -23,7 +23,7 @@ def plan_rows(length, advance, rows, held, free_state, free_ring, block_table, p
                slot=np.full(max_rows, -1, np.int64), block_table=table, free_ring=ring, detail=0)
     take = [max(0, n - int(h)) for n, h in zip(need, held)]
     give = [max(0, int(h) - n) for n, h in zip(need, held)]
-    bad = any(length[b] < 0 or rows[b] < 0 or held[b] < 0 or base[b] < 0 or held[b] > width
+    bad = any(length[b] < 0 or advance[b] < 0 or rows[b] < 0 or held[b] < 0 or held[b] > width
               or base[b] > int(held[b]) * page for b in range(B))
     if bad or not 0 <= head < cap or not 0 <= count <= cap:
         return dict(out, detail=1)

@@ -47,7 +47,7 @@ __device__ __forceinline__ Ask ask_of(const PlanArgs& p, int b) {
     const int64_t rows = p.rows[b], held = p.held[b];
     const int64_t base = len + adv, end = base + rows;
     const int64_t room = static_cast<int64_t>(p.max_blocks) * p.page;
-    if (len < 0 || rows < 0 || held < 0 || base < 0 || held > p.max_blocks || base > held * p.page) {
+    if (len < 0 || adv < 0 || rows < 0 || held < 0 || held > p.max_blocks || base > held * p.page) {
         a.bad = 1;
         return a;
     }

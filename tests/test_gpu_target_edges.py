@@ -104,6 +104,17 @@ def test_plan_tells_the_first_reason(dsv, B, first, second):  # noqa: F811
     _same_plan(got, want)
 
 
+@pytest.mark.parametrize("B", [9, 1500])
+def test_plan_refuses_a_negative_advance(dsv, B):  # noqa: F811
+    c = _plan_case(42, B, 8, 20, 4, 17, finish=0.0)
+    c["length"][B - 1], c["advance"][B - 1] = 5, -1
+    got, code, why = _run_plan(dsv, c)
+    assert (code, why) == (6, 1)
+    want = target.plan_rows(**c)
+    assert want["detail"] == 1
+    _same_plan(got, want)
+
+
 # --------------------------------------------------- streams ---
 def _sleep(ms=50):
     torch.cuda._sleep(int(ms * 2e6))
