@@ -293,10 +293,8 @@ extern "C" dspark_status_t dspark_plan_rows(int B, int page, int max_blocks, int
     const int64_t tile = small ? 256 : 1024;
     const int64_t row_tiles = (max_rows + tile - 1) / tile, req_tiles = (B + tile - 1) / tile;
     const int64_t grid = row_tiles > req_tiles ? row_tiles : req_tiles;
-    if (grid > 1) {
-        if (small) return launch_cleared(workspace, kStatusBytes + 16, plan_rows<256>, dim3(static_cast<unsigned>(grid)), 256, 0, s, p);
+    if (grid > 1)
         return launch_cleared(workspace, kStatusBytes + 16, plan_rows<1024>, dim3(static_cast<unsigned>(grid)), 1024, 0, s, p);
-    }
     if (small) plan_rows<256><<<1, 256, 0, s>>>(p);
     else plan_rows<1024><<<1, 1024, 0, s>>>(p);
     return launch_status();
