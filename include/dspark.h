@@ -512,9 +512,9 @@ dspark_status_t dspark_paged_attention(int B, int64_t rows, int max_rows, int Hq
  *   masked: y = -inf
  * in float32, rounded once.  Untouched tokens keep their bits.
  *   ell [B] int32 in 0..R-1: only rows 0..ell[b] are read and written (those that
- *   dspark_verify reads); NULL: all.  history [B][ld_history] int32 with history_len;
- *   prompt_len NULL: no prompt.  draft [B][R-1] int32 or NULL.  repetition (> 0),
- *   frequency, presence [B] float32, each may be NULL (1, 0, 0).
+ *   dspark_verify reads); NULL: all.  history [B][ld_history] int32 with history_len (NULL
+ *   as well where ld_history is 0); prompt_len NULL: no prompt.  draft [B][R-1] int32 or
+ *   NULL.  repetition (> 0), frequency, presence [B] float32, each may be NULL (1, 0, 0).
  *   bias_token [B][n_bias] int32 (-1: unused), bias_value [B][n_bias] float32; entries of
  *   one token add up in their order.
  *   mask_row [B][R] int32: the row of mask that holds for this row, -1 for none; mask

@@ -316,8 +316,9 @@ extern "C" dspark_status_t dspark_adjust_logits(int B, int R, int V, dspark_dtyp
     if ((dt != DSPARK_BF16 && dt != DSPARK_F32) || V % (dt == DSPARK_BF16 ? 8 : 4) != 0)
         return DSPARK_ERR_INVALID_ARGUMENT;
     if (logits == nullptr || out == nullptr || !aligned16(logits) || !aligned16(out)) return DSPARK_ERR_INVALID_ARGUMENT;
-    if ((history == nullptr) != (history_len == nullptr) || (prompt_len != nullptr && history == nullptr) ||
-        ld_history < 0)
+    // a history of no columns has no address; its lengths are checked on the device like any others
+    const bool has_history = history != nullptr || (history_len != nullptr && ld_history == 0);
+    if (has_history != (history_len != nullptr) || (prompt_len != nullptr && !has_history) || ld_history < 0)
         return DSPARK_ERR_INVALID_ARGUMENT;
     if (n_bias < 0 || (n_bias > 0 && (bias_token == nullptr || bias_value == nullptr)))
         return DSPARK_ERR_INVALID_ARGUMENT;

@@ -6,8 +6,8 @@ import pytest
 import torch
 
 from oracle import target
-from tests.test_gpu_target import (KINDS, _attend_case, _check_attend, _gpu, _oracle, _plan_case, _run_attend,
-                                   _run_plan, _same_plan, dsv)  # noqa: F401
+from tests.test_gpu_target import (KINDS, _adjust_case, _attend_case, _check_attend, _code, _gpu, _oracle, _plan_case,
+                                   _run_attend, _run_plan, _same_plan, _ws, dsv)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -113,6 +113,22 @@ def test_plan_refuses_a_negative_advance(dsv, B):  # noqa: F811
     want = target.plan_rows(**c)
     assert want["detail"] == 1
     _same_plan(got, want)
+
+
+# ------------------------------------------------------------------ adjust ---
+def test_adjust_with_a_history_of_no_columns(dsv):  # noqa: F811
+    """Requests without a token yet: the history has no columns, and its lengths are zero."""
+    c = _adjust_case(62, 3, 2, 512, "f32", 0, 2, 0)
+    g = {k: v if v is None else v.cuda() for k, v in c.items()}
+    none = torch.zeros(3, dtype=torch.int32, device="cuda")
+    ws = _ws()
+    want = dsv.dspark_adjust_logits(**g, out=torch.zeros_like(g["logits"]))
+    g.update(history=torch.zeros((3, 0), dtype=torch.int32, device="cuda"), history_len=none, prompt_len=none)
+    got = dsv.dspark_adjust_logits(**g, out=torch.zeros_like(g["logits"]), workspace=ws)
+    assert _code(ws)[0] == 0 and torch.equal(got, want)
+    g["history_len"] = none + 1
+    dsv.dspark_adjust_logits(**g, out=torch.zeros_like(g["logits"]), workspace=ws)
+    assert _code(ws) == [6, 2]
 
 
 # --------------------------------------------------- streams ---
