@@ -481,7 +481,7 @@ dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int page, int num_
  *   q: row i at i * q_stride elements, Hq heads of D adjacent elements in `dt`, 16-byte
  *   aligned rows; out [rows][Hq][D] in `dt`; lse [rows][Hq] float32 or NULL.
  *   rows: what q and out have room for (row_offset[B] or more; the rest is not
- *   touched); max_rows: the most rows of one request.
+ *   touched; 0: nothing is launched); max_rows: the most rows of one request.
  *   cache_dt, k_scale, v_scale as for dspark_write_kv: a stored value stands for
  *   itself times scale[head].
  * The work is divided evenly over the GPU by the lengths on the device, so a call can be

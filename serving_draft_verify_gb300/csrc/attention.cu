@@ -269,7 +269,7 @@ extern "C" dspark_status_t dspark_paged_attention(
     const float* k_scale, const float* v_scale, float scale, int window, void* out, float* lse, void* workspace,
     size_t workspace_bytes, dspark_stream_t stream) {
     using namespace dspark;
-    if (B < 1 || B > 65535 || rows < 0 || rows > 0x7fffffffll || max_rows < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 ||
+    if (B < 1 || B > 65535 || rows < 0 || rows > 0x7fffffffll || max_rows < (rows > 0 ? 1 : 0) || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 ||
         Hq > 1024 || D < 8 || D > 256 || D % 8 != 0 || page < 1 || max_blocks < 1 || num_blocks < 1 ||
         ld_table < max_blocks || window < 0)
         return DSPARK_ERR_INVALID_ARGUMENT;

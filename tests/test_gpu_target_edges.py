@@ -89,6 +89,12 @@ def test_pages_before_the_window_may_be_gone(dsv, lens, Hq, Hkv, D, page, window
     assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
 
 
+def test_attention_of_an_empty_step(dsv):  # noqa: F811
+    c = _attend_case(34, [(20, 0), (3, 0)], 4, 2, 64, 16, "bf16", "bf16", 0)
+    out, code = _run_attend(dsv, dict(c, max_rows=0))
+    assert code[0] == 0 and out["out"].shape == (0, 4, 64)
+
+
 # -------------------------------------------------------------------- plan ---
 @pytest.mark.parametrize("B,first,second", [(1500, 3, 1027), (1500, 1027, 3), (9, 1, 2), (2100, 2049, 1025)])
 def test_plan_tells_the_first_reason(dsv, B, first, second):  # noqa: F811
