@@ -17,12 +17,18 @@ namespace dspark {
 namespace {
 
 constexpr int kItems = 4;
+constexpr int kThreads = 128;
 constexpr int kMaxRows = 256;                   // of a block
+// Rows up to which a call is one launch: its first block clears the status and looks at all slots
+// instead of a clearing launch and every block at its own.  us in a graph so and with the clearing
+// launch (8 heads of 128, bf16): 16 rows 2.2 and 2.9, 256 rows 2.7 and 3.1, 1024 rows 4.6 and 3.6.
+constexpr int64_t kAlone = 256;
 
 struct WriteArgs {
     int64_t rows, k_stride, v_stride, slots;    // strides in elements
     int heads, D, page, rows_per_block, parts;  // parts: 8-element pieces of one row of one tensor
     int lanes;                                  // threads of a row: a power of two, or all
+    bool alone;                                 // no clearing came before
     const void *k, *v;
     const int64_t* slot;
     const float *k_scale, *v_scale;
@@ -74,28 +80,29 @@ __device__ __forceinline__ uint32_t stored(float x, float y, float s, float inv)
     return __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x, s), __fdiv_rn(y, s)), __NV_SATFINITE, __NV_E4M3);
 }
 
-template <typename T, bool kFp8, int kThreads>
+template <typename T, bool kFp8>
 __global__ void __launch_bounds__(kThreads) write_kv(WriteArgs p) {
     __shared__ int64_t s_to[kMaxRows];          // a row's first element of head 0 in the cache, -1: none
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_block;
     const int64_t left = p.rows - row0;
     const int n = left < p.rows_per_block ? static_cast<int>(left) : p.rows_per_block;
-    if (gridDim.x == 1) {                       // alone: no clearing came before
-        if (threadIdx.x < 4) reinterpret_cast<uint32_t*>(p.status)[threadIdx.x] = 0;
-        __syncthreads();
-    }
-    for (int r = threadIdx.x; r < n; r += kThreads) {
+    // Alone, the first block clears the status and looks at the slots of all rows.
+    const bool all = p.alone && blockIdx.x == 0;
+    if (all && threadIdx.x < 4) reinterpret_cast<uint32_t*>(p.status)[threadIdx.x] = 0;
+    bool past = false;
+    for (int r = threadIdx.x; r < (all ? static_cast<int>(p.rows) : n); r += kThreads) {
         const int64_t slot = p.slot[row0 + r];
         int64_t to = -1;
         if (slot >= p.slots) {
-            tell(p.status, DSPARK_ERR_DEVICE_CHECK, 1);
+            past = true;
         } else if (slot >= 0) {
             const int64_t block = (slot >> 32) == 0 ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.page) : slot / p.page;
             to = (block * p.heads * p.page + (slot - block * p.page)) * p.D;
         }
-        s_to[r] = to;
+        if (r < n) s_to[r] = to;
     }
     __syncthreads();
+    if (past && (all || !p.alone)) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 1);
     const int groups = kThreads / p.lanes, mine = threadIdx.x / p.lanes, per_head = p.D / 8;
     for (int e = threadIdx.x % p.lanes; e < 2 * p.parts; e += p.lanes) {
         const bool is_v = e >= p.parts;
@@ -168,32 +175,23 @@ extern "C" dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int pag
     p.slots = static_cast<int64_t>(num_blocks) * page;
     p.heads = Hkv, p.D = D, p.page = page;
     p.parts = static_cast<int>(width / 8);
-    // Few rows (64 KB, what 1024 threads move in one go) are one block, which clears the status itself.
-    // Otherwise four rows a thread, and fewer where the rows would not fill the GPU.
-    const bool one = rows <= kMaxRows && rows * 2 * p.parts <= 1024 * kItems;
-    const int threads = one ? 1024 : 128;
+    // Four rows a thread, and fewer where the rows would not fill the GPU.
     p.lanes = 1;
-    while (p.lanes < threads && p.lanes < 2 * p.parts) p.lanes *= 2;
-    const int groups = threads / p.lanes;
-    p.rows_per_block = one ? kMaxRows : groups * kItems < kMaxRows ? groups * kItems : kMaxRows;
-    while (!one && p.rows_per_block > 1 && (rows + p.rows_per_block - 1) / p.rows_per_block < 2 * sm_count(current_device()))
+    while (p.lanes < kThreads && p.lanes < 2 * p.parts) p.lanes *= 2;
+    const int groups = kThreads / p.lanes;
+    p.rows_per_block = groups * kItems < kMaxRows ? groups * kItems : kMaxRows;
+    while (p.rows_per_block > 1 && (rows + p.rows_per_block - 1) / p.rows_per_block < 2 * sm_count(current_device()))
         p.rows_per_block /= 2;
+    p.alone = rows <= kAlone;
     p.k = k, p.v = v, p.slot = slot, p.k_scale = k_scale, p.v_scale = v_scale, p.kc = k_cache, p.vc = v_cache;
     p.status = static_cast<StatusBlock*>(workspace);
     const unsigned grid = static_cast<unsigned>((rows + p.rows_per_block - 1) / p.rows_per_block);
     const bool bf16 = dt == DSPARK_BF16, fp8 = cache_dt == DSPARK_E4M3;
-    if (grid == 1) {
-        // (also rows that are one block of the other kind: it clears the status as well)
-        if (one) {
-            if (bf16) (fp8 ? write_kv<__nv_bfloat16, true, 1024> : write_kv<__nv_bfloat16, false, 1024>)<<<1, 1024, 0, s>>>(p);
-            else (fp8 ? write_kv<float, true, 1024> : write_kv<float, false, 1024>)<<<1, 1024, 0, s>>>(p);
-        } else {
-            if (bf16) (fp8 ? write_kv<__nv_bfloat16, true, 128> : write_kv<__nv_bfloat16, false, 128>)<<<1, 128, 0, s>>>(p);
-            else (fp8 ? write_kv<float, true, 128> : write_kv<float, false, 128>)<<<1, 128, 0, s>>>(p);
-        }
+    void (*kernel)(WriteArgs) = bf16 ? (fp8 ? write_kv<__nv_bfloat16, true> : write_kv<__nv_bfloat16, false>)
+                                     : (fp8 ? write_kv<float, true> : write_kv<float, false>);
+    if (p.alone) {
+        kernel<<<grid, kThreads, 0, s>>>(p);
         return launch_status();
     }
-    void (*kernel)(WriteArgs) = bf16 ? (fp8 ? write_kv<__nv_bfloat16, true, 128> : write_kv<__nv_bfloat16, false, 128>)
-                                     : (fp8 ? write_kv<float, true, 128> : write_kv<float, false, 128>);
-    return launch_cleared(workspace, kStatusBytes, kernel, dim3(grid), 128, 0, s, p);
+    return launch_cleared(workspace, kStatusBytes, kernel, dim3(grid), kThreads, 0, s, p);
 }

@@ -137,7 +137,7 @@ def test_adjust_with_a_history_of_no_columns(dsv):  # noqa: F811
     assert _code(ws) == [6, 2]
 
 
-# --------------------------------------------------- streams ---
+# ---------------------------------------- streams and graphs ---
 def _sleep(ms=50):
     torch.cuda._sleep(int(ms * 2e6))
 
@@ -171,3 +171,38 @@ def test_memory_made_for_another_stream(dsv, call):  # noqa: F811
     out = run(side)
     torch.cuda.synchronize()
     assert (later == 77).all() and not (out == 77).all()
+
+
+def _write_case(seed, n=40):
+    g = torch.Generator().manual_seed(seed)
+    k, v = (torch.randn((n, 8, 128), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    slot = torch.randperm(6 * 16, generator=g)[:n].cuda()
+    want = torch.zeros((2, 6, 8, 16, 128), dtype=torch.bfloat16, device="cuda")
+    for x, to in ((k, want[0]), (v, want[1])):
+        to[slot // 16, :, slot % 16] = x
+    return k, v, slot, want
+
+
+@pytest.mark.parametrize("n", [3, 40, 90])
+def test_write_in_a_graph_and_on_another_stream(dsv, n):  # noqa: F811
+    k, v, slot, want = _write_case(81, n)
+    kc, vc = torch.zeros_like(want[0]), torch.zeros_like(want[0])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    dsv.dspark_write_kv(k, v, slot, kc, vc, stream=s)
+    s.synchronize()
+    assert torch.equal(kc, want[0]) and torch.equal(vc, want[1])
+    ws, graph = _ws(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dsv.dspark_write_kv(k, v, slot, kc, vc, workspace=ws)
+    for seed in (82, 83):
+        k2, v2, slot2, want = _write_case(seed, n)
+        k.copy_(k2), v.copy_(v2), slot.copy_(slot2), kc.zero_(), vc.zero_()
+        graph.replay()
+        assert _code(ws)[0] == 0 and torch.equal(kc, want[0]) and torch.equal(vc, want[1])
+    slot[0] = 96                                         # past the cache: told by the replay, gone in the next
+    graph.replay()
+    assert _code(ws) == [6, 1]
+    slot[0] = -1
+    graph.replay()
+    assert _code(ws)[0] == 0
