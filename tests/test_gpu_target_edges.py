@@ -121,6 +121,26 @@ def test_plan_refuses_a_negative_advance(dsv, B):  # noqa: F811
     _same_plan(got, want)
 
 
+# ------------------------------------------------------------------- write ---
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1.0, 0.0625, 2.0 ** -140, 3.0e38])
+def test_write_ties_and_far_scales(dsv, dtype, scale):  # noqa: F811
+    """Scales of a power of two make a sixteenth of bf16 rows exact ties; scales whose reciprocal is not
+    a normal number take the quotient proper."""
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator().manual_seed(51)
+    k = (torch.randn((90, 2, 64), generator=g) * 50 * min(scale, 1e30)).to(t).cuda()
+    kc, vc = (torch.zeros((8, 2, 16, 64), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+    s = torch.full((2,), scale, device="cuda")
+    slot = torch.randperm(128, generator=g)[:90].cuda()
+    dsv.dspark_write_kv(k, k, slot, kc, vc, k_scale=s, v_scale=s)
+    f = lambda x: x.double().cpu().numpy()  # noqa: E731
+    zero = np.zeros((8, 2, 16, 64))
+    want = target.write_kv(f(k), f(k), slot.tolist(), zero, zero, f(s), f(s))[0]
+    np.testing.assert_array_equal(f(kc), want)
+    np.testing.assert_array_equal(f(vc), want)
+
+
 # ------------------------------------------------------------------ adjust ---
 def test_adjust_with_a_history_of_no_columns(dsv):  # noqa: F811
     """Requests without a token yet: the history has no columns, and its lengths are zero."""
