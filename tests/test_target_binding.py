@@ -28,6 +28,8 @@ class _Elsewhere:
 def test_tensors_of_another_device_are_refused(dsv, monkeypatch):
     """The library launches on the current device: tensors of another one would be read from there."""
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
+    monkeypatch.setattr(dsv._binding, "_several", None)
     x = _Elsewhere()
     for call in (lambda: dsv.dspark_plan_rows(x, x, x, x, x, x, 16, 8), lambda: dsv.dspark_write_kv(x, x, x, x, x),
                  lambda: dsv.dspark_paged_attention(x, x, x, x, x, x, 4), lambda: dsv.dspark_adjust_logits(x)):
