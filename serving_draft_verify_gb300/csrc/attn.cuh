@@ -193,46 +193,56 @@ struct Piece {
     __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units; }
 };
 
-// Walks the block's units piece by piece (every thread the same way).
+// Walks the block's units piece by piece (every thread the same way).  The first piece is looked for
+// tile by tile; a further one starts the segment after the last (a prompt of 8192 rows has thousands).
 template <int M, int KT>
 struct Walk {
     const Args& p;
-    int64_t at, last, req_first, per_head;
-    int b;
+    int64_t at, last;
+    int b, h, tile, u0;               // u0: units of the segment before the piece, -1 behind a segment
     Request r;
     __device__ __forceinline__ Walk(const Args& args, const Start& s)
-        : p(args), at(s.first), last(s.last), req_first(s.first - s.into), per_head(s.a.units), b(s.b), r(s.a.r) {}
-    __device__ __forceinline__ bool next(Piece& out) {
-        if (at >= last) return false;
-        while (at >= req_first + p.Hkv * per_head) {
-            req_first += p.Hkv * per_head;
-            if (++b >= p.B) return false;      // only where the lengths change under the call
-            const Asked a = ask<M, KT>(p, b, false);
-            r = a.r;
-            per_head = a.units;
-        }
-        int64_t into = at - req_first;
-        out.h = static_cast<int>(div_pos(into, per_head));
-        into -= out.h * per_head;
-        int t = 0;
-        Span sp = span_of<M, KT>(p, r, 0);
+        : p(args), at(s.first), last(s.last), b(s.b), h(0), tile(0), u0(0), r(s.a.r) {
+        if (at >= last) return;
+        h = static_cast<int>(div_pos(s.into, s.a.units));
+        int64_t into = s.into - h * s.a.units;
         const int nt = tiles_of<M>(p, r);
 #pragma unroll 1
-        while (into >= sp.units(KT) && t + 1 < nt) {
-            into -= sp.units(KT);
-            sp = span_of<M, KT>(p, r, ++t);
+        for (; tile + 1 < nt; ++tile) {
+            const int n = span_of<M, KT>(p, r, tile).units(KT);
+            if (into < n) break;
+            into -= n;
+        }
+        u0 = static_cast<int>(into);
+    }
+    __device__ __forceinline__ bool next(Piece& out) {
+        if (at >= last) return false;
+        if (u0 < 0) {
+            u0 = 0;
+            if (++tile >= tiles_of<M>(p, r)) {
+                tile = 0;
+                if (++h >= p.Hkv) {
+                    h = 0;
+                    do {
+                        if (++b >= p.B) return false;      // only where the lengths change under the call
+                        r = request_of(p, b, false);
+                    } while (r.n == 0);
+                }
+            }
         }
         out.r = r;
         out.b = b;
-        out.tile = t;
-        out.span = sp;
-        out.units = sp.units(KT);
-        out.u0 = static_cast<int>(into);
-        out.seg_first = at - into;
-        const int64_t left = last - at, rest = out.units - into;
+        out.h = h;
+        out.tile = tile;
+        out.span = span_of<M, KT>(p, r, tile);
+        out.units = out.span.units(KT);
+        out.u0 = u0;
+        out.seg_first = at - u0;
+        const int64_t left = last - at, rest = out.units - u0;
         const int n = static_cast<int>(left < rest ? left : rest);
-        out.u1 = out.u0 + n;
+        out.u1 = u0 + n;
         at += n;
+        u0 = -1;
         return true;
     }
 };

@@ -95,6 +95,38 @@ def test_attention_of_an_empty_step(dsv):  # noqa: F811
     assert code[0] == 0 and out["out"].shape == (0, 4, 64)
 
 
+def _dense(c):
+    """The oracle of one request by dense float64 products on the GPU (for thousands of rows)."""
+    q, page, D = c["q"].double(), c["k_cache"].shape[2], c["q"].shape[2]
+    n, Hq = q.shape[:2]
+    total = int(c["length"][0]) + n
+    ids = c["block_table"][0, :-(-total // page)].long()
+    Hkv = c["k_cache"].shape[1]
+    out, weight = torch.empty_like(q), torch.empty_like(q)
+    lse, size = (torch.empty((n, Hq), dtype=torch.float64, device="cuda") for _ in range(2))
+    hide = torch.arange(total, device="cuda")[None] > (total - n + torch.arange(n, device="cuda"))[:, None]
+    for h in range(Hq):
+        g = h // (Hq // Hkv)
+        k, v = (x[ids, g].double().reshape(-1, D)[:total] * (1.0 if s is None else s[g].double())
+                for x, s in ((c["k_cache"], c["k_scale"]), (c["v_cache"], c["v_scale"])))
+        s = (q[:, h] @ k.T * D ** -0.5).masked_fill(hide, -float("inf"))
+        lse[:, h] = torch.logsumexp(s, 1)
+        p = torch.exp(s - lse[:, h, None])
+        out[:, h], weight[:, h] = p @ v, p @ v.abs()
+        size[:, h] = (q[:, h].abs() @ k.abs().T * D ** -0.5).masked_fill(hide, 0).amax(1)
+    np_ = lambda x: x.cpu().numpy()  # noqa: E731
+    return dict(out=np_(out), lse=np_(lse), weight=np_(weight), size=np_(size), keys=total - n + 1 + np.arange(n))
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS, ids=["-".join(k) for k in KINDS])
+@pytest.mark.parametrize("before,rows,Hq,Hkv,D", [(0, 2500, 8, 2, 64), (777, 1300, 4, 1, 128), (100, 600, 4, 2, 256)])
+def test_prompts_of_thousands_of_rows(dsv, dtype, cache, before, rows, Hq, Hkv, D):  # noqa: F811
+    c = _attend_case(36, [(before, rows)], Hq, Hkv, D, 16, dtype, cache, 0, poison=False)
+    out, code = _run_attend(dsv, c)
+    assert code[0] == 0
+    _check_attend(out, _dense(c), dtype, D)
+
+
 # -------------------------------------------------------------------- plan ---
 @pytest.mark.parametrize("B,first,second", [(1500, 3, 1027), (1500, 1027, 3), (9, 1, 2), (2100, 2049, 1025)])
 def test_plan_tells_the_first_reason(dsv, B, first, second):  # noqa: F811
