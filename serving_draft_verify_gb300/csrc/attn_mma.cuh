@@ -76,7 +76,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // output's own rounding of 2^-8 covers.  (Below 2^-103 the rest leaves bf16's normal numbers.)
 __device__ __forceinline__ void split_bf16(float e0, float e1, uint32_t& high, uint32_t& low) {
     constexpr float kOnTop = 1.f + 0x1p-23f;
-    high = __byte_perm(__float_as_uint(e0), __float_as_uint(e1), 0x7632);
+    asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(high) : "f"(e1), "f"(e0));
     low = pack_bf16(fmaf(e0, kOnTop, -bf16lo(high)), fmaf(e1, kOnTop, -bf16hi(high)));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {

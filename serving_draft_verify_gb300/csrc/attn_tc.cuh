@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         uint64_t *full = keys ? bars.k_full : bars.v_full, *empty = keys ? bars.k_empty : bars.v_empty;
         unsigned char* ring = keys ? s_k : s_v;
         const uint64_t policy = policy_evict_normal();
+        const int shift = __ffs(box) - 1;                        // a box is a power of two of rows
         for (uint32_t n = 0; next_piece(walk, pc); ++n) {
             if (!keys) {
                 wait(&bars.q_empty[n & 1], (n >> 1) + 1);
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int u = pc.u0; u < pc.u1; ++u, ++i, k0 += kTcKT) {
                 // boxes wholly before the first key that the tile sees stay away: the softmax makes those
                 // values 0, as it does those past the last key
-                const int stage = i & 1, before = max(seen - k0, 0) / box, boxes = (min(kTcKT, hi - k0) + box - 1) / box - before;
+                const int stage = i & 1, before = max(seen - k0, 0) >> shift, boxes = ((min(kTcKT, hi - k0) + box - 1) >> shift) - before;
                 // lane l finds the row of box l; lane 0 issues them all (an instruction that several
                 // lanes issue goes lane by lane, at several times the cost)
                 int y = 0;
