@@ -475,13 +475,18 @@ dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int page, int num_
  * own, with window > 0 only the last `window` of them.  Query head hq reads key head
  * hq / (Hq / Hkv):
  *   s_j = scale q . k_j,  lse = ln sum_j exp(s_j),  out = sum_j exp(s_j - lse) v_j
- * in float32, out rounded once to `dt`.  Keys and values a row does not see have no
- * part in it, whatever they hold.  Table entries of pages past the last position, and with a
- * window of pages wholly before position len[b] - window + 1, are not read.
+ * in float32, out rounded once to `dt`.  For bf16 rows the weights of the second sum count
+ * at least 15 bits (bf16 caches; a visible value of +-inf stays that down to weights of 2^-103
+ * of the largest) or 11 bits (8-bit caches, where q's elements below 2^-25 of their row's
+ * largest lose bits too), below out's own rounding; lse counts them whole.
+ * Keys and values a row does not see have no part in it, whatever they hold.  Table entries
+ * of pages past the last position, and with a window of pages wholly before position
+ * len[b] - window + 1, are not read.
  *   q: row i at i * q_stride elements, Hq heads of D adjacent elements in `dt`, 16-byte
  *   aligned rows; out [rows][Hq][D] in `dt`; lse [rows][Hq] float32 or NULL.
  *   rows: what q and out have room for (row_offset[B] or more; the rest is not
- *   touched; 0: nothing is launched); max_rows: the most rows of one request.
+ *   touched; 0: nothing is launched); max_rows: the most rows of one request.  It also
+ *   chooses the kernel, so a bound far above the rows there are costs time.
  *   cache_dt, k_scale, v_scale as for dspark_write_kv: a stored value stands for
  *   itself times scale[head].
  * The work is divided evenly over the GPU by the lengths on the device, so a call can be

@@ -12,11 +12,12 @@ namespace dspark {
 namespace attn {
 namespace {
 
-// Query rows of a key head above which tcgen05 takes over.  32 heads on 8, us on the warp-level
-// instructions and on tcgen05: 64 requests of up to 4000 keys, 12 rows a request (48 query rows) 188 and
-// 205, 16 rows 229 and 222, 17 rows 284 and 240; 128 requests of up to 6000 keys, 17 rows 723 and 498.
-// Short caches favour the former longer (256 requests of up to 500 keys, 16 rows: 242 and 302), but the
-// lengths are on the device.
+// Query rows of a key head above which tcgen05 takes over, by max_rows.  32 heads on 8, us on the
+// warp-level instructions and on tcgen05: 64 requests of up to 4000 keys, 12 rows a request (48 query
+// rows) 188 and 205, 16 rows 229 and 222, 17 rows 284 and 240; 128 requests of up to 6000 keys, 17 rows
+// 723 and 501.  Short caches favour the former longer (256 requests of up to 500 keys, 16 rows: 242 and
+// 302), and so do steps whose requests have far fewer rows than max_rows (64 requests of one row, up to
+// 16384 keys: 371 and, called with max_rows 17, 629), but lengths and rows are on the device.
 constexpr int kWide = 64;
 
 // ------------------------------------------------------------ float32 rows ---

@@ -21,7 +21,7 @@
 // exchange their maxima in those units alone.  The instruction cache is a bound here: with six
 // roles in one kernel, what runs once a piece or never (the walk, the joining, waits that have to
 // wait) stands in functions of its own.
-// 128 requests of up to 6000 keys, up to 17 rows, 32 heads on 8, pages of 16: 498 us for 1.65 GB (3.3
+// 128 requests of up to 6000 keys, up to 17 rows, 32 heads on 8, pages of 16: 501 us for 1.65 GB (3.3
 // TB/s).  What bounds it is the copying: a box cannot leave its page, and boxes of 16 rows of 128
 // bytes take some 150 cycles each, 4900 cycles a unit (pages of 32 rows and more: 3800, the softmax).
 // Boxes of whole rows, a softmax in two groups by turns and copies by threads were all slower.

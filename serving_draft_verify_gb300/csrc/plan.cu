@@ -15,8 +15,8 @@
 // request's tile.  The last block to finish (a counter, nobody waits) writes the
 // per-request state, so the state may be updated in place.
 //
-// Bound by latency (16 bytes a row and a few words a request move): a call in a graph takes 3.4 us
-// for 16 requests (one block of 256 threads) and 9.9 us for 1024 requests with 20,000 rows.
+// Bound by latency (16 bytes a row and a few words a request move): a call in a graph takes 3.5 us
+// for 16 requests (one block of 256 threads) and 9.8 us for 1024 requests with 20,000 rows.
 #include "launch.cuh"
 
 namespace dspark {
@@ -288,7 +288,8 @@ extern "C" dspark_status_t dspark_plan_rows(int B, int page, int max_blocks, int
                rows,     held,      free_state, free_ring,      block_table, len_out, held_out,  free_state_out,
                row_offset, row_request, position, slot,         static_cast<StatusBlock*>(workspace),
                reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + kStatusBytes)};
-    // a small step is one small block: its scans and barriers are the call's time
+    // a small step is one small block: its scans and barriers are the call's time (16 requests in a graph:
+    // 3.5 us, with the large block 4.4)
     const bool small = B <= 256 && max_rows <= 256;
     const int64_t tile = small ? 256 : 1024;
     const int64_t row_tiles = (max_rows + tile - 1) / tile, req_tiles = (B + tile - 1) / tile;
