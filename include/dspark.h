@@ -2,7 +2,7 @@
  * dspark.h -- C ABI of the DSpark draft / schedule / verify / accept-rate path
  * for one NVIDIA GB300 GPU (sm_103a).
  *
- * Ten operations, each a hand-written CUDA kernel sequence:
+ * Thirteen operations, each a hand-written CUDA kernel sequence:
  *   dspark_draft_block      semi-autoregressive draft block, confidence, survival
  *   dspark_schedule_prefix  hardware-aware prefix scheduler (Algorithm 1)
  *   dspark_verify           rejection-sampling verification + residual/bonus token
@@ -11,6 +11,9 @@
  *   dspark_decode_rounds    draft -> schedule -> verify rounds, anchor carried
  *   dspark_plan_rows        pages, positions and cache slots of the rows a step adds
  *   dspark_write_kv         the rows' keys and values into the paged cache
+ *   dspark_rotate           rotary positions of rows of heads, and their gradient
+ *   dspark_rotate_write_kv  queries rotated, keys rotated and stored, values stored, in one launch
+ *   dspark_read_kv          rows of the paged cache back as float32 or bf16
  *   dspark_paged_attention  the rows' attention over the paged cache
  *   dspark_adjust_logits    penalties, biases and grammar masks on the target rows
  * (and _ex variants of the draft and verify calls for the gated / RNN heads)
@@ -73,9 +76,10 @@ typedef enum {
     DSPARK_ERR_DEVICE_CHECK = 6        /* device status only: a device-side input check failed */
 } dspark_status_t;
 
-/* DSPARK_E4M3 (8 bits: sign, 4 exponent, 3 mantissa bits, largest 448) is a type of
- * caches only. */
-typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_E4M3 = 2 } dspark_dtype_t;
+/* DSPARK_E4M3 (8 bits: sign, 4 exponent, 3 mantissa bits, largest 448) and DSPARK_E2M1 (4
+ * bits: sign, 2 exponent bits, 1 mantissa bit, largest 6, with a scale for every 16 elements) are
+ * types of caches only. */
+typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_E4M3 = 2, DSPARK_E2M1 = 3 } dspark_dtype_t;
 
 typedef struct CUstream_st* dspark_stream_t;   /* same type as cudaStream_t */
 
@@ -407,7 +411,7 @@ dspark_status_t dspark_training_loss(int64_t rows, int V, dspark_dtype_t dt,
 /* ------------------------------------------------------------------------ *
  * The target model's side of a round.  Between the schedule and the verification
  * the target model runs over the rows of each request (the anchor and the scheduled
- * draft tokens, ell[b] + 1 of them, or a piece of a prompt); the four calls below
+ * draft tokens, ell[b] + 1 of them, or a piece of a prompt); the calls below
  * are the parts of that step that the cache and the tokens decide.  The pages leave
  * the target model to the serving engine (DeepSpec walkthrough sections 8.1 - 8.3:
  * target forward, then accept, then the cache cut back to what was accepted).
@@ -416,6 +420,12 @@ dspark_status_t dspark_training_loss(int64_t rows, int V, dspark_dtype_t dt,
  * head adjacent.  Slot s is row s % page of page s / page.  block_table [B][ld]
  * int32: entry j of request b names the page of its positions j page .. j page +
  * page - 1.  Any page size of at least 1 is taken.
+ *
+ * 4-bit caches (DSPARK_E2M1) are [num_blocks][Hkv] pages of dspark_kv_page_bytes() bytes: `page` rows
+ * of D / 2 bytes, element 2i in the low half of byte i; behind them `page` rows of D / 16 scales (e4m3), the
+ * bytes of a row rounded up to 4; the whole rounded up to 16.  An element stands for its code (0, 1/2,
+ * 1, 3/2, 2, 3, 4, 6, with a sign) times the scale of its block of 16 times the head's scale.
+ * D % 32 == 0, and a page's elements below 2^31 - 1024 (else DSPARK_ERR_UNSUPPORTED).
  *
  * Row planning.  Request b has len[b] rows in the cache before the last step's rows;
  * advance[b] of those stay (the accepted ones and the anchor: n_accept[b] + 1), and
@@ -452,15 +462,23 @@ dspark_status_t dspark_plan_rows(int B, int page, int max_blocks, int num_blocks
                                  int32_t* position, int64_t* slot, void* workspace, size_t workspace_bytes,
                                  dspark_stream_t stream);
 
+/* Bytes of one head's page in a cache of this type; 0 where there is none such. */
+size_t dspark_kv_page_bytes(int page, int D, dspark_dtype_t cache_dt);
+
 /* Stores keys and values of a step's rows: k_cache[slot[i]] = k[i], v likewise.
  *   k, v: row i at i * k_stride (v_stride) elements, Hkv heads of D adjacent elements
  *   in `dt` (a slice of a fused projection needs no copy); strides in elements, rows
  *   16-byte aligned.  slot [rows] int64; a negative one skips the row.
  *   cache_dt: `dt`, or DSPARK_E4M3 with k_scale, v_scale [Hkv] float32 > 0: then
  *   e4m3(x / scale[head]), nearest even, beyond +-448 the largest value, NaN kept.
+ *   DSPARK_E2M1 with k_scale, v_scale [Hkv] float32 in 2^-64 .. 2^64: for each block of 16
+ *   elements s = e4m3(max |x| (1 / (6 scale[head]))), then e2m1(x (1 / (s scale[head]))), every
+ *   operation in float32, nearest even, beyond the largest value the largest; a block with
+ *   s = 0 is stored as zeros, one with a NaN reads as NaN throughout.
  *   Two rows must not have one slot.
  * A slot past the last page sets DSPARK_ERR_DEVICE_CHECK and its row is skipped.
- * D % 8 == 0 (16 for DSPARK_E4M3), D <= 256, Hkv <= 1024.  rows == 0 launches nothing. */
+ * D % 8 == 0 (16 for DSPARK_E4M3, 32 for DSPARK_E2M1), D <= 256, Hkv <= 1024.  rows == 0 launches
+ * nothing. */
 size_t dspark_write_kv_workspace_size(void);
 
 dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int page, int num_blocks, dspark_dtype_t dt,
@@ -468,6 +486,81 @@ dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int page, int num_
                                 int64_t v_stride, const int64_t* slot, const float* k_scale,
                                 const float* v_scale, void* k_cache, void* v_cache, void* workspace,
                                 size_t workspace_bytes, dspark_stream_t stream);
+
+/* Rotary positions.  Pair i of a head (i < rot / 2) is its elements i and i + rot / 2, or 2i and 2i + 1
+ * where `interleaved` is 1; row n of x turns it by the angle a = position[n] freq[i]:
+ *   y1 = m (x1 cos a - x2 sin a),  y2 = m (x2 cos a + x1 sin a),  m = magnitude,
+ * and by -a where `transposed` is 1, which makes of a gradient with respect to y the one with respect to
+ * x.  Elements from rot on are copied.  The angle is taken modulo a turn before it is rounded, so far
+ * positions are as exact as near ones.
+ *   x, out: row n at n * x_stride (out_stride) elements, `heads` heads of D adjacent elements in
+ *   `dt`, rows 16-byte aligned; queries and keys that lie side by side are one call.  out may be x itself
+ *   with the same stride, or rows that share no element with x's (other slices of one buffer); anything
+ *   else that overlaps is refused.
+ *   position [rows] int32; a negative one: the row of out is not written.
+ *   freq [rot / 2] float32, device, |freq| < 2^26 (else that pair becomes NaN).
+ * D % 16 == 0, D <= 256; rot % 16 == 0, 16 <= rot <= D; heads <= 4096.  rows == 0 launches nothing. */
+size_t dspark_rotate_workspace_size(void);
+
+dspark_status_t dspark_rotate(int64_t rows, int heads, int D, int rot, int interleaved, int transposed,
+                              dspark_dtype_t dt, const void* x, int64_t x_stride, const int32_t* position,
+                              const float* freq, float magnitude, void* out, int64_t out_stride, void* workspace,
+                              size_t workspace_bytes, dspark_stream_t stream);
+
+/* Frequencies for dspark_rotate, on the host: freq (host) [rot / 2] and, unless NULL, the magnitude.  With
+ * f_i = base^(-2i / rot):
+ *   PLAIN   f_i
+ *   LINEAR  f_i / factor
+ *   BASE    base replaced by base factor^(rot / (rot - 2))
+ *   RAMP    (YaRN, Peng et al. 2023) f_i k_i + (f_i / factor) (1 - k_i), k_i = 1 - (i - a) / (b - a) kept
+ *           within 0 and 1, a = max(0, floor d(high)), b = min(rot - 1, ceil d(low)), d(t) = rot ln(original /
+ *           (2 pi t)) / (2 ln base): pairs that turn `high` times or more over the original length keep
+ *           their frequency; magnitude 0.1 ln(factor) + 1 (otherwise 1)
+ *   BANDS   the same with k_i = (original f_i / 2 pi - low) / (high - low).
+ * rot even, 2 .. 256 (above 2 for BASE); base > 1; factor >= 1; original > 0 and 0 < low < high for the last
+ * two.  No device is touched. */
+typedef enum {
+    DSPARK_ROTARY_PLAIN = 0,
+    DSPARK_ROTARY_LINEAR = 1,
+    DSPARK_ROTARY_BASE = 2,
+    DSPARK_ROTARY_RAMP = 3,
+    DSPARK_ROTARY_BANDS = 4
+} dspark_rotary_scaling_t;
+
+dspark_status_t dspark_rotary_frequencies(int rot, double base, dspark_rotary_scaling_t scaling, double factor,
+                                          double original, double low, double high, float* freq, float* magnitude);
+
+/* What a layer does between its projection and its attention, in one launch: q_out = q rotated,
+ * k_cache[slot[i]] = k[i] rotated, v_cache[slot[i]] = v[i].
+ * Arguments as for dspark_rotate and dspark_write_kv; a rotated key is rounded once, to what the cache
+ * holds.  A row with a negative position is skipped altogether; a negative slot skips only its keys
+ * and values.  Hq may be 0 (q, q_out NULL).  q_out may be q itself with the same stride; no other overlap with q, k
+ * or v.
+ * A slot past the last page sets DSPARK_ERR_DEVICE_CHECK and its keys and values are skipped.
+ * D % 16 == 0, rot % 16 == 0 (both 32 for DSPARK_E2M1), Hq <= 4096, Hkv <= 1024. */
+size_t dspark_rotate_write_kv_workspace_size(void);
+
+dspark_status_t dspark_rotate_write_kv(int64_t rows, int Hq, int Hkv, int D, int rot, int interleaved, int page,
+                                       int num_blocks, dspark_dtype_t dt, dspark_dtype_t cache_dt, const void* q,
+                                       int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                       int64_t v_stride, const int32_t* position, const float* freq, float magnitude,
+                                       const int64_t* slot, const float* k_scale, const float* v_scale, void* q_out,
+                                       int64_t q_out_stride, void* k_cache, void* v_cache, void* workspace,
+                                       size_t workspace_bytes, dspark_stream_t stream);
+
+/* Rows of the cache: k[i] = k_cache[slot[i]], v likewise, a stored value times its scales in float32 and
+ * rounded once to `dt` (DSPARK_F32 or DSPARK_BF16), whatever the cache's type.
+ *   slot [rows] int64, a negative one: the row is not written; slots may repeat.  k, v: row i at i * k_stride
+ *   (v_stride) elements, Hkv heads of D adjacent elements, 16-byte aligned rows, which share no memory
+ *   with each other or the caches.
+ * A slot past the last page sets DSPARK_ERR_DEVICE_CHECK and its row is not written.
+ * D % 8 == 0 (16 for DSPARK_E4M3, 32 for DSPARK_E2M1), D <= 256, Hkv <= 1024. */
+size_t dspark_read_kv_workspace_size(void);
+
+dspark_status_t dspark_read_kv(int64_t rows, int Hkv, int D, int page, int num_blocks, dspark_dtype_t dt,
+                               dspark_dtype_t cache_dt, const int64_t* slot, const void* k_cache, const void* v_cache,
+                               const float* k_scale, const float* v_scale, void* k, int64_t k_stride, void* v,
+                               int64_t v_stride, void* workspace, size_t workspace_bytes, dspark_stream_t stream);
 
 /* Attention of a step's rows over the cache (their own keys and values stored).  Row i
  * of request b (rows row_offset[b] .. row_offset[b+1] - 1 of q) stands at position
@@ -477,8 +570,9 @@ dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int page, int num_
  *   s_j = scale q . k_j,  lse = ln sum_j exp(s_j),  out = sum_j exp(s_j - lse) v_j
  * in float32, out rounded once to `dt`.  For bf16 rows the weights of the second sum count
  * at least 15 bits (bf16 caches; a visible value of +-inf stays that down to weights of 2^-103
- * of the largest) or 11 bits (8-bit caches, where q's elements below 2^-25 of their row's
- * largest lose bits too), below out's own rounding; lse counts them whole.
+ * of the largest) or 11 bits (8- and 4-bit caches, where weights below 2^-28 of the largest and q's
+ * elements below 2^-25 of their row's largest lose bits too), below out's own rounding; lse counts them
+ * whole.
  * Keys and values a row does not see have no part in it, whatever they hold.  Table entries
  * of pages past the last position, and with a window of pages wholly before position
  * len[b] - window + 1, are not read.
@@ -488,14 +582,14 @@ dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int page, int num_
  *   touched; 0: nothing is launched); max_rows: the most rows of one request.  It also
  *   chooses the kernel, so a bound far above the rows there are costs time.
  *   cache_dt, k_scale, v_scale as for dspark_write_kv: a stored value stands for
- *   itself times scale[head].
+ *   itself times scale[head] (and in 4-bit caches its block's scale).
  * The work is divided evenly over the GPU by the lengths on the device, so a call can be
  * captured in a graph and replayed with other lengths.  The same inputs give the same
  * bits.
  * DSPARK_ERR_DEVICE_CHECK: a request whose rows or length are negative, above max_rows,
  * above what q or its table have room for (detail 1; its rows are not written), or a
  * page id outside [0, num_blocks) (2; page 0 is read instead).
- * Hq % Hkv == 0, Hq <= 1024; D % 8 == 0 (16 for DSPARK_E4M3), D <= 256;
+ * Hq % Hkv == 0, Hq <= 1024; D % 8 == 0 (16 for DSPARK_E4M3, 32 for DSPARK_E2M1), D <= 256;
  * max_blocks page and max_rows Hq / Hkv below 2^31 - 1024. */
 size_t dspark_paged_attention_workspace_size(int D);
 

@@ -18,12 +18,14 @@ Modules
   rounds    several draft -> schedule -> verify rounds with the anchor carried
   heads     the gated and recurrent sequential heads (the rank-r row behind the bias)
   target    the target model's side: row planning, cache writes, paged attention, adjusted rows
+  rotary    rotary positions and their frequencies for long contexts
+  cache4    the cache in 4 bits: codes, block scales, page layout
 
 Parity status: every function is pinned by tests/test_oracle_*.py against
 closed forms, brute force, the generator's published vectors or distribution
 tests; none is "parity unpinned".
 """
-from . import philox, sampling, draft, schedule, verify, tv, loss, rounds, heads, target  # noqa: F401
+from . import philox, sampling, draft, schedule, verify, tv, loss, rounds, heads, target, rotary, cache4  # noqa: F401
 from .draft import draft_block, markov_bias, confidence, draft_logits  # noqa: F401
 from .schedule import schedule_prefix  # noqa: F401
 from .verify import verify as verify_round  # noqa: F401

@@ -12,6 +12,13 @@ from ._binding import (  # noqa: F401
     dspark_adjust_logits,
     dspark_paged_attention,
     dspark_plan_rows,
+    dspark_read_kv,
+    dspark_rotary_frequencies,
+    dspark_rotate,
+    dspark_rotate_write_kv,
+    kv4_cache,
+    kv4_page_bytes,
+    ROTARY_SCALINGS,
     dspark_write_kv,
     dspark_training_loss,
     dspark_decode_rounds,

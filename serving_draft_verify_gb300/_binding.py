@@ -18,6 +18,8 @@ DSPARK_OK = 0
 DSPARK_F32 = 0
 DSPARK_BF16 = 1
 DSPARK_E4M3 = 2
+DSPARK_E2M1 = 3
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
 MAX_GAMMA = 32
 
 _c_int, _c_i64, _c_u64, _c_size, _c_float = (ctypes.c_int, ctypes.c_int64, ctypes.c_uint64,
@@ -58,6 +60,15 @@ _SIGNATURES = {
     "dspark_write_kv_workspace_size": (_c_size, []),
     "dspark_write_kv": (_c_int, [_c_i64, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _p, _c_i64, _p, _c_i64, _p,
                                  _p, _p, _p, _p, _p, _c_size, _p]),
+    "dspark_kv_page_bytes": (_c_size, [_c_int, _c_int, _c_int]),
+    "dspark_rotate_workspace_size": (_c_size, []),
+    "dspark_rotate": (_c_int, [_c_i64] + [_c_int] * 6 + [_p, _c_i64, _p, _p, _c_float, _p, _c_i64, _p, _c_size, _p]),
+    "dspark_rotary_frequencies": (_c_int, [_c_int, ctypes.c_double, _c_int] + [ctypes.c_double] * 4 + [_p, _p]),
+    "dspark_rotate_write_kv_workspace_size": (_c_size, []),
+    "dspark_rotate_write_kv": (_c_int, [_c_i64] + [_c_int] * 9 + [_p, _c_i64, _p, _c_i64, _p, _c_i64, _p, _p, _c_float,
+                                        _p, _p, _p, _p, _c_i64, _p, _p, _p, _c_size, _p]),
+    "dspark_read_kv_workspace_size": (_c_size, []),
+    "dspark_read_kv": (_c_int, [_c_i64] + [_c_int] * 6 + [_p, _p, _p, _p, _p, _p, _c_i64, _p, _c_i64, _p, _c_size, _p]),
     "dspark_paged_attention_workspace_size": (_c_size, [_c_int]),
     "dspark_paged_attention": (_c_int, [_c_int, _c_i64] + [_c_int] * 9 + [_p, _c_i64, _p, _p, _p, _c_i64, _p, _p, _p,
                                         _p, _c_float, _c_int, _p, _p, _p, _c_size, _p]),
@@ -615,7 +626,7 @@ def _heads(t, dev, dtype, name):
         raise ValueError(f"{name} must be a 3-dimensional CUDA tensor of {dtype} on the call's device")
     n, heads, D = t.shape
     s = t.stride()
-    if (D > 1 and s[2] != 1) or (heads > 1 and s[1] != D):
+    if n > 0 and ((D > 1 and s[2] != 1) or (heads > 1 and s[1] != D)):      # no rows: any strides
         raise ValueError(f"{name}: the heads of a row must be adjacent")
     return s[0] if n > 1 else heads * D
 
@@ -685,44 +696,162 @@ def dspark_plan_rows(length, rows, held, free_state, free_ring, block_table, pag
     return out
 
 
-def _cache_code(k_cache, v_cache, k_scale, v_scale, dev, dtype):
-    """Type code of the caches and the addresses of their scales."""
+def kv4_page_bytes(page, D):
+    """Bytes of one head's page in a 4-bit cache."""
+    return (page * (D // 2 + -(-(D // 16) // 4) * 4) + 15) // 16 * 16
+
+
+def kv4_cache(num_blocks, Hkv, page, D, device="cuda"):
+    """A 4-bit cache of zeros: uint8 [num_blocks, Hkv, kv4_page_bytes(page, D)]."""
+    if page < 1 or D < 32 or D > 256 or D % 32:
+        raise ValueError(f"4-bit caches have pages of at least one row and heads of 32, 64, .. 256 elements, not {page} and {D}")
+    return torch.zeros((num_blocks, Hkv, kv4_page_bytes(page, D)), dtype=torch.uint8, device=device)
+
+
+def _cache_code(k_cache, v_cache, k_scale, v_scale, dev, dtype, D=None):
+    """Shape (num_blocks, Hkv, page, D) and type code of the caches, and the addresses of their scales.  D: of
+    the rows; a 4-bit cache's shape gives only its pages' bytes, from which it and the page follow."""
     shape = k_cache.shape
-    if len(shape) != 4:
-        raise ValueError("caches have the shape [num_blocks, Hkv, page, D]")
     t = k_cache.dtype
+    four = t is torch.uint8
+    if len(shape) != (3 if four else 4):
+        raise ValueError("caches have the shape [num_blocks, Hkv, page, D], 4-bit ones [num_blocks, Hkv, bytes]")
     _check_all(dev, ((k_cache, shape, t, "k_cache"), (v_cache, shape, t, "v_cache")))
-    if t is torch.float8_e4m3fn:
+    if four or t is torch.float8_e4m3fn:
         if k_scale is None or v_scale is None:
-            raise ValueError("8-bit caches need k_scale and v_scale")
+            raise ValueError("8-bit and 4-bit caches need k_scale and v_scale")
         _check_all(dev, ((k_scale, shape[1:2], torch.float32, "k_scale"), (v_scale, shape[1:2], torch.float32, "v_scale")))
-        return DSPARK_E4M3, k_scale.data_ptr(), v_scale.data_ptr()
-    if t is not dtype:
+        if not four:
+            return shape, DSPARK_E4M3, k_scale.data_ptr(), v_scale.data_ptr()
+        # a row has 20 bytes at least, more than a page is rounded up by: one page size fits, or none
+        page = shape[2] // (D // 2 + -(-(D // 16) // 4) * 4) if D >= 32 else 0
+        if D % 32 or page < 1 or kv4_page_bytes(page, D) != shape[2]:
+            raise ValueError(f"no 4-bit cache of heads of {D} has pages of {shape[2]} bytes")
+        return (shape[0], shape[1], page, D), DSPARK_E2M1, k_scale.data_ptr(), v_scale.data_ptr()
+    if dtype is not None and t is not dtype:
         raise TypeError(f"caches of {t} for rows of {dtype}")
     if k_scale is not None or v_scale is not None:
-        raise ValueError("only 8-bit caches have scales")
-    return _code_of(t), None, None
+        raise ValueError("only 8-bit and 4-bit caches have scales")
+    return shape, _code_of(t), None, None
 
 
 def dspark_write_kv(k, v, slot, k_cache, v_cache, k_scale=None, v_scale=None, workspace=None, stream=None):
     """Stores the rows' keys and values: k, v [n, Hkv, D] (rows at any stride: slices of a fused
     projection) at slot [n] int64 (negative: none) of the caches [num_blocks, Hkv, page, D], of
-    the rows' type or float8_e4m3fn with k_scale, v_scale [Hkv] float32."""
+    the rows' type or float8_e4m3fn, or 4-bit ones (kv4_cache), with k_scale, v_scale [Hkv] float32."""
     lib = load()
     dev = _device_of(k_cache, "k_cache")
-    nb, Hkv, page, D = k_cache.shape
     dt = _code_of(k.dtype)
     ks, vs = _heads(k, dev, k.dtype, "k"), _heads(v, dev, k.dtype, "v")
+    (nb, Hkv, page, D), code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, k.dtype, k.shape[2])
     n = k.shape[0]
     if k.shape != (n, Hkv, D) or v.shape != (n, Hkv, D):
         raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} for caches of {Hkv} heads of {D}")
     _on(slot, dev, (n,), torch.int64, "slot")
-    code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, k.dtype)
     ws = _scratch(lib.dspark_write_kv_workspace_size, k_cache, workspace, stream)
     _check("dspark_write_kv",
            lib.dspark_write_kv(n, Hkv, D, page, nb, dt, code, k.data_ptr(), ks, v.data_ptr(), vs, slot.data_ptr(), ksc,
                                vsc, k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(), ws.nbytes,
                                _stream_of(dev, stream)))
+
+
+def dspark_rotary_frequencies(rot, base=10000.0, scaling="plain", factor=1.0, original=0.0, low=1.0, high=32.0,
+                              device="cuda"):
+    """(freq [rot / 2] float32 on `device`, magnitude) for dspark_rotate; scaling: one of ROTARY_SCALINGS.  Made
+    once, on the host."""
+    freq = torch.empty(max(0, int(rot) // 2), dtype=torch.float32)
+    m = ctypes.c_float()
+    _check("dspark_rotary_frequencies",
+           load().dspark_rotary_frequencies(int(rot), float(base), ROTARY_SCALINGS[scaling], float(factor), float(original),
+                                            float(low), float(high), freq.data_ptr(), ctypes.addressof(m)))
+    return freq.to(device), m.value
+
+
+def dspark_rotate(x, position, freq, interleaved=False, transposed=False, magnitude=1.0, out=None, workspace=None,
+                  stream=None):
+    """Rotary positions of x [n, heads, D] (rows at any stride): the first 2 freq.numel() elements of a head
+    turn by position [n] int32 times freq [rot / 2] float32, backwards with `transposed` (the gradient).  Rows
+    of a negative position are not written.  `out` may be x itself."""
+    lib = load()
+    dev = _device_of(x, "x")
+    dt = _code_of(x.dtype)
+    xs = _heads(x, dev, x.dtype, "x")
+    n, heads, D = x.shape
+    if out is None:
+        out = _made_on(stream, lambda: dict(out=torch.empty((n, heads, D), dtype=x.dtype, device=x.device)))["out"]
+    os_ = _heads(out, dev, x.dtype, "out")
+    half, = freq.shape
+    if out.shape != x.shape:
+        raise ValueError(f"out {tuple(out.shape)} for x {tuple(x.shape)}")
+    _check_all(dev, ((position, (n,), torch.int32, "position"), (freq, (half,), torch.float32, "freq")))
+    ws = _scratch(lib.dspark_rotate_workspace_size, x, workspace, stream)
+    _check("dspark_rotate",
+           lib.dspark_rotate(n, heads, D, 2 * half, bool(interleaved), bool(transposed), dt, x.data_ptr(), xs,
+                             position.data_ptr(), freq.data_ptr(), float(magnitude), out.data_ptr(), os_, ws.data_ptr(),
+                             ws.nbytes, _stream_of(dev, stream)))
+    return out
+
+
+def dspark_rotate_write_kv(q, k, v, position, freq, slot, k_cache, v_cache, k_scale=None, v_scale=None, interleaved=False,
+                           magnitude=1.0, out=None, workspace=None, stream=None):
+    """dspark_rotate of q [n, Hq, D] and k [n, Hkv, D] with dspark_write_kv of the rotated keys and of v, in
+    one launch.  Returns the rotated queries (`out`, which may be q itself); q may be None."""
+    lib = load()
+    dev = _device_of(k_cache, "k_cache")
+    dt = _code_of(k.dtype)
+    ks, vs = _heads(k, dev, k.dtype, "k"), _heads(v, dev, k.dtype, "v")
+    (nb, Hkv, page, D), code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, k.dtype, k.shape[2])
+    n = k.shape[0]
+    if k.shape != (n, Hkv, D) or v.shape != (n, Hkv, D):
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} for caches of {Hkv} heads of {D}")
+    Hq = qs = os_ = 0
+    if q is not None:
+        qs, Hq = _heads(q, dev, k.dtype, "q"), q.shape[1]
+        if out is None:
+            out = _made_on(stream, lambda: dict(out=torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)))["out"]
+        os_ = _heads(out, dev, k.dtype, "out")
+        if q.shape != (n, Hq, D) or out.shape != q.shape:
+            raise ValueError(f"q {tuple(q.shape)} and out {tuple(out.shape)} for {n} rows of heads of {D}")
+    elif out is not None:
+        raise ValueError("out without q")
+    half, = freq.shape
+    _check_all(dev, ((position, (n,), torch.int32, "position"), (freq, (half,), torch.float32, "freq"),
+                     (slot, (n,), torch.int64, "slot")))
+    ws = _scratch(lib.dspark_rotate_write_kv_workspace_size, k_cache, workspace, stream)
+    _check("dspark_rotate_write_kv",
+           lib.dspark_rotate_write_kv(n, Hq, Hkv, D, 2 * half, bool(interleaved), page, nb, dt, code, _addr(q), qs,
+                                      k.data_ptr(), ks, v.data_ptr(), vs, position.data_ptr(), freq.data_ptr(),
+                                      float(magnitude), slot.data_ptr(), ksc, vsc, _addr(out), os_, k_cache.data_ptr(),
+                                      v_cache.data_ptr(), ws.data_ptr(), ws.nbytes, _stream_of(dev, stream)))
+    return out
+
+
+def dspark_read_kv(slot, k_cache, v_cache, k_scale=None, v_scale=None, D=None, dtype=torch.bfloat16, out=None,
+                   workspace=None, stream=None):
+    """Rows of the caches at slot [n] int64 (negative: not written) as `dtype`: dict k, v [n, Hkv, D].  `out` may
+    hold them (rows at any stride); without it a 4-bit cache's head size D has to be given."""
+    lib = load()
+    dev = _device_of(k_cache, "k_cache")
+    if out is not None:
+        D, dtype = out["k"].shape[2], out["k"].dtype
+    elif D is None:
+        D = k_cache.shape[-1] if k_cache.dim() == 4 else 0
+    (nb, Hkv, page, D), code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, None, D)
+    n, = slot.shape
+    if out is None:
+        new = lambda: torch.empty((n, Hkv, D), dtype=dtype, device=k_cache.device)  # noqa: E731
+        out = _made_on(stream, lambda: dict(k=new(), v=new()))
+    k, v = out["k"], out["v"]
+    ks, vs = _heads(k, dev, dtype, "k"), _heads(v, dev, dtype, "v")
+    if k.shape != (n, Hkv, D) or v.shape != (n, Hkv, D):
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} for {n} rows of {Hkv} heads of {D}")
+    _on(slot, dev, (n,), torch.int64, "slot")
+    ws = _scratch(lib.dspark_read_kv_workspace_size, k_cache, workspace, stream)
+    _check("dspark_read_kv",
+           lib.dspark_read_kv(n, Hkv, D, page, nb, _code_of(dtype), code, slot.data_ptr(), k_cache.data_ptr(),
+                              v_cache.data_ptr(), ksc, vsc, k.data_ptr(), ks, v.data_ptr(), vs, ws.data_ptr(), ws.nbytes,
+                              _stream_of(dev, stream)))
+    return out
 
 
 def dspark_paged_attention(q, row_offset, length, block_table, k_cache, v_cache, max_rows, scale=None, window=0,
@@ -733,14 +862,13 @@ def dspark_paged_attention(q, row_offset, length, block_table, k_cache, v_cache,
     Returns dict out [n, Hq, D] and lse [n, Hq] float32 (an `out` without lse skips it)."""
     lib = load()
     dev = _device_of(k_cache, "k_cache")
-    nb, Hkv, page, D = k_cache.shape
     B, = length.shape
     qs = _heads(q, dev, q.dtype, "q")
     n, Hq, qd = q.shape
+    (nb, Hkv, page, D), code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, q.dtype, qd)
     if qd != D:
         raise ValueError(f"q has heads of {qd}, the caches of {D}")
     width = block_table.shape[1]
-    code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, q.dtype)
     if out is None:
         out = _made_on(stream, lambda: dict(out=torch.empty((n, Hq, D), dtype=q.dtype, device=q.device),
                                             lse=torch.empty((n, Hq), dtype=torch.float32, device=q.device)))

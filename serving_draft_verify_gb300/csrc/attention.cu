@@ -6,6 +6,7 @@
 
 #include "attn.cuh"
 #include "attn_mma.cuh"
+#include "attn_mma4.cuh"
 #include "attn_tc.cuh"
 
 namespace dspark {
@@ -26,41 +27,49 @@ constexpr int kWide = 64;
 // (asynchronously, as they are stored) while this one's are computed on.
 constexpr int kSimtM = 16, kSimtKT = 32, kSimtThreads = 128;
 
-// Four adjacent stored elements, and two, as float.
+// Rows as they are staged, and four and two adjacent elements of one as float.
 template <typename C>
-__device__ __forceinline__ float4 four_of(const unsigned char* at);
+struct Staged {
+    __host__ __device__ static int bytes(int D) { return D * static_cast<int>(sizeof(C)) + 16; }
+    __device__ static float4 four(const unsigned char* row, int d, int) {
+        if constexpr (sizeof(C) == 4) return *reinterpret_cast<const float4*>(row + 4 * d);
+        else return static_cast<float4>(*reinterpret_cast<const __nv_fp8x4_e4m3*>(row + d));
+    }
+    __device__ static float2 two(const unsigned char* row, int d, int) {
+        if constexpr (sizeof(C) == 4) return *reinterpret_cast<const float2*>(row + 4 * d);
+        else return static_cast<float2>(*reinterpret_cast<const __nv_fp8x2_e4m3*>(row + d));
+    }
+};
+// 4 bits: the codes, behind them the scales.
+struct E2m1 {};
 template <>
-__device__ __forceinline__ float4 four_of<float>(const unsigned char* at) {
-    return *reinterpret_cast<const float4*>(at);
-}
-template <>
-__device__ __forceinline__ float4 four_of<__nv_fp8_e4m3>(const unsigned char* at) {
-    return static_cast<float4>(*reinterpret_cast<const __nv_fp8x4_e4m3*>(at));
-}
+struct Staged<E2m1> {
+    __host__ __device__ static int bytes(int D) { return (D / 2 + (D / 16 + 3) / 4 * 4 + 15) / 16 * 16 + 16; }
+    __device__ static float4 four(const unsigned char* row, int d, int D) {
+        uint32_t h[4];
+        e2m1x8_f16(*reinterpret_cast<const uint16_t*>(row + d / 2), h);
+        const float s = e4m3_float(row[D / 2 + d / 16]);
+        return make_float4(f16lo(h[0]) * s, f16hi(h[0]) * s, f16lo(h[1]) * s, f16hi(h[1]) * s);
+    }
+    __device__ static float2 two(const unsigned char* row, int d, int D) {
+        uint32_t h[4];
+        e2m1x8_f16(row[d / 2], h);
+        const float s = e4m3_float(row[D / 2 + d / 16]);
+        return make_float2(f16lo(h[0]) * s, f16hi(h[0]) * s);
+    }
+};
 template <typename C>
-__device__ __forceinline__ float2 two_of(const unsigned char* row, int d);
-template <>
-__device__ __forceinline__ float2 two_of<float>(const unsigned char* row, int d) {
-    return *reinterpret_cast<const float2*>(row + 4 * d);
-}
-template <>
-__device__ __forceinline__ float2 two_of<__nv_fp8_e4m3>(const unsigned char* row, int d) {
-    return static_cast<float2>(*reinterpret_cast<const __nv_fp8x2_e4m3*>(row + d));
-}
+constexpr bool kFour = std::is_same_v<C, E2m1>;
 template <typename C>
-constexpr int simt_row(int D) {                    // bytes of a staged row
-    return D * static_cast<int>(sizeof(C)) + 16;
-}
-template <typename C>
-constexpr size_t simt_smem(int D) {
-    return 4 * static_cast<size_t>(kSimtKT) * simt_row<C>(D) + (static_cast<size_t>(kSimtM) * D + kSimtM * kSimtKT) * 4;
+size_t simt_smem(int D) {
+    return 4 * static_cast<size_t>(kSimtKT) * Staged<C>::bytes(D) + (static_cast<size_t>(kSimtM) * D + kSimtM * kSimtKT) * 4;
 }
 
 template <typename C, int kCols>
 __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constant__ Args p) {
     constexpr int M = kSimtM, KT = kSimtKT;
     extern __shared__ float4 smem4[];
-    const int row_bytes = simt_row<C>(p.D), chunks = p.D * static_cast<int>(sizeof(C)) / 16;
+    const int row_bytes = Staged<C>::bytes(p.D), chunks = kFour<C> ? p.D / 32 : p.D * static_cast<int>(sizeof(C)) / 16;
     unsigned char* s_kv = reinterpret_cast<unsigned char*>(smem4);                  // [2 stages][keys, values][KT] rows
     float* s_q = reinterpret_cast<float*>(s_kv + 4 * KT * row_bytes);              // [M][D]
     float* s_p = s_q + M * p.D;                        // [M][KT]: exp of the scores, -1 where masked
@@ -75,32 +84,47 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
     Piece pc;
     while (walk.next(pc)) {
         const int left = pc.r.n * p.G - pc.tile * M, valid = left < M ? left : M;
-        // lane j has the place (in rows) of key j of a unit, found a unit ahead of its copy
-        auto find_rows = [&](int u) -> int64_t {
-            const int key = pc.span.lo + u * KT + lane;
-            if (u >= pc.u1 || key < pc.span.seen || key >= pc.span.hi) return 0;
-            const int blk = key / p.page;
-            return (static_cast<int64_t>(page_id(p, pc.b, blk)) * p.Hkv + pc.h) * p.page + (key - blk * p.page);
+        // lane j has the place (in bytes) of key j of a unit, and of its scales, found a unit ahead of its copy
+        struct Place {
+            int64_t row, scale;
         };
-        auto load = [&](int u, int64_t rows) {
+        auto find_rows = [&](int u) -> Place {
+            const int key = pc.span.lo + u * KT + lane;
+            if (u >= pc.u1 || key < pc.span.seen || key >= pc.span.hi) return Place{0, 0};
+            const int blk = key / p.page, in = key - blk * p.page;
+            const int64_t page = static_cast<int64_t>(page_id(p, pc.b, blk)) * p.Hkv + pc.h;
+            if constexpr (kFour<C>)
+                return Place{page * p.g4.whole + static_cast<int64_t>(in) * p.g4.code,
+                             page * p.g4.whole + p.g4.codes + static_cast<int64_t>(in) * p.g4.scale};
+            else return Place{(page * p.page + in) * (p.D * static_cast<int>(sizeof(C))), 0};
+        };
+        auto load = [&](int u, const Place& rows) {
             if (u < pc.u1) {
                 const uint32_t to = smem_u32(s_kv) + ((u - pc.u0) & 1) * 2 * KT * row_bytes;
                 const int n = KT * chunks;             // a multiple of the warp's 32
                 for (int e = tid; e < n; e += kSimtThreads) {
                     const int r = e / chunks, c = e - r * chunks;
-                    const int64_t row = __shfl_sync(0xffffffffu, rows, r);
+                    const int64_t row = __shfl_sync(0xffffffffu, rows.row, r);
                     const int key = pc.span.lo + u * KT + r;
                     const bool real = key >= pc.span.seen && key < pc.span.hi;
-                    const int64_t at = real ? row * (p.D * static_cast<int>(sizeof(C))) + c * 16 : 0;
+                    const int64_t at = real ? row + c * 16 : 0;
                     copy16(to + r * row_bytes + c * 16, static_cast<const char*>(p.kc) + at, real);
                     copy16(to + (KT + r) * row_bytes + c * 16, static_cast<const char*>(p.vc) + at, real);
+                }
+                if constexpr (kFour<C>) {
+                    const int key = pc.span.lo + u * KT + lane;
+                    const bool real = key >= pc.span.seen && key < pc.span.hi;
+                    for (int i = 4 * w; i < p.g4.scale; i += kSimtThreads / 8) {
+                        copy4(to + lane * row_bytes + p.g4.code + i, static_cast<const char*>(p.kc) + (real ? rows.scale + i : 0), real ? 4 : 0);
+                        copy4(to + (KT + lane) * row_bytes + p.g4.code + i, static_cast<const char*>(p.vc) + (real ? rows.scale + i : 0), real ? 4 : 0);
+                    }
                 }
             }
             copy_commit();
         };
         __syncthreads();                               // the last piece is done with the stages
         load(pc.u0, find_rows(pc.u0));
-        int64_t rows = find_rows(pc.u0 + 1);
+        Place rows = find_rows(pc.u0 + 1);
         const float qs = p.scale_log2 * (p.k_scale != nullptr ? p.k_scale[pc.h] : 1.f);
         for (int e = tid; e < M * p.D / 4; e += kSimtThreads) {
             const int m = e / (p.D / 4), d = (e - m * (p.D / 4)) * 4;
@@ -135,7 +159,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
                 float s[R] = {};
 #pragma unroll 4
                 for (int d = 0; d < p.D; d += 4) {
-                    const float4 k = four_of<C>(s_k + lane * row_bytes + d * sizeof(C));
+                    const float4 k = Staged<C>::four(s_k + lane * row_bytes, d, p.D);
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
                         const float4 q = *reinterpret_cast<const float4*>(s_q + (w + 4 * r) * p.D + d);
@@ -171,7 +195,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
                         float2 v[kCols / 2];
 #pragma unroll
                         for (int c = 0; c < kCols / 2; ++c)
-                            v[c] = 2 * lane + 64 * c < p.D ? two_of<C>(s_v + (j + i) * row_bytes, 2 * lane + 64 * c) : make_float2(0.f, 0.f);
+                            v[c] = 2 * lane + 64 * c < p.D ? Staged<C>::two(s_v + (j + i) * row_bytes, 2 * lane + 64 * c, p.D) : make_float2(0.f, 0.f);
 #pragma unroll
                         for (int r = 0; r < R; ++r) {
                             const float x = i == 0 ? e[r].x : i == 1 ? e[r].y : i == 2 ? e[r].z : e[r].w;
@@ -242,6 +266,14 @@ dspark_status_t launch_f32(const Args& p, cudaStream_t s) {
     return launch_simt<C, 8>(p, s);
 }
 
+// 4-bit caches: 32 query rows at a time where a request may have more than 16 of a key head.
+dspark_status_t launch_bf16_e2m1(const Args& p, cudaStream_t s) {
+    const bool one = static_cast<int64_t>(p.max_rows) * p.G <= 16;
+    if (p.D <= 64) return one ? launch_mma4<64, 1>(p, s) : launch_mma4<64, 2>(p, s);
+    if (p.D <= 128) return one ? launch_mma4<128, 1>(p, s) : launch_mma4<128, 2>(p, s);
+    return launch_mma4<256, 1>(p, s);
+}
+
 // bf16 rows: sixteen query rows at a time on the warp-level instructions, or 128 on tcgen05 where a
 // request may have more rows than kWide.
 template <bool kFp8>
@@ -274,9 +306,9 @@ extern "C" dspark_status_t dspark_paged_attention(
         Hq > 1024 || D < 8 || D > 256 || D % 8 != 0 || page < 1 || max_blocks < 1 || num_blocks < 1 ||
         ld_table < max_blocks || window < 0)
         return DSPARK_ERR_INVALID_ARGUMENT;
-    if ((dt != DSPARK_BF16 && dt != DSPARK_F32) || (cache_dt != dt && cache_dt != DSPARK_E4M3))
-        return DSPARK_ERR_INVALID_ARGUMENT;
-    if (cache_dt == DSPARK_E4M3 && (D % 16 != 0 || k_scale == nullptr || v_scale == nullptr))
+    const bool scaled = cache_dt == DSPARK_E4M3 || cache_dt == DSPARK_E2M1;
+    if ((dt != DSPARK_BF16 && dt != DSPARK_F32) || (cache_dt != dt && !scaled)) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (scaled && (D % (cache_dt == DSPARK_E4M3 ? 16 : 32) != 0 || k_scale == nullptr || v_scale == nullptr))
         return DSPARK_ERR_INVALID_ARGUMENT;
     if (!(scale == scale) || scale - scale != 0.f) return DSPARK_ERR_INVALID_ARGUMENT;
     const int64_t align = dt == DSPARK_BF16 ? 8 : 4;
@@ -288,6 +320,7 @@ extern "C" dspark_status_t dspark_paged_attention(
     if (static_cast<int64_t>(max_blocks) * page > 0x7fffffffll - 1024 ||
         static_cast<int64_t>(max_rows) * (Hq / Hkv) > 0x7fffffffll - 1024)
         return DSPARK_ERR_UNSUPPORTED;
+    if (cache_dt == DSPARK_E2M1 && static_cast<int64_t>(page) * D > 0x7fffffffll - 1024) return DSPARK_ERR_UNSUPPORTED;
     if (workspace == nullptr || !aligned256(workspace)) return DSPARK_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < dspark_paged_attention_workspace_size(D)) return DSPARK_ERR_WORKSPACE_TOO_SMALL;
     clear_stale_error();
@@ -298,13 +331,15 @@ extern "C" dspark_status_t dspark_paged_attention(
     p.num_blocks = num_blocks, p.max_rows = max_rows, p.window = window, p.rows = rows, p.ld_table = ld_table;
     p.q_stride = q_stride, p.q = q, p.row_offset = row_offset, p.length = len, p.table = block_table;
     p.kc = k_cache, p.vc = v_cache;
-    if (cache_dt == DSPARK_E4M3) p.k_scale = k_scale, p.v_scale = v_scale;
+    if (scaled) p.k_scale = k_scale, p.v_scale = v_scale;
+    p.g4 = page4_of(page, D);
     p.scale_log2 = scale * kLog2e, p.out = out, p.lse = lse;
     char* ws = static_cast<char*>(workspace);
     p.status = reinterpret_cast<StatusBlock*>(ws);
     p.counters = reinterpret_cast<uint32_t*>(ws + kStatusBytes);
     p.part_ml = reinterpret_cast<float*>(ws + kStatusBytes + attn::kCounterBytes);
     p.part_o = p.part_ml + 2 * static_cast<size_t>(attn::kMaxPartRows);
+    if (cache_dt == DSPARK_E2M1) return dt == DSPARK_BF16 ? attn::launch_bf16_e2m1(p, s) : attn::launch_f32<attn::E2m1>(p, s);
     const bool fp8 = cache_dt == DSPARK_E4M3;
     if (dt == DSPARK_BF16) return fp8 ? attn::launch_bf16<true>(p, s) : attn::launch_bf16<false>(p, s);
     return fp8 ? attn::launch_f32<__nv_fp8_e4m3>(p, s) : attn::launch_f32<float>(p, s);

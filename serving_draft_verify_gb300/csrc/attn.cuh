@@ -19,6 +19,7 @@
 // who came last.
 #pragma once
 
+#include "kv_store.cuh"
 #include "launch.cuh"
 
 namespace dspark {
@@ -31,6 +32,7 @@ struct Args {
     const int32_t *row_offset, *length, *table;
     const void *kc, *vc;
     const float *k_scale, *v_scale;
+    Page4 g4;                         // of a 4-bit cache
     float scale_log2;                 // scale * log2(e)
     void* out;
     float* lse;

@@ -1,0 +1,536 @@
+// Attention over a 4-bit cache (kv_store.cuh has the format): 16 or 32 query rows of a key head
+// at a time on the warp-level tensor instructions.
+//
+// The work is divided as in attn_mma.cuh: each of a block's four warps takes 32 keys of every unit of
+// 128, with a ring of its own, its own running maximum and sum and its own rows of the output.
+//
+//   S = Q K^T    m16n8k16 in f16, keys as columns,
+//   P = 2^(S - m), with a factor 2^14 that the sum carries too, rounded to 11 bits,
+//   O += P V.
+//
+// A stored value is code x block scale x head scale.  The product of the first two is exact in f16, so a
+// pair of elements costs one conversion and one multiplication; the head's scale goes into the
+// scores' scale (keys) and the end result (values).  Q's rows are scaled by a power of two into f16's range.
+//
+// Codes as operands.  ldmatrix hands a thread 4 adjacent bytes of one key, elements 8t .. 8t + 7 of 32:
+// two steps of the first product take them as they come (k = 2t, 2t + 1, 2t + 8, 2t + 9 stand for elements
+// 8t .. 8t + 3, then 8t + 4 .. 8t + 7), and Q's elements are those 16 bytes of its row, no permutation
+// needed.  All four bytes lie in one block of 16: one scale.  For the second product the transposing ldmatrix hands out
+// two bytes (elements 4g .. 4g + 3) of key 2t and the same two of key 2t + 1; converted, scaled each by
+// its key's scale, their halves change places.  Column g of tile j is then element 4g + j, so that a
+// thread ends with eight adjacent elements of its rows.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "attn_mma.cuh"
+
+namespace dspark {
+namespace attn {
+
+template <int DT, int TM>
+struct Mma4Shape {
+    static constexpr int kThreads = 128, kWarps = 4;
+    static constexpr int M = 16 * TM;
+    static constexpr int KS = 32;                           // keys of a warp's step
+    static constexpr int KT = KS * kWarps;                  // keys of a unit
+    static constexpr int kRow = DT / 2;                     // bytes of a row's codes
+    static constexpr int kScale = DT / 16;                  // and of its scales
+    static constexpr int kStage = 2 * KS * (kRow + kScale); // codes of keys, of values, scales of keys, of values
+    static constexpr int kStages = DT <= 64 ? 4 : DT <= 128 ? 2 + TM : 2;
+    static constexpr int kWarpBytes = kStage * kStages;     // also holds a warp's result at the end
+    static constexpr int kLd = DT + 8;                      // row of that result, floats
+    static constexpr int kQBytes = M * DT * 2;
+    static constexpr int kSmem = kWarps * kWarpBytes + kQBytes;
+    static constexpr int kPerSm = DT <= 128 ? (TM == 1 ? 3 : 2) : 1;
+    static_assert(M * kLd * 4 <= kWarpBytes, "a warp's result fits its ring");
+    static_assert(kPerSm * (kSmem + 3072) <= 227 * 1024, "shared memory");
+};
+
+// Byte offset of 16-byte chunk c of row r in rows of kRow bytes, free of conflicts for eight rows.
+template <int kRow>
+__device__ __forceinline__ uint32_t code_at(int r, int c) {
+    if constexpr (kRow >= 64) return chunk_at<kRow>(r, c);
+    else return r * kRow + ((c ^ ((r >> 2) & 1)) << 4);
+}
+// Byte offset of 16-byte chunk c of query row m: a quarter warp reads four chunks of two rows.
+template <int DT>
+__device__ __forceinline__ uint32_t query_at(int m, int c) {
+    return m * (2 * DT) + ((c ^ ((m & 1) << 2)) << 4);
+}
+// 4 bytes to shared memory, the first n of them read, the others zero.
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int n) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Both halves from the low (0) or the high (1) half.
+__device__ __forceinline__ uint32_t both(uint32_t x, int high) { return __byte_perm(x, 0, high ? 0x3232 : 0x1010); }
+
+// Of a row's DT / 16 scale bytes (kWords words), every second one from `odd` on: one f16 for each 32
+// elements, two to a word.
+template <int DT>
+__device__ __forceinline__ void half_scales(const uint32_t* w, uint32_t pick, uint32_t* out) {
+    if constexpr (DT == 64) {
+        out[0] = e4m3x2_f16x2(__byte_perm(w[0], 0, pick));
+    } else {
+#pragma unroll
+        for (int i = 0; i < DT / 128; ++i) {
+            const uint32_t four = __byte_perm(w[2 * i], w[2 * i + 1], pick);
+            out[2 * i] = e4m3x2_f16x2(four);
+            out[2 * i + 1] = e4m3x2_f16x2(four >> 16);
+        }
+    }
+}
+template <int kWords>
+__device__ __forceinline__ void load_words(const unsigned char* at, uint32_t* w) {
+    if constexpr (kWords == 1) {
+        w[0] = *reinterpret_cast<const uint32_t*>(at);
+    } else if constexpr (kWords == 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(at);
+        w[0] = x.x, w[1] = x.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) {
+            const uint4 x = *reinterpret_cast<const uint4*>(at + 16 * i);
+            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+        }
+    }
+}
+
+template <int DT, int TM>
+__global__ void __launch_bounds__(128, (Mma4Shape<DT, TM>::kPerSm)) attend_mma4(const __grid_constant__ Args p) {
+    using Sh = Mma4Shape<DT, TM>;
+    constexpr int M = Sh::M, KS = Sh::KS, KT = Sh::KT, kRow = Sh::kRow, kScale = Sh::kScale, kStages = Sh::kStages;
+    constexpr int kThreads = Sh::kThreads, kWarps = Sh::kWarps;
+    constexpr int kChunks = kRow / 16;                       // 16-byte chunks of a row's codes
+    constexpr int kV = KS * kRow, kKs = 2 * KS * kRow, kVs = kKs + KS * kScale;      // parts of a stage behind the keys
+    constexpr int kPairs = (DT + 63) / 64;                   // words of scales a thread keeps of one row
+    constexpr float kShift = 14.f;                           // P carries 2^kShift
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ long long scratch[38];
+    __shared__ float s_m[kWarps][M], s_l[kWarps][M], s_qs[M];
+    __shared__ float2 s_row[M];
+    __shared__ int s_flag;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
+    const float ninf = -__uint_as_float(0x7f800000u);
+    unsigned char* ring = smem + w * Sh::kWarpBytes;
+    const uint32_t ring_a = smem_u32(ring);
+    unsigned char* s_q = smem + kWarps * Sh::kWarpBytes;
+    const uint32_t q_a = smem_u32(s_q);
+    const int real_chunks = p.D / 32;
+    const bool whole_pages = p.page % 16 == 0;               // 16 keys (half of a step's) lie on one page
+    const bool adjacent = whole_pages && p.D == DT;          // and fill the rows
+    const uint32_t k_pick = t < 2 ? 0x6420 : 0x7531, v_pick = g < 4 ? 0x6420 : 0x7531;
+    const char* kc = static_cast<const char*>(p.kc);
+    const char* vc = static_cast<const char*>(p.vc);
+
+    const Start st = find_start<M, KT, kThreads>(p, scratch);
+    Walk<M, KT> walk(p, st);
+    Piece pc;
+    while (walk.next(pc)) {
+        const int left = pc.r.n * p.G - pc.tile * M;
+        const int valid = left < M ? left : M;
+        // ---- the first keys and values are on their way before anything else
+        const int steps = pc.u1 - pc.u0;
+        const int key0 = pc.span.lo + pc.u0 * KT + w * KS;   // this warp's first key; then every KT
+        // Where the keys of step s lie: the head's page and the row in it of lane's key, or of the first of
+        // its 16 where a page holds them.
+        struct Place {
+            int64_t page;
+            int row;
+        };
+        auto find_rows = [&](int s) -> Place {
+            const int key = key0 + s * KT + (whole_pages ? lane & 16 : lane);
+            if (s >= steps || key + (whole_pages ? 15 : 0) < pc.span.seen || key >= pc.span.hi) return Place{0, 0};
+            const int blk = key / p.page;
+            return Place{(static_cast<int64_t>(page_id(p, pc.b, blk)) * p.Hkv + pc.h) * p.g4.whole, key - blk * p.page};
+        };
+        auto load = [&](int s, const Place& at) {
+            const int first = key0 + s * KT;
+            if (s < steps && first < pc.span.hi && first + KS > pc.span.seen) {
+                const uint32_t to = ring_a + (s % kStages) * Sh::kStage;
+                const int64_t code = at.page + static_cast<int64_t>(at.row) * p.g4.code;
+                const int64_t scale = at.page + p.g4.codes + static_cast<int64_t>(at.row) * p.g4.scale;
+                if (adjacent && first >= pc.span.seen && first + KS <= pc.span.hi) {
+                    // sixteen rows are one run of codes and one of scales: 16 bytes a lane
+                    constexpr int kIn = 16 * kChunks / 32;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const int64_t run = __shfl_sync(0xffffffffu, code, 16 * b) + lane * 16;
+#pragma unroll
+                        for (int i = 0; i < kIn; ++i) {
+                            const int e = lane + 32 * (kIn * b + i);
+                            const uint32_t d = to + code_at<kRow>(e / kChunks, e % kChunks);
+                            cp_async16_at(d, kc + run + 512 * i);
+                            cp_async16_at(d + kV, vc + run + 512 * i);
+                        }
+                    }
+                    if (lane % 16 < kScale) {
+                        cp_async16_at(to + kKs + (lane / 16 * kScale + lane % 16) * 16, kc + scale + lane % 16 * 16);
+                        cp_async16_at(to + kVs + (lane / 16 * kScale + lane % 16) * 16, vc + scale + lane % 16 * 16);
+                    }
+                } else {
+                    const int in16 = whole_pages ? lane & 15 : 0;            // of lane's key in its 16
+#pragma unroll
+                    for (int i = 0; i < KS * kChunks / 32; ++i) {
+                        const int e = lane + 32 * i, r = e / kChunks, c = e % kChunks;
+                        const int64_t run = __shfl_sync(0xffffffffu, code, r) + (whole_pages ? (r & 15) * p.g4.code : 0);
+                        const bool real = first + r >= pc.span.seen && first + r < pc.span.hi && c < real_chunks;
+                        const int64_t from = real ? run + c * 16 : 0;
+                        const uint32_t d = to + code_at<kRow>(r, c);
+                        copy16(d, kc + from, real);
+                        copy16(d + kV, vc + from, real);
+                    }
+                    const bool real = first + lane >= pc.span.seen && first + lane < pc.span.hi;
+                    const int64_t from = real ? scale + in16 * p.g4.scale : 0;
+#pragma unroll
+                    for (int i = 0; i < kScale / 4; ++i) {
+                        const int n = real ? min(4, max(0, p.D / 16 - 4 * i)) : 0;
+                        copy4(to + kKs + lane * kScale + 4 * i, kc + from + (n > 0 ? 4 * i : 0), n);
+                        copy4(to + kVs + lane * kScale + 4 * i, vc + from + (n > 0 ? 4 * i : 0), n);
+                    }
+                }
+            }
+            copy_commit();
+        };
+        // The queries first (16-bit, rows past the last zero): they arrive with the first keys.
+        for (int e = tid; e < M * (DT / 8); e += kThreads) {
+            const int m = e / (DT / 8), c = e - m * (DT / 8), qi = pc.tile * M + m;
+            const bool real = m < valid && c * 8 < p.D;
+            const int64_t at = real ? (static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.q_stride +
+                                          static_cast<int64_t>(pc.h * p.G + qi % p.G) * p.D + c * 8
+                                    : 0;
+            copy16(q_a + query_at<DT>(m, c), static_cast<const __nv_bfloat16*>(p.q) + at, real);
+        }
+        Place ahead[kStages];
+#pragma unroll
+        for (int s = 0; s < kStages; ++s) ahead[s] = find_rows(s);
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) load(s, ahead[s]);
+        Place rows = ahead[kStages - 1];
+        copy_wait<kStages - 2>();
+        __syncthreads();
+        // rows to f16, in place: the largest element comes to 2^10 .. 2^11, a negative scale's sign with it
+        for (int m = w; m < M; m += kWarps) {
+            uint32_t own[kPairs];
+            float big = 0.f;
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) {
+                const int i = lane + 32 * k;                 // pair i: columns 2i, 2i + 1
+                own[k] = i < DT / 2 ? *reinterpret_cast<const uint32_t*>(s_q + query_at<DT>(m, i >> 2) + (i & 3) * 4) : 0u;
+                big = fmaxf(big, fmaxf(fabsf(bf16lo(own[k])), fabsf(bf16hi(own[k]))));
+            }
+            big = warp_max(big);
+            // 2^up and 2^-up by their exponent bits (up stays where both are normal numbers)
+            int up = 0;
+            if (big > 0.f && big < __uint_as_float(0x7f800000u)) up = min(10 - (static_cast<int>(__float_as_uint(big) >> 23) - 127), 126);
+            const float grow = __uint_as_float((p.scale_log2 < 0.f ? 0x80000000u : 0u) | static_cast<uint32_t>(127 + up) << 23);
+            const float back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) {
+                const int i = lane + 32 * k;
+                if (i < DT / 2)
+                    *reinterpret_cast<uint32_t*>(s_q + query_at<DT>(m, i >> 2) + (i & 3) * 4) = pack_f16(bf16lo(own[k]) * grow, bf16hi(own[k]) * grow);
+            }
+            if (lane == 0) s_qs[m] = fabsf(p.scale_log2) * p.k_scale[pc.h] * back;
+        }
+        __syncthreads();
+        float sc[TM][2], mx[TM][2], l[TM][2];
+        float o[TM][DT / 8][4];
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                sc[tm][r] = fmaxf(s_qs[16 * tm + g + 8 * r], 1.17549435e-38f);      // -inf times it is -inf
+                mx[tm][r] = ninf;
+                l[tm][r] = 0.f;
+            }
+#pragma unroll
+            for (int n = 0; n < DT / 8; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[tm][n][i] = 0.f;
+        }
+
+        const int pos_lo = pc.r.len + pc.tile * M / p.G, pos_hi = pc.span.hi - 1;   // the tile's first and last position
+        for (int s = 0; s < steps; ++s) {
+            copy_wait<kStages - 2>();
+            __syncwarp();
+            load(s + kStages - 1, rows);
+            rows = find_rows(s + kStages);
+            const int first = key0 + s * KT;
+            if (first >= pc.span.hi || first + KS <= pc.span.seen) continue;
+            unsigned char* stage = ring + (s % kStages) * Sh::kStage;
+            const uint32_t k_a = ring_a + (s % kStages) * Sh::kStage, v_a = k_a + kV;
+
+            // ---- S = Q K^T
+            uint32_t scale[4][kPairs];                       // of keys 8i + g: this thread's block of every 32 elements
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t x[kScale / 4];
+                load_words<kScale / 4>(stage + kKs + (8 * i + g) * kScale, x);
+                half_scales<DT>(x, k_pick, scale[i]);
+            }
+            float sv[TM][4][4];
+#pragma unroll
+            for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sv[tm][n][i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < DT / 32; ++c) {
+                uint32_t kf[4], qa[TM][2][4];
+                ldsm4(kf, k_a + code_at<kRow>(lane, c));
+#pragma unroll
+                for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(s_q + query_at<DT>(16 * tm + g + 8 * r, 4 * c + t));
+                        qa[tm][0][r] = x.x, qa[tm][0][2 + r] = x.y, qa[tm][1][r] = x.z, qa[tm][1][2 + r] = x.w;
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t h[4];
+                    e2m1x8_f16(kf[i], h);
+                    const uint32_t a = both(scale[i][c / 2], c & 1);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) h[j] = hmul2(h[j], a);
+#pragma unroll
+                    for (int tm = 0; tm < TM; ++tm) {
+                        mma16816<true>(sv[tm][i], qa[tm][0], h[0], h[1]);
+                        mma16816<true>(sv[tm][i], qa[tm][1], h[2], h[3]);
+                    }
+                }
+            }
+            // ---- scores; hidden keys at -inf.  Their scale (to units of log 2) is not negative, so the
+            // largest is found before scaling and the scaling is part of the exponent's addition.
+            const bool masked = first + KS - 1 > pos_lo || (p.window > 0 && first <= pos_hi - p.window);
+            uint32_t hidden[TM][2];                      // bit 2n + i: key 8n + 2t + i is hidden from row g (+ 8)
+            float nm[TM][2];
+            bool moved = false;
+#pragma unroll
+            for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    hidden[tm][r] = 0;
+                    if (masked) {
+                        const int pos = pc.r.len + (pc.tile * M + 16 * tm + g + 8 * r) / p.G;
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int key = first + 8 * n + 2 * t + i;
+                                if (key > pos || key >= pc.span.hi || (p.window > 0 && key <= pos - p.window)) {
+                                    hidden[tm][r] |= 1u << (2 * n + i);
+                                    sv[tm][n][2 * r + i] = ninf;
+                                }
+                            }
+                    }
+                    float m2[2] = {ninf, ninf};
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) m2[i] = fmaxf(m2[i], sv[tm][n][2 * r + i]);
+                    float mm = fmaxf(m2[0], m2[1]);
+                    mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 1));
+                    mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 2));
+                    mm = fmaxf(mx[tm][r], mm == ninf ? ninf : mm * sc[tm][r]);
+                    nm[tm][r] = mm;
+                    moved |= mm != mx[tm][r];
+                }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float a = fast_exp2(mx[tm][r] - (nm[tm][r] == ninf ? 0.f : nm[tm][r]));
+                        l[tm][r] *= a;
+                        mx[tm][r] = nm[tm][r];
+#pragma unroll
+                        for (int n = 0; n < DT / 8; ++n) {
+                            o[tm][n][2 * r] *= a;
+                            o[tm][n][2 * r + 1] *= a;
+                        }
+                    }
+            }
+            // ---- P
+            uint32_t ph[TM][2][4];
+#pragma unroll
+            for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float use = (mx[tm][r] == ninf ? 0.f : mx[tm][r]) - kShift;
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const float e0 = fast_exp2(fmaf(sv[tm][n][2 * r], sc[tm][r], -use));
+                        const float e1 = fast_exp2(fmaf(sv[tm][n][2 * r + 1], sc[tm][r], -use));
+                        l[tm][r] += e0 + e1;
+                        ph[tm][n >> 1][(n & 1) * 2 + r] = pack_f16(e0, e1);
+                    }
+                }
+            // ---- O += P V.  A hidden key's P is 0, which keeps its value out as long as that is a number.
+            // Steps with hidden keys look at the scales: a block that is not a number is added here, to
+            // the rows that see it, and becomes 0 for the product.
+            if (masked) {
+                unsigned char* vs = stage + kVs;
+                bool odd = false;
+                for (int i = lane; i < KS * kScale / 4; i += 32) odd |= any_odd<true>(reinterpret_cast<const uint32_t*>(vs)[i]);
+                if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+                    for (int j = 0; j < KS; ++j) {
+                        const int src = g * 4 + ((j & 7) >> 1), bit = 2 * (j >> 3) + (j & 1);
+#pragma unroll
+                        for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const bool in = !(__shfl_sync(0xffffffffu, hidden[tm][r], src) >> bit & 1u);
+#pragma unroll
+                                for (int c = 0; c < DT / 32; ++c)
+                                    if (in && any_odd<true>(vs[j * kScale + 2 * c + (t >> 1)])) {
+#pragma unroll
+                                        for (int n = 0; n < 4; ++n) o[tm][4 * c + n][2 * r] = o[tm][4 * c + n][2 * r + 1] = __uint_as_float(0x7fffffffu);
+                                    }
+                            }
+                    }
+                    __syncwarp();
+                    for (int i = lane; i < KS * kScale / 4; i += 32) {
+                        uint32_t& u = reinterpret_cast<uint32_t*>(vs)[i];
+                        u = without_odd<true>(u);
+                    }
+                    __syncwarp();
+                }
+            }
+            uint32_t vscale[4][2][kPairs];                   // of keys 8i + 2t and 8i + 2t + 1
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t x[kScale / 2];
+                load_words<kScale / 2>(stage + kVs + (8 * i + 2 * t) * kScale, x);
+                half_scales<DT>(x, v_pick, vscale[i][0]);
+                half_scales<DT>(x + kScale / 4, v_pick, vscale[i][1]);
+            }
+#pragma unroll
+            for (int c = 0; c < DT / 32; ++c) {
+                uint32_t vf[4];
+                ldsm4_t(vf, v_a + code_at<kRow>(lane, c));
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t bf[4][2];                       // of tile j: keys 16b + 2t (+1), and 16b + 8 + 2t (+1)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t h[4];
+                        e2m1x8_f16(vf[2 * b + i], h);
+                        const uint32_t a0 = both(vscale[2 * b + i][0][c / 2], c & 1), a1 = both(vscale[2 * b + i][1][c / 2], c & 1);
+                        h[0] = hmul2(h[0], a0);
+                        h[1] = hmul2(h[1], a0);
+                        h[2] = hmul2(h[2], a1);
+                        h[3] = hmul2(h[3], a1);
+                        bf[0][i] = __byte_perm(h[0], h[2], 0x5410);
+                        bf[1][i] = __byte_perm(h[0], h[2], 0x7632);
+                        bf[2][i] = __byte_perm(h[1], h[3], 0x5410);
+                        bf[3][i] = __byte_perm(h[1], h[3], 0x7632);
+                    }
+#pragma unroll
+                    for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) mma16816<true>(o[tm][4 * c + j], ph[tm][b], bf[j][0], bf[j][1]);
+                }
+            }
+        }
+        copy_wait<0>();
+        __syncwarp();
+
+        // ---- the four warps' results join
+        float* mine = reinterpret_cast<float*>(ring);
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float sum = l[tm][r];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                const int m = 16 * tm + g + 8 * r;
+                if (t == 0) {
+                    s_m[w][m] = mx[tm][r];
+                    s_l[w][m] = sum;
+                }
+#pragma unroll
+                for (int c = 0; c < DT / 32; ++c)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        *reinterpret_cast<float4*>(mine + m * Sh::kLd + 32 * c + 8 * t + 4 * i) =
+                            make_float4(o[tm][4 * c][2 * r + i], o[tm][4 * c + 1][2 * r + i], o[tm][4 * c + 2][2 * r + i], o[tm][4 * c + 3][2 * r + i]);
+            }
+        __syncthreads();
+        const bool whole = pc.whole();
+        if (tid < M) {
+            // a row's maximum and sum, and each warp's factor in its output (the values' scale and, where
+            // this is the whole, the sum with it)
+            float big = ninf, sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) big = fmaxf(big, s_m[i][tid]);
+            const float use = big == ninf ? 0.f : big, vs = p.v_scale[pc.h];
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) sum += s_l[i][tid] * fast_exp2(s_m[i][tid] - use);
+            const float f = !whole ? vs : sum != 0.f ? vs / sum : 0.f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) s_m[i][tid] = f * fast_exp2(s_m[i][tid] - use);
+            if (tid < valid) {
+                if (!whole) {
+                    reinterpret_cast<float2*>(p.part_ml)[part_place(blockIdx.x, pc.u0 == 0) * M + tid] = make_float2(big - kShift, sum);
+                } else if (p.lse != nullptr) {
+                    const int qi = pc.tile * M + tid;
+                    p.lse[(static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.Hq + pc.h * p.G + qi % p.G] = lse_of(big - kShift, sum);
+                }
+            }
+        }
+        __syncthreads();
+        const int four = p.D / 4;
+        float* part = p.part_o + part_place(blockIdx.x, pc.u0 == 0) * M * p.D;
+#pragma unroll 2
+        for (int e = tid; e < valid * four; e += kThreads) {
+            const int m = e / four, d = (e - m * four) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const float f = s_m[i][m];
+                const float4 v = *reinterpret_cast<const float4*>(smem + i * Sh::kWarpBytes + (m * Sh::kLd + d) * 4);
+                x.x = fmaf(v.x, f, x.x);
+                x.y = fmaf(v.y, f, x.y);
+                x.z = fmaf(v.z, f, x.z);
+                x.w = fmaf(v.w, f, x.w);
+            }
+            if (whole) {
+                const int qi = pc.tile * M + m, head = pc.h * p.G + qi % p.G;
+                const int64_t row = static_cast<int64_t>(pc.r.row0) + qi / p.G;
+                store_four(static_cast<__nv_bfloat16*>(p.out) + (row * p.Hq + head) * p.D + d, x);
+            } else {
+                store_four(part + m * p.D + d, x);
+            }
+        }
+        if (!whole && part_done(p, pc, st, &s_flag, tid, [] { __syncthreads(); }))
+            join_parts<__nv_bfloat16, M, kThreads>(p, pc, st, s_row, tid, [] { __syncthreads(); });
+        __syncthreads();
+    }
+    if (blockIdx.x == 0) head_cleared();
+}
+
+template <int DT, int TM>
+dspark_status_t launch_mma4(const Args& p, cudaStream_t s) {
+    using Sh = Mma4Shape<DT, TM>;
+    static OncePerDevice once;
+    const int dev = current_device();
+    if (once.run(dev, [] {
+            return cudaFuncSetAttribute(attend_mma4<DT, TM>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+        }) != cudaSuccess)
+        return DSPARK_ERR_CUDA;
+    const int grid = grid_for(sm_count(dev) * Sh::kPerSm, Sh::M);
+    if (grid < 1) return DSPARK_ERR_CUDA;
+    return launch_cleared(p.status, kHeadBytes, attend_mma4<DT, TM>, dim3(grid), Sh::kThreads, Sh::kSmem, s, p);
+}
+
+}  // namespace attn
+}  // namespace dspark

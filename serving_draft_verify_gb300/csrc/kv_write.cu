@@ -2,7 +2,8 @@
 //
 // cache[slot / page][head][slot % page][:] = row[head][:], copied, or stored in
 // 8 bits as e4m3(clamp(x / scale[head], +-448)), rounded to nearest even.  The
-// quotient is formed in float32 by an IEEE division; NaN stays NaN.
+// quotient is formed in float32 by an IEEE division; NaN stays NaN.  4-bit caches are
+// written by the kernel of rotate.cu, without a rotation.
 //
 // Bound by memory: each element is read once and written once.  A thread has one piece of eight
 // elements of a row (key or value, head, place) and moves it for four rows at a time, all loads
@@ -10,9 +11,8 @@
 // 16384 rows of 8 heads of 128: bf16 24 us (134 MB, 5.6 TB/s), to 8 bits 25 us (100 MB); with two
 // rows at a time 37 and 33 us, with eight 24 and 27, with blocks of 256 threads 28 to 8 bits.
 // float32 47 us (268 MB, 5.7 TB/s), to 8 bits 39 us (168 MB), caches flushed before each.
-#include <cuda_fp8.h>
-
 #include "launch.cuh"
+#include "rotate.cuh"
 
 namespace dspark {
 namespace {
@@ -36,59 +36,6 @@ struct WriteArgs {
     void *kc, *vc;
     StatusBlock* status;
 };
-
-template <typename T>
-struct Eight;
-template <>
-struct Eight<__nv_bfloat16> {
-    uint4 w;
-    __device__ void load(const void* p) { w = __ldg(static_cast<const uint4*>(p)); }
-    __device__ void store(void* p) const { *static_cast<uint4*>(p) = w; }
-    __device__ void floats(float* f) const {
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = bf16lo(u[i]);
-            f[2 * i + 1] = bf16hi(u[i]);
-        }
-    }
-};
-template <>
-struct Eight<float> {
-    float4 a, b;
-    __device__ void load(const void* p) {
-        a = __ldg(static_cast<const float4*>(p));
-        b = __ldg(static_cast<const float4*>(p) + 1);
-    }
-    __device__ void store(void* p) const {
-        static_cast<float4*>(p)[0] = a;
-        static_cast<float4*>(p)[1] = b;
-    }
-    __device__ void floats(float* f) const {
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-        f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    }
-};
-
-// How far to either side of x * (1 / s) a number that rounds to the bytes of x / s is looked for.  The
-// two are within 2^-22 of each other; where s is a power of two they are the same, and 2^-30 is
-// gone in the sum's rounding (but makes an infinite x differ, which then takes the quotient proper).
-__device__ __forceinline__ float margin_of(float s) {
-    const uint32_t u = __float_as_uint(s) & 0x7FFFFFFFu;
-    return (u & 0x007FFFFFu) == 0 && u >= 0x00800000u && u < 0x7F800000u ? 0x1p-30f : 0x1p-21f;
-}
-// Two stored bytes of x / s.  The quotient proper costs nine instructions an element; where the numbers
-// `margin` to either side of x * (1 / s) round to the same bytes so does the quotient (the rounding
-// is monotonic).  One element in 100,000 does not end there where the quotients are spread evenly, but
-// one in 16 where they keep bf16's few bits and are ties: 16384 rows at scale 1 took 33 us, without
-// the margin 23; at 0.0125 (1 / 80) it is 28.
-__device__ __forceinline__ uint32_t stored(float x, float y, float s, float inv, float margin) {
-    const float a = x * inv, b = y * inv;
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(fmaf(a, -margin, a), fmaf(b, -margin, b)), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(fmaf(a, margin, a), fmaf(b, margin, b)), __NV_SATFINITE, __NV_E4M3);
-    if (lo == hi && inv < 3e38f && inv > 1e-37f) return lo;
-    return __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x, s), __fdiv_rn(y, s)), __NV_SATFINITE, __NV_E4M3);
-}
 
 template <typename T, bool kFp8>
 __global__ void __launch_bounds__(kThreads) write_kv(WriteArgs p) {
@@ -166,9 +113,9 @@ extern "C" dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int pag
     if (rows < 0 || rows > 0x7fffffffll || Hkv < 1 || Hkv > 1024 || D < 8 || D > 256 || D % 8 != 0 || page < 1 ||
         num_blocks < 1)
         return DSPARK_ERR_INVALID_ARGUMENT;
-    if ((dt != DSPARK_BF16 && dt != DSPARK_F32) || (cache_dt != dt && cache_dt != DSPARK_E4M3))
-        return DSPARK_ERR_INVALID_ARGUMENT;
-    if (cache_dt == DSPARK_E4M3 && (D % 16 != 0 || k_scale == nullptr || v_scale == nullptr))
+    const bool scaled = cache_dt == DSPARK_E4M3 || cache_dt == DSPARK_E2M1;
+    if ((dt != DSPARK_BF16 && dt != DSPARK_F32) || (cache_dt != dt && !scaled)) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (scaled && (D % (cache_dt == DSPARK_E4M3 ? 16 : 32) != 0 || k_scale == nullptr || v_scale == nullptr))
         return DSPARK_ERR_INVALID_ARGUMENT;
     const int64_t width = static_cast<int64_t>(Hkv) * D, align = dt == DSPARK_BF16 ? 8 : 4;
     if (k_stride < width || v_stride < width || k_stride % align != 0 || v_stride % align != 0)
@@ -176,11 +123,20 @@ extern "C" dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int pag
     if (k_cache == nullptr || v_cache == nullptr || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k) ||
         !aligned16(v) || (rows > 0 && (k == nullptr || v == nullptr || slot == nullptr)))
         return DSPARK_ERR_INVALID_ARGUMENT;
+    if (cache_dt == DSPARK_E2M1 && static_cast<int64_t>(page) * D > 0x7fffffffll - 1024) return DSPARK_ERR_UNSUPPORTED;
     if (workspace == nullptr || !aligned256(workspace)) return DSPARK_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < dspark_write_kv_workspace_size()) return DSPARK_ERR_WORKSPACE_TOO_SMALL;
     clear_stale_error();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (rows == 0) return clear_status(workspace, s);
+    if (cache_dt == DSPARK_E2M1) {
+        RotateArgs r{};
+        r.rows = rows, r.k_stride = k_stride, r.v_stride = v_stride;
+        r.slots = static_cast<int64_t>(num_blocks) * page;
+        r.Hkv = Hkv, r.D = D, r.page = page, r.k = k, r.v = v, r.slot = slot, r.k_scale = k_scale, r.v_scale = v_scale;
+        r.kc = k_cache, r.vc = v_cache, r.status = static_cast<StatusBlock*>(workspace);
+        return launch_rotate(r, dt, cache_dt, s);
+    }
     WriteArgs p{};
     p.rows = rows, p.k_stride = k_stride, p.v_stride = v_stride;
     p.slots = static_cast<int64_t>(num_blocks) * page;
