@@ -266,12 +266,12 @@ dspark_status_t launch_f32(const Args& p, cudaStream_t s) {
     return launch_simt<C, 8>(p, s);
 }
 
-// 4-bit caches: 32 query rows at a time where a request may have more than 16 of a key head.
+// 4-bit caches: 8, 16 or 32 query rows of a key head at a time, by the most that a request may have.
 dspark_status_t launch_bf16_e2m1(const Args& p, cudaStream_t s) {
-    const bool one = static_cast<int64_t>(p.max_rows) * p.G <= 16;
-    if (p.D <= 64) return one ? launch_mma4<64, 1>(p, s) : launch_mma4<64, 2>(p, s);
-    if (p.D <= 128) return one ? launch_mma4<128, 1>(p, s) : launch_mma4<128, 2>(p, s);
-    return launch_mma4<256, 1>(p, s);
+    const int64_t most = static_cast<int64_t>(p.max_rows) * p.G;
+    if (p.D <= 64) return most <= 8 ? launch_mma4<64, 1>(p, s) : most <= 16 ? launch_mma4<64, 2>(p, s) : launch_mma4<64, 4>(p, s);
+    if (p.D <= 128) return most <= 8 ? launch_mma4<128, 1>(p, s) : most <= 16 ? launch_mma4<128, 2>(p, s) : launch_mma4<128, 4>(p, s);
+    return most <= 8 ? launch_mma4<256, 1>(p, s) : launch_mma4<256, 2>(p, s);
 }
 
 // bf16 rows: sixteen query rows at a time on the warp-level instructions, or 128 on tcgen05 where a
@@ -333,6 +333,9 @@ extern "C" dspark_status_t dspark_paged_attention(
     p.kc = k_cache, p.vc = v_cache;
     if (scaled) p.k_scale = k_scale, p.v_scale = v_scale;
     p.g4 = page4_of(page, D);
+    p.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (page == 1 << i) p.page_shift = i;
     p.scale_log2 = scale * kLog2e, p.out = out, p.lse = lse;
     char* ws = static_cast<char*>(workspace);
     p.status = reinterpret_cast<StatusBlock*>(ws);

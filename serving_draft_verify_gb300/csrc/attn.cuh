@@ -33,6 +33,7 @@ struct Args {
     const void *kc, *vc;
     const float *k_scale, *v_scale;
     Page4 g4;                         // of a 4-bit cache
+    int page_shift;                   // page = 1 << page_shift, or -1
     float scale_log2;                 // scale * log2(e)
     void* out;
     float* lse;

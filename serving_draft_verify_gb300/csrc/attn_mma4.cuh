@@ -1,24 +1,33 @@
-// Attention over a 4-bit cache (kv_store.cuh has the format): 16 or 32 query rows of a key head
+// Attention over a 4-bit cache (kv_store.cuh has the format): 8, 16 or 32 query rows of a key head
 // at a time on the warp-level tensor instructions.
 //
 // The work is divided as in attn_mma.cuh: each of a block's four warps takes 32 keys of every unit of
-// 128, with a ring of its own, its own running maximum and sum and its own rows of the output.
+// 128, with a ring of its own, its own running maximum and sum and its own part of the output.  What
+// bounds it is not the bytes but turning codes into operands, some 250 instructions of a warp for 32 keys of
+// 128 elements, so keys and values are the side of the products that has 16 rows and the queries the one that
+// has 8: a step for up to 8 query rows (plain decoding with groups of 8 and fewer) then costs half the
+// products and half the exponentials.
 //
-//   S = Q K^T    m16n8k16 in f16, keys as columns,
-//   P = 2^(S - m), with a factor 2^14 that the sum carries too, rounded to 11 bits,
-//   O += P V.
+//   S' = K Q'    m16n8k16 in f16, query rows as columns,
+//   P' = 2^(S' - m), with a factor 2^14 that the sum carries too, rounded to 11 bits,
+//   O' += V' P'  P' turned from accumulators to operands by movmatrix.
 //
-// A stored value is code x block scale x head scale.  The product of the first two is exact in f16, so a
-// pair of elements costs one conversion and one multiplication; the head's scale goes into the
-// scores' scale (keys) and the end result (values).  Q's rows are scaled by a power of two into f16's range.
+// m is the largest score of a row, or up to 1 (in units of log 2) below it: f16 has room for that, so
+// the maximum has to be found across the warp, and the output scaled, only in steps where a vote says so.
+//
+// A stored value is code x block scale x head scale.  The product of the first two is exact in f16; the
+// head's scale goes into the scores' scale (keys) and the end result (values).  Q's rows are scaled by a
+// power of two into f16's range.
 //
 // Codes as operands.  ldmatrix hands a thread 4 adjacent bytes of one key, elements 8t .. 8t + 7 of 32:
 // two steps of the first product take them as they come (k = 2t, 2t + 1, 2t + 8, 2t + 9 stand for elements
 // 8t .. 8t + 3, then 8t + 4 .. 8t + 7), and Q's elements are those 16 bytes of its row, no permutation
 // needed.  All four bytes lie in one block of 16: one scale.  For the second product the transposing ldmatrix hands out
-// two bytes (elements 4g .. 4g + 3) of key 2t and the same two of key 2t + 1; converted, scaled each by
-// its key's scale, their halves change places.  Column g of tile j is then element 4g + j, so that a
-// thread ends with eight adjacent elements of its rows.
+// two bytes (elements 4g .. 4g + 3) of key 2t and the same two of key 2t + 1.  The halves of their
+// conversions have to be paired key by key; a multiplication by (s, 0) and one by (0, s') that adds to it do that
+// and the scaling at once, on the pipe that has less to do (permuting after scaling took it from the pipe
+// that converts).  Rows g and g + 8 of tile j then are elements 4g + 2j and 4g + 2j + 1, so that a thread
+// ends with four adjacent elements of its rows.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -28,21 +37,22 @@
 namespace dspark {
 namespace attn {
 
-template <int DT, int TM>
+template <int DT, int NT>
 struct Mma4Shape {
     static constexpr int kThreads = 128, kWarps = 4;
-    static constexpr int M = 16 * TM;
+    static constexpr int M = 8 * NT;                        // query rows of a tile
     static constexpr int KS = 32;                           // keys of a warp's step
     static constexpr int KT = KS * kWarps;                  // keys of a unit
     static constexpr int kRow = DT / 2;                     // bytes of a row's codes
     static constexpr int kScale = DT / 16;                  // and of its scales
     static constexpr int kStage = 2 * KS * (kRow + kScale); // codes of keys, of values, scales of keys, of values
-    static constexpr int kStages = DT <= 64 ? 4 : DT <= 128 ? 2 + TM : 2;
+    static constexpr int kPerSm = NT == 4 || DT > 128 ? 2 : NT == 2 ? 3 : 4;
+    static constexpr int kStages = DT <= 64 ? 4 : DT <= 128 ? (NT == 4 ? 4 : NT == 2 ? 3 : 2) : 2;
     static constexpr int kWarpBytes = kStage * kStages;     // also holds a warp's result at the end
-    static constexpr int kLd = DT + 8;                      // row of that result, floats
+    static constexpr int kLd = DT + 4;                      // row of that result, floats
     static constexpr int kQBytes = M * DT * 2;
     static constexpr int kSmem = kWarps * kWarpBytes + kQBytes;
-    static constexpr int kPerSm = DT <= 128 ? (TM == 1 ? 3 : 2) : 1;
+    static constexpr bool kQReg = NT * DT <= 128;           // the queries' operands stay in registers
     static_assert(M * kLd * 4 <= kWarpBytes, "a warp's result fits its ring");
     static_assert(kPerSm * (kSmem + 3072) <= 227 * 1024, "shared memory");
 };
@@ -67,8 +77,21 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// Both halves from the low (0) or the high (1) half.
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+// The low (0) or the high (1) half twice; in the low half, over 0; in the high half, over 0.
 __device__ __forceinline__ uint32_t both(uint32_t x, int high) { return __byte_perm(x, 0, high ? 0x3232 : 0x1010); }
+__device__ __forceinline__ uint32_t in_low(uint32_t x, int high) { return high ? x >> 16 : x & 0xFFFFu; }
+__device__ __forceinline__ uint32_t in_high(uint32_t x, int high) { return high ? x & 0xFFFF0000u : x << 16; }
+// An 8 x 8 matrix of f16, two adjacent elements of a row a thread, transposed.
+__device__ __forceinline__ uint32_t turned8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
 
 // Of a row's DT / 16 scale bytes (kWords words), every second one from `odd` on: one f16 for each 32
 // elements, two to a word.
@@ -101,9 +124,9 @@ __device__ __forceinline__ void load_words(const unsigned char* at, uint32_t* w)
     }
 }
 
-template <int DT, int TM>
-__global__ void __launch_bounds__(128, (Mma4Shape<DT, TM>::kPerSm)) attend_mma4(const __grid_constant__ Args p) {
-    using Sh = Mma4Shape<DT, TM>;
+template <int DT, int NT>
+__global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(const __grid_constant__ Args p) {
+    using Sh = Mma4Shape<DT, NT>;
     constexpr int M = Sh::M, KS = Sh::KS, KT = Sh::KT, kRow = Sh::kRow, kScale = Sh::kScale, kStages = Sh::kStages;
     constexpr int kThreads = Sh::kThreads, kWarps = Sh::kWarps;
     constexpr int kChunks = kRow / 16;                       // 16-byte chunks of a row's codes
@@ -146,7 +169,7 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, TM>::kPerSm)) attend_mma4(
         auto find_rows = [&](int s) -> Place {
             const int key = key0 + s * KT + (whole_pages ? lane & 16 : lane);
             if (s >= steps || key + (whole_pages ? 15 : 0) < pc.span.seen || key >= pc.span.hi) return Place{0, 0};
-            const int blk = key / p.page;
+            const int blk = p.page_shift >= 0 ? key >> p.page_shift : key / p.page;
             return Place{(static_cast<int64_t>(page_id(p, pc.b, blk)) * p.Hkv + pc.h) * p.g4.whole, key - blk * p.page};
         };
         auto load = [&](int s, const Place& at) {
@@ -239,20 +262,29 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, TM>::kPerSm)) attend_mma4(
             if (lane == 0) s_qs[m] = fabsf(p.scale_log2) * p.k_scale[pc.h] * back;
         }
         __syncthreads();
-        float sc[TM][2], mx[TM][2], l[TM][2];
-        float o[TM][DT / 8][4];
+        uint4 qf[Sh::kQReg ? DT / 32 : 1][Sh::kQReg ? NT : 1];
+        auto load_q = [&](int c, int n) { return *reinterpret_cast<const uint4*>(s_q + query_at<DT>(8 * n + g, 4 * c + t)); };
+        if constexpr (Sh::kQReg) {
 #pragma unroll
-        for (int tm = 0; tm < TM; ++tm) {
+            for (int c = 0; c < DT / 32; ++c)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) qf[c][n] = load_q(c, n);
+        }
+        // This thread's query rows: 8n + 2t and 8n + 2t + 1, shared with the seven other g.
+        float sc[NT][2], mx[NT][2], l[NT][2];
+        float o[NT][DT / 16][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                sc[tm][r] = fmaxf(s_qs[16 * tm + g + 8 * r], 1.17549435e-38f);      // -inf times it is -inf
-                mx[tm][r] = ninf;
-                l[tm][r] = 0.f;
+                sc[n][r] = fmaxf(s_qs[8 * n + 2 * t + r], 1.17549435e-38f);         // -inf times it is -inf
+                mx[n][r] = ninf;
+                l[n][r] = 0.f;
             }
 #pragma unroll
-            for (int n = 0; n < DT / 8; ++n)
+            for (int d = 0; d < DT / 16; ++d)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[tm][n][i] = 0.f;
+                for (int i = 0; i < 4; ++i) o[n][d][i] = 0.f;
         }
 
         const int pos_lo = pc.r.len + pc.tile * M / p.G, pos_hi = pc.span.hi - 1;   // the tile's first and last position
@@ -266,7 +298,7 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, TM>::kPerSm)) attend_mma4(
             unsigned char* stage = ring + (s % kStages) * Sh::kStage;
             const uint32_t k_a = ring_a + (s % kStages) * Sh::kStage, v_a = k_a + kV;
 
-            // ---- S = Q K^T
+            // ---- S' = K Q'
             uint32_t scale[4][kPairs];                       // of keys 8i + g: this thread's block of every 32 elements
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -274,105 +306,106 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, TM>::kPerSm)) attend_mma4(
                 load_words<kScale / 4>(stage + kKs + (8 * i + g) * kScale, x);
                 half_scales<DT>(x, k_pick, scale[i]);
             }
-            float sv[TM][4][4];
+            float sv[NT][2][4];                              // keys 16b + g (+ 8 from the third on), rows 2t, 2t + 1
 #pragma unroll
-            for (int tm = 0; tm < TM; ++tm)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sv[tm][n][i] = 0.f;
+                    for (int i = 0; i < 4; ++i) sv[n][b][i] = 0.f;
 #pragma unroll
             for (int c = 0; c < DT / 32; ++c) {
-                uint32_t kf[4], qa[TM][2][4];
+                uint32_t kf[4];
                 ldsm4(kf, k_a + code_at<kRow>(lane, c));
+                uint4 q[NT];
 #pragma unroll
-                for (int tm = 0; tm < TM; ++tm)
+                for (int n = 0; n < NT; ++n) {
+                    if constexpr (Sh::kQReg) q[n] = qf[c][n];
+                    else q[n] = load_q(c, n);
+                }
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(s_q + query_at<DT>(16 * tm + g + 8 * r, 4 * c + t));
-                        qa[tm][0][r] = x.x, qa[tm][0][2 + r] = x.y, qa[tm][1][r] = x.z, qa[tm][1][2 + r] = x.w;
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t h[2][4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        e2m1x8_f16(kf[2 * b + i], h[i]);
+                        const uint32_t a = both(scale[2 * b + i][c / 2], c & 1);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) h[i][j] = hmul2(h[i][j], a);
                     }
+                    const uint32_t a0[4] = {h[0][0], h[1][0], h[0][1], h[1][1]}, a1[4] = {h[0][2], h[1][2], h[0][3], h[1][3]};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t h[4];
-                    e2m1x8_f16(kf[i], h);
-                    const uint32_t a = both(scale[i][c / 2], c & 1);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) h[j] = hmul2(h[j], a);
-#pragma unroll
-                    for (int tm = 0; tm < TM; ++tm) {
-                        mma16816<true>(sv[tm][i], qa[tm][0], h[0], h[1]);
-                        mma16816<true>(sv[tm][i], qa[tm][1], h[2], h[3]);
+                    for (int n = 0; n < NT; ++n) {
+                        mma16816<true>(sv[n][b], a0, q[n].x, q[n].y);
+                        mma16816<true>(sv[n][b], a1, q[n].z, q[n].w);
                     }
                 }
             }
             // ---- scores; hidden keys at -inf.  Their scale (to units of log 2) is not negative, so the
             // largest is found before scaling and the scaling is part of the exponent's addition.
             const bool masked = first + KS - 1 > pos_lo || (p.window > 0 && first <= pos_hi - p.window);
-            uint32_t hidden[TM][2];                      // bit 2n + i: key 8n + 2t + i is hidden from row g (+ 8)
-            float nm[TM][2];
-            bool moved = false;
+            uint32_t hidden[NT];                             // bit 4r + i: key 8i + g is hidden from row 2t + r
+            bool above = false;
+            float big[NT][2];
 #pragma unroll
-            for (int tm = 0; tm < TM; ++tm)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    hidden[tm][r] = 0;
-                    if (masked) {
-                        const int pos = pc.r.len + (pc.tile * M + 16 * tm + g + 8 * r) / p.G;
-#pragma unroll
-                        for (int n = 0; n < 4; ++n)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int key = first + 8 * n + 2 * t + i;
-                                if (key > pos || key >= pc.span.hi || (p.window > 0 && key <= pos - p.window)) {
-                                    hidden[tm][r] |= 1u << (2 * n + i);
-                                    sv[tm][n][2 * r + i] = ninf;
-                                }
-                            }
-                    }
-                    float m2[2] = {ninf, ninf};
-#pragma unroll
-                    for (int n = 0; n < 4; ++n)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) m2[i] = fmaxf(m2[i], sv[tm][n][2 * r + i]);
-                    float mm = fmaxf(m2[0], m2[1]);
-                    mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 1));
-                    mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 2));
-                    mm = fmaxf(mx[tm][r], mm == ninf ? ninf : mm * sc[tm][r]);
-                    nm[tm][r] = mm;
-                    moved |= mm != mx[tm][r];
-                }
-            if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-                for (int tm = 0; tm < TM; ++tm)
+            for (int n = 0; n < NT; ++n) {
+                hidden[n] = 0;
+                if (masked) {
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const float a = fast_exp2(mx[tm][r] - (nm[tm][r] == ninf ? 0.f : nm[tm][r]));
-                        l[tm][r] *= a;
-                        mx[tm][r] = nm[tm][r];
+                        const int pos = pc.r.len + (pc.tile * M + 8 * n + 2 * t + r) / p.G;
 #pragma unroll
-                        for (int n = 0; n < DT / 8; ++n) {
-                            o[tm][n][2 * r] *= a;
-                            o[tm][n][2 * r + 1] *= a;
+                        for (int i = 0; i < 4; ++i) {
+                            const int key = first + 8 * i + g;
+                            if (key > pos || key >= pc.span.hi || (p.window > 0 && key <= pos - p.window)) {
+                                hidden[n] |= 1u << (4 * r + i);
+                                sv[n][i >> 1][(i & 1) * 2 + r] = ninf;
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    big[n][r] = fmaxf(fmaxf(sv[n][0][r], sv[n][0][2 + r]), fmaxf(sv[n][1][r], sv[n][1][2 + r]));
+                    above |= big[n][r] * sc[n][r] > mx[n][r] + 1.f;
+                }
+            }
+            if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float m = big[n][r];
+#pragma unroll
+                        for (int x = 4; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+                        m = fmaxf(mx[n][r], m == ninf ? ninf : m * sc[n][r]);
+                        const float a = fast_exp2(mx[n][r] - (m == ninf ? 0.f : m));
+                        l[n][r] *= a;
+                        mx[n][r] = m;
+#pragma unroll
+                        for (int d = 0; d < DT / 16; ++d) {
+                            o[n][d][r] *= a;
+                            o[n][d][2 + r] *= a;
                         }
                     }
             }
-            // ---- P
-            uint32_t ph[TM][2][4];
+            // ---- P'
+            uint32_t pb[NT][2][2];
 #pragma unroll
-            for (int tm = 0; tm < TM; ++tm)
+            for (int n = 0; n < NT; ++n) {
+                const float use0 = (mx[n][0] == ninf ? 0.f : mx[n][0]) - kShift, use1 = (mx[n][1] == ninf ? 0.f : mx[n][1]) - kShift;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float use = (mx[tm][r] == ninf ? 0.f : mx[tm][r]) - kShift;
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const float e0 = fast_exp2(fmaf(sv[tm][n][2 * r], sc[tm][r], -use));
-                        const float e1 = fast_exp2(fmaf(sv[tm][n][2 * r + 1], sc[tm][r], -use));
-                        l[tm][r] += e0 + e1;
-                        ph[tm][n >> 1][(n & 1) * 2 + r] = pack_f16(e0, e1);
+                    for (int i = 0; i < 2; ++i) {
+                        const float e0 = fast_exp2(fmaf(sv[n][b][2 * i], sc[n][0], -use0));
+                        const float e1 = fast_exp2(fmaf(sv[n][b][2 * i + 1], sc[n][1], -use1));
+                        l[n][0] += e0;
+                        l[n][1] += e1;
+                        pb[n][b][i] = turned8x8(pack_f16(e0, e1));
                     }
-                }
-            // ---- O += P V.  A hidden key's P is 0, which keeps its value out as long as that is a number.
+            }
+            // ---- O' += V' P'.  A hidden key's P is 0, which keeps its value out as long as that is a number.
             // Steps with hidden keys look at the scales: a block that is not a number is added here, to
             // the rows that see it, and becomes 0 for the product.
             if (masked) {
@@ -382,19 +415,18 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, TM>::kPerSm)) attend_mma4(
                 if (__any_sync(0xffffffffu, odd)) {
 #pragma unroll 1
                     for (int j = 0; j < KS; ++j) {
-                        const int src = g * 4 + ((j & 7) >> 1), bit = 2 * (j >> 3) + (j & 1);
 #pragma unroll
-                        for (int tm = 0; tm < TM; ++tm)
+                        for (int n = 0; n < NT; ++n) {
+                            const uint32_t seen = ~__shfl_sync(0xffffffffu, hidden[n], (j & 7) * 4 + t) >> (j >> 3);
 #pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                const bool in = !(__shfl_sync(0xffffffffu, hidden[tm][r], src) >> bit & 1u);
+                            for (int c = 0; c < DT / 32; ++c)
+                                if (any_odd<true>(vs[j * kScale + 2 * c + (g >> 2)])) {
 #pragma unroll
-                                for (int c = 0; c < DT / 32; ++c)
-                                    if (in && any_odd<true>(vs[j * kScale + 2 * c + (t >> 1)])) {
-#pragma unroll
-                                        for (int n = 0; n < 4; ++n) o[tm][4 * c + n][2 * r] = o[tm][4 * c + n][2 * r + 1] = __uint_as_float(0x7fffffffu);
-                                    }
-                            }
+                                    for (int r = 0; r < 2; ++r)
+                                        if (seen >> (4 * r) & 1u)
+                                            o[n][2 * c][r] = o[n][2 * c][2 + r] = o[n][2 * c + 1][r] = o[n][2 * c + 1][2 + r] = __uint_as_float(0x7fffffffu);
+                                }
+                        }
                     }
                     __syncwarp();
                     for (int i = lane; i < KS * kScale / 4; i += 32) {
@@ -418,25 +450,21 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, TM>::kPerSm)) attend_mma4(
                 ldsm4_t(vf, v_a + code_at<kRow>(lane, c));
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    uint32_t bf[4][2];                       // of tile j: keys 16b + 2t (+1), and 16b + 8 + 2t (+1)
+                    uint32_t a[2][4];                        // of tile j: rows g and g + 8, keys 16b + 2t (+ 1), and 8 on
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         uint32_t h[4];
                         e2m1x8_f16(vf[2 * b + i], h);
-                        const uint32_t a0 = both(vscale[2 * b + i][0][c / 2], c & 1), a1 = both(vscale[2 * b + i][1][c / 2], c & 1);
-                        h[0] = hmul2(h[0], a0);
-                        h[1] = hmul2(h[1], a0);
-                        h[2] = hmul2(h[2], a1);
-                        h[3] = hmul2(h[3], a1);
-                        bf[0][i] = __byte_perm(h[0], h[2], 0x5410);
-                        bf[1][i] = __byte_perm(h[0], h[2], 0x7632);
-                        bf[2][i] = __byte_perm(h[1], h[3], 0x5410);
-                        bf[3][i] = __byte_perm(h[1], h[3], 0x7632);
+                        const uint32_t s0 = in_low(vscale[2 * b + i][0][c / 2], c & 1), s1 = in_high(vscale[2 * b + i][1][c / 2], c & 1);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) a[j][2 * i + r] = hfma2(both(h[j], r), s0, hmul2(both(h[2 + j], r), s1));
                     }
 #pragma unroll
-                    for (int tm = 0; tm < TM; ++tm)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) mma16816<true>(o[tm][4 * c + j], ph[tm][b], bf[j][0], bf[j][1]);
+                        for (int j = 0; j < 2; ++j) mma16816<true>(o[n][2 * c + j], a[j], pb[n][b][0], pb[n][b][1]);
                 }
             }
         }
@@ -446,23 +474,21 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, TM>::kPerSm)) attend_mma4(
         // ---- the four warps' results join
         float* mine = reinterpret_cast<float*>(ring);
 #pragma unroll
-        for (int tm = 0; tm < TM; ++tm)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float sum = l[tm][r];
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                const int m = 16 * tm + g + 8 * r;
-                if (t == 0) {
-                    s_m[w][m] = mx[tm][r];
+                float sum = l[n][r];
+#pragma unroll
+                for (int x = 4; x < 32; x *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                const int m = 8 * n + 2 * t + r;
+                if (g == 0) {
+                    s_m[w][m] = mx[n][r];
                     s_l[w][m] = sum;
                 }
 #pragma unroll
                 for (int c = 0; c < DT / 32; ++c)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        *reinterpret_cast<float4*>(mine + m * Sh::kLd + 32 * c + 8 * t + 4 * i) =
-                            make_float4(o[tm][4 * c][2 * r + i], o[tm][4 * c + 1][2 * r + i], o[tm][4 * c + 2][2 * r + i], o[tm][4 * c + 3][2 * r + i]);
+                    *reinterpret_cast<float4*>(mine + m * Sh::kLd + 32 * c + 4 * g) =
+                        make_float4(o[n][2 * c][r], o[n][2 * c][2 + r], o[n][2 * c + 1][r], o[n][2 * c + 1][2 + r]);
             }
         __syncthreads();
         const bool whole = pc.whole();
@@ -518,18 +544,18 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, TM>::kPerSm)) attend_mma4(
     if (blockIdx.x == 0) head_cleared();
 }
 
-template <int DT, int TM>
+template <int DT, int NT>
 dspark_status_t launch_mma4(const Args& p, cudaStream_t s) {
-    using Sh = Mma4Shape<DT, TM>;
+    using Sh = Mma4Shape<DT, NT>;
     static OncePerDevice once;
     const int dev = current_device();
     if (once.run(dev, [] {
-            return cudaFuncSetAttribute(attend_mma4<DT, TM>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+            return cudaFuncSetAttribute(attend_mma4<DT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
         }) != cudaSuccess)
         return DSPARK_ERR_CUDA;
     const int grid = grid_for(sm_count(dev) * Sh::kPerSm, Sh::M);
     if (grid < 1) return DSPARK_ERR_CUDA;
-    return launch_cleared(p.status, kHeadBytes, attend_mma4<DT, TM>, dim3(grid), Sh::kThreads, Sh::kSmem, s, p);
+    return launch_cleared(p.status, kHeadBytes, attend_mma4<DT, NT>, dim3(grid), Sh::kThreads, Sh::kSmem, s, p);
 }
 
 }  // namespace attn
