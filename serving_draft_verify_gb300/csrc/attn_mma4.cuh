@@ -82,8 +82,14 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
-// The low (0) or the high (1) half twice; in the low half, over 0; in the high half, over 0.
-__device__ __forceinline__ uint32_t both(uint32_t x, int high) { return __byte_perm(x, 0, high ? 0x3232 : 0x1010); }
+// The low (0) or the high (1) half twice (as an operand this costs nothing, which a byte permutation
+// does); in the low half, over 0; in the high half, over 0.
+__device__ __forceinline__ uint32_t both(uint32_t x, int high) {
+    uint32_t r;
+    if (high) asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(r) : "r"(x));
+    else asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(r) : "r"(x));
+    return r;
+}
 __device__ __forceinline__ uint32_t in_low(uint32_t x, int high) { return high ? x >> 16 : x & 0xFFFFu; }
 __device__ __forceinline__ uint32_t in_high(uint32_t x, int high) { return high ? x & 0xFFFF0000u : x << 16; }
 // An 8 x 8 matrix of f16, two adjacent elements of a row a thread, transposed.
@@ -101,11 +107,7 @@ __device__ __forceinline__ void half_scales(const uint32_t* w, uint32_t pick, ui
         out[0] = e4m3x2_f16x2(__byte_perm(w[0], 0, pick));
     } else {
 #pragma unroll
-        for (int i = 0; i < DT / 128; ++i) {
-            const uint32_t four = __byte_perm(w[2 * i], w[2 * i + 1], pick);
-            out[2 * i] = e4m3x2_f16x2(four);
-            out[2 * i + 1] = e4m3x2_f16x2(four >> 16);
-        }
+        for (int i = 0; i < DT / 128; ++i) e4m3x4_f16(__byte_perm(w[2 * i], w[2 * i + 1], pick), out[2 * i], out[2 * i + 1]);
     }
 }
 template <int kWords>
@@ -148,6 +150,7 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
     const bool whole_pages = p.page % 16 == 0;               // 16 keys (half of a step's) lie on one page
     const bool adjacent = whole_pages && p.D == DT;          // and fill the rows
     const uint32_t k_pick = t < 2 ? 0x6420 : 0x7531, v_pick = g < 4 ? 0x6420 : 0x7531;
+    const uint32_t place0 = code_at<kRow>(lane / kChunks, lane % kChunks);
     const char* kc = static_cast<const char*>(p.kc);
     const char* vc = static_cast<const char*>(p.vc);
 
@@ -172,10 +175,9 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
             const int blk = p.page_shift >= 0 ? key >> p.page_shift : key / p.page;
             return Place{(static_cast<int64_t>(page_id(p, pc.b, blk)) * p.Hkv + pc.h) * p.g4.whole, key - blk * p.page};
         };
-        auto load = [&](int s, const Place& at) {
+        auto load = [&](int s, uint32_t to, const Place& at) {
             const int first = key0 + s * KT;
             if (s < steps && first < pc.span.hi && first + KS > pc.span.seen) {
-                const uint32_t to = ring_a + (s % kStages) * Sh::kStage;
                 const int64_t code = at.page + static_cast<int64_t>(at.row) * p.g4.code;
                 const int64_t scale = at.page + p.g4.codes + static_cast<int64_t>(at.row) * p.g4.scale;
                 if (adjacent && first >= pc.span.seen && first + KS <= pc.span.hi) {
@@ -187,7 +189,8 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
 #pragma unroll
                         for (int i = 0; i < kIn; ++i) {
                             const int e = lane + 32 * (kIn * b + i);
-                            const uint32_t d = to + code_at<kRow>(e / kChunks, e % kChunks);
+                            // 32 chunks of whole eights of rows on, the swizzle is the same
+                            const uint32_t d = to + (32 / kChunks % 8 == 0 ? place0 + 512 * (kIn * b + i) : code_at<kRow>(e / kChunks, e % kChunks));
                             cp_async16_at(d, kc + run + 512 * i);
                             cp_async16_at(d + kV, vc + run + 512 * i);
                         }
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
 #pragma unroll
         for (int s = 0; s < kStages; ++s) ahead[s] = find_rows(s);
 #pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) load(s, ahead[s]);
+        for (int s = 0; s < kStages - 1; ++s) load(s, ring_a + s * Sh::kStage, ahead[s]);
         Place rows = ahead[kStages - 1];
         copy_wait<kStages - 2>();
         __syncthreads();
@@ -271,7 +274,7 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
                 for (int n = 0; n < NT; ++n) qf[c][n] = load_q(c, n);
         }
         // This thread's query rows: 8n + 2t and 8n + 2t + 1, shared with the seven other g.
-        float sc[NT][2], mx[NT][2], l[NT][2];
+        float sc[NT][2], mx[NT][2], use[NT][2], l[NT][2];    // use: m as the exponents take it, without P's shift
         float o[NT][DT / 16][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -279,6 +282,7 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
             for (int r = 0; r < 2; ++r) {
                 sc[n][r] = fmaxf(s_qs[8 * n + 2 * t + r], 1.17549435e-38f);         // -inf times it is -inf
                 mx[n][r] = ninf;
+                use[n][r] = -kShift;
                 l[n][r] = 0.f;
             }
 #pragma unroll
@@ -288,15 +292,18 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
         }
 
         const int pos_lo = pc.r.len + pc.tile * M / p.G, pos_hi = pc.span.hi - 1;   // the tile's first and last position
+        int now = 0, last = (kStages - 1) * Sh::kStage;      // the step's stage and the one before, in the ring
         for (int s = 0; s < steps; ++s) {
             copy_wait<kStages - 2>();
             __syncwarp();
-            load(s + kStages - 1, rows);
+            load(s + kStages - 1, ring_a + last, rows);
             rows = find_rows(s + kStages);
             const int first = key0 + s * KT;
+            unsigned char* stage = ring + now;
+            const uint32_t k_a = ring_a + now, v_a = k_a + kV;
+            last = now;
+            now = now == (kStages - 1) * Sh::kStage ? 0 : now + Sh::kStage;
             if (first >= pc.span.hi || first + KS <= pc.span.seen) continue;
-            unsigned char* stage = ring + (s % kStages) * Sh::kStage;
-            const uint32_t k_a = ring_a + (s % kStages) * Sh::kStage, v_a = k_a + kV;
 
             // ---- S' = K Q'
             uint32_t scale[4][kPairs];                       // of keys 8i + g: this thread's block of every 32 elements
@@ -367,7 +374,7 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     big[n][r] = fmaxf(fmaxf(sv[n][0][r], sv[n][0][2 + r]), fmaxf(sv[n][1][r], sv[n][1][2 + r]));
-                    above |= big[n][r] * sc[n][r] > mx[n][r] + 1.f;
+                    above |= fmaf(big[n][r], sc[n][r], -mx[n][r]) > 1.f;
                 }
             }
             if (__any_sync(0xffffffffu, above)) {
@@ -382,6 +389,7 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
                         const float a = fast_exp2(mx[n][r] - (m == ninf ? 0.f : m));
                         l[n][r] *= a;
                         mx[n][r] = m;
+                        use[n][r] = (m == ninf ? 0.f : m) - kShift;
 #pragma unroll
                         for (int d = 0; d < DT / 16; ++d) {
                             o[n][d][r] *= a;
@@ -393,13 +401,12 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
             uint32_t pb[NT][2][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float use0 = (mx[n][0] == ninf ? 0.f : mx[n][0]) - kShift, use1 = (mx[n][1] == ninf ? 0.f : mx[n][1]) - kShift;
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float e0 = fast_exp2(fmaf(sv[n][b][2 * i], sc[n][0], -use0));
-                        const float e1 = fast_exp2(fmaf(sv[n][b][2 * i + 1], sc[n][1], -use1));
+                        const float e0 = fast_exp2(fmaf(sv[n][b][2 * i], sc[n][0], -use[n][0]));
+                        const float e1 = fast_exp2(fmaf(sv[n][b][2 * i + 1], sc[n][1], -use[n][1]));
                         l[n][0] += e0;
                         l[n][1] += e1;
                         pb[n][b][i] = turned8x8(pack_f16(e0, e1));
@@ -436,35 +443,38 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
                     __syncwarp();
                 }
             }
-            uint32_t vscale[4][2][kPairs];                   // of keys 8i + 2t and 8i + 2t + 1
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t x[kScale / 2];
-                load_words<kScale / 2>(stage + kVs + (8 * i + 2 * t) * kScale, x);
-                half_scales<DT>(x, v_pick, vscale[i][0]);
-                half_scales<DT>(x + kScale / 4, v_pick, vscale[i][1]);
-            }
+            for (int b = 0; b < 2; ++b) {
+                uint32_t vscale[2][2][kPairs];               // of keys 16b + 8i + 2t and the next
 #pragma unroll
-            for (int c = 0; c < DT / 32; ++c) {
-                uint32_t vf[4];
-                ldsm4_t(vf, v_a + code_at<kRow>(lane, c));
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t x[kScale / 2];
+                    load_words<kScale / 2>(stage + kVs + (16 * b + 8 * i + 2 * t) * kScale, x);
+                    half_scales<DT>(x, v_pick, vscale[i][0]);
+                    half_scales<DT>(x + kScale / 4, v_pick, vscale[i][1]);
+                }
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    uint32_t a[2][4];                        // of tile j: rows g and g + 8, keys 16b + 2t (+ 1), and 8 on
+                for (int c2 = 0; c2 < DT / 64; ++c2) {
+                    uint32_t vf[4];                          // keys 16b .. and 16b + 8 .. of 32 elements, then of the next 32
+                    ldsm4_t(vf, v_a + code_at<kRow>(16 * b + (lane & 15), 2 * c2 + (lane >> 4)));
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t h[4];
-                        e2m1x8_f16(vf[2 * b + i], h);
-                        const uint32_t s0 = in_low(vscale[2 * b + i][0][c / 2], c & 1), s1 = in_high(vscale[2 * b + i][1][c / 2], c & 1);
+                    for (int odd = 0; odd < 2; ++odd) {
+                        uint32_t a[2][4];                    // of tile j: rows g and g + 8, keys 16b + 2t (+ 1), and 8 on
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t h[4];
+                            e2m1x8_f16(vf[2 * odd + i], h);
+                            const uint32_t s0 = in_low(vscale[i][0][c2], odd), s1 = in_high(vscale[i][1][c2], odd);
 #pragma unroll
-                            for (int r = 0; r < 2; ++r) a[j][2 * i + r] = hfma2(both(h[j], r), s0, hmul2(both(h[2 + j], r), s1));
+                            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) a[j][2 * i + r] = hfma2(both(h[j], r), s0, hmul2(both(h[2 + j], r), s1));
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) mma16816<true>(o[n][4 * c2 + 2 * odd + j], a[j], pb[n][b][0], pb[n][b][1]);
                     }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) mma16816<true>(o[n][2 * c + j], a[j], pb[n][b][0], pb[n][b][1]);
                 }
             }
         }

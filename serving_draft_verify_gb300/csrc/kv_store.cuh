@@ -55,11 +55,19 @@ __device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t* h) {
         : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
         : "r"(w));
 }
-// Two e4m3 bytes as two f16 (exact), and one as a float.
+// Two e4m3 bytes as two f16 (exact), four as four, and one as a float.
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
     return r;
+}
+__device__ __forceinline__ void e4m3x4_f16(uint32_t four, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
 }
 __device__ __forceinline__ float f16lo(uint32_t w) {
     float f;
