@@ -254,14 +254,17 @@ struct Walk {
 // segment (it is the block's last piece) and one for a part that does not.
 __device__ __forceinline__ int64_t part_place(int block, bool starts) { return 2ll * block + (starts ? 1 : 0); }
 
-// The page id at entry j of request b's table, checked.
-__device__ __forceinline__ int page_id(const Args& p, int b, int j) {
-    int id = __ldg(p.table + static_cast<int64_t>(b) * p.ld_table + j);
+// A page id from a table, checked.
+__device__ __forceinline__ int checked_page(const Args& p, int id) {
     if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks)) {
         tell(p.status, DSPARK_ERR_DEVICE_CHECK, 2);
         id = 0;
     }
     return id;
+}
+// The page id at entry j of request b's table, checked.
+__device__ __forceinline__ int page_id(const Args& p, int b, int j) {
+    return checked_page(p, __ldg(p.table + static_cast<int64_t>(b) * p.ld_table + j));
 }
 
 // Four adjacent output elements, rounded once.

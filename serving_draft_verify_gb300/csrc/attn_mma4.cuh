@@ -23,11 +23,13 @@
 // two steps of the first product take them as they come (k = 2t, 2t + 1, 2t + 8, 2t + 9 stand for elements
 // 8t .. 8t + 3, then 8t + 4 .. 8t + 7), and Q's elements are those 16 bytes of its row, no permutation
 // needed.  All four bytes lie in one block of 16: one scale.  For the second product the transposing ldmatrix hands out
-// two bytes (elements 4g .. 4g + 3) of key 2t and the same two of key 2t + 1.  The halves of their
-// conversions have to be paired key by key; a multiplication by (s, 0) and one by (0, s') that adds to it do that
-// and the scaling at once, on the pipe that has less to do (permuting after scaling took it from the pipe
-// that converts).  Rows g and g + 8 of tile j then are elements 4g + 2j and 4g + 2j + 1, so that a thread
-// ends with four adjacent elements of its rows.
+// two bytes (elements 4g .. 4g + 3) of key 2t and the same two of key 2t + 1, whose conversions hold two elements of a key
+// where the operand wants an element of two keys.  For 8 query rows they are taken as they are, as if an
+// element's two neighbours were two keys: once with weights (P, 0), which gives the even elements, once with (0, P) for the
+// odd ones.  That is twice the products, which are few.  For more rows the halves are paired: a multiplication by
+// (0, s') and one by (s, 0) that adds to it do that and the scaling at once, on the pipe that has less to do than
+// the one that converts and permutes.  Either way rows g and g + 8 of tile r are elements 4g + r and 4g + 2 + r, and a
+// thread ends with four adjacent elements of its rows.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -46,8 +48,8 @@ struct Mma4Shape {
     static constexpr int kRow = DT / 2;                     // bytes of a row's codes
     static constexpr int kScale = DT / 16;                  // and of its scales
     static constexpr int kStage = 2 * KS * (kRow + kScale); // codes of keys, of values, scales of keys, of values
-    static constexpr int kPerSm = NT == 4 || DT > 128 ? 2 : NT == 2 ? 3 : 4;
-    static constexpr int kStages = DT <= 64 ? 4 : DT <= 128 ? (NT == 4 ? 4 : NT == 2 ? 3 : 2) : 2;
+    static constexpr int kPerSm = NT == 4 || DT > 128 ? 2 : 3;
+    static constexpr int kStages = DT <= 64 ? 4 : DT <= 128 ? (NT == 4 ? 4 : 3) : 2;
     static constexpr int kWarpBytes = kStage * kStages;     // also holds a warp's result at the end
     static constexpr int kLd = DT + 4;                      // row of that result, floats
     static constexpr int kQBytes = M * DT * 2;
@@ -163,23 +165,24 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
         // ---- the first keys and values are on their way before anything else
         const int steps = pc.u1 - pc.u0;
         const int key0 = pc.span.lo + pc.u0 * KT + w * KS;   // this warp's first key; then every KT
-        // Where the keys of step s lie: the head's page and the row in it of lane's key, or of the first of
-        // its 16 where a page holds them.
+        // Where the keys of step s lie: the page's id and the row in it of lane's key, or of the first of
+        // its 16 where a page holds them.  The id is looked at only when the copies are issued, a step later:
+        // checking it here would wait for it.
         struct Place {
-            int64_t page;
-            int row;
+            int id, row;
         };
+        const int32_t* table = p.table + static_cast<int64_t>(pc.b) * p.ld_table;
         auto find_rows = [&](int s) -> Place {
             const int key = key0 + s * KT + (whole_pages ? lane & 16 : lane);
             if (s >= steps || key + (whole_pages ? 15 : 0) < pc.span.seen || key >= pc.span.hi) return Place{0, 0};
             const int blk = p.page_shift >= 0 ? key >> p.page_shift : key / p.page;
-            return Place{(static_cast<int64_t>(page_id(p, pc.b, blk)) * p.Hkv + pc.h) * p.g4.whole, key - blk * p.page};
+            return Place{__ldg(table + blk), key - blk * p.page};
         };
         auto load = [&](int s, uint32_t to, const Place& at) {
             const int first = key0 + s * KT;
             if (s < steps && first < pc.span.hi && first + KS > pc.span.seen) {
-                const int64_t code = at.page + static_cast<int64_t>(at.row) * p.g4.code;
-                const int64_t scale = at.page + p.g4.codes + static_cast<int64_t>(at.row) * p.g4.scale;
+                const int64_t page = (static_cast<int64_t>(checked_page(p, at.id)) * p.Hkv + pc.h) * p.g4.whole;
+                const int64_t code = page + at.row * p.g4.code, scale = page + (p.g4.codes + at.row * p.g4.scale);
                 if (adjacent && first >= pc.span.seen && first + KS <= pc.span.hi) {
                     // sixteen rows are one run of codes and one of scales: 16 bytes a lane
                     constexpr int kIn = 16 * kChunks / 32;
@@ -459,21 +462,34 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
                     ldsm4_t(vf, v_a + code_at<kRow>(16 * b + (lane & 15), 2 * c2 + (lane >> 4)));
 #pragma unroll
                     for (int odd = 0; odd < 2; ++odd) {
-                        uint32_t a[2][4];                    // of tile j: rows g and g + 8, keys 16b + 2t (+ 1), and 8 on
+                        if constexpr (NT == 1) {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t h[4];
-                            e2m1x8_f16(vf[2 * odd + i], h);
-                            const uint32_t s0 = in_low(vscale[i][0][c2], odd), s1 = in_high(vscale[i][1][c2], odd);
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t h[4];
+                                e2m1x8_f16(vf[2 * odd + i], h);
+                                const uint32_t s0 = both(vscale[i][0][c2], odd), s1 = both(vscale[i][1][c2], odd);
+                                const uint32_t a[4] = {hmul2(h[0], s0), hmul2(h[1], s0), hmul2(h[2], s1), hmul2(h[3], s1)};
+                                const uint32_t x = pb[0][b][i];
+                                mma16816<true>(o[0][4 * c2 + 2 * odd], a, x & 0xFFFFu, x >> 16);
+                                mma16816<true>(o[0][4 * c2 + 2 * odd + 1], a, x << 16, x & 0xFFFF0000u);
+                            }
+                        } else {
+                            uint32_t a[2][4];                // of tile j: rows g and g + 8, keys 16b + 2t (+ 1), and 8 on
 #pragma unroll
-                            for (int j = 0; j < 2; ++j)
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t h[4];
+                                e2m1x8_f16(vf[2 * odd + i], h);
+                                const uint32_t s0 = in_low(vscale[i][0][c2], odd), s1 = in_high(vscale[i][1][c2], odd);
 #pragma unroll
-                                for (int r = 0; r < 2; ++r) a[j][2 * i + r] = hfma2(both(h[j], r), s0, hmul2(both(h[2 + j], r), s1));
+                                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                                    for (int r = 0; r < 2; ++r) a[r][2 * i + j] = hfma2(both(h[j], r), s0, hmul2(both(h[2 + j], r), s1));
+                            }
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) mma16816<true>(o[n][4 * c2 + 2 * odd + r], a[r], pb[n][b][0], pb[n][b][1]);
                         }
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) mma16816<true>(o[n][4 * c2 + 2 * odd + j], a[j], pb[n][b][0], pb[n][b][1]);
                     }
                 }
             }
@@ -498,7 +514,7 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
 #pragma unroll
                 for (int c = 0; c < DT / 32; ++c)
                     *reinterpret_cast<float4*>(mine + m * Sh::kLd + 32 * c + 4 * g) =
-                        make_float4(o[n][2 * c][r], o[n][2 * c][2 + r], o[n][2 * c + 1][r], o[n][2 * c + 1][2 + r]);
+                        make_float4(o[n][2 * c][r], o[n][2 * c + 1][r], o[n][2 * c][2 + r], o[n][2 * c + 1][2 + r]);
             }
         __syncthreads();
         const bool whole = pc.whole();
