@@ -81,21 +81,33 @@ __device__ __forceinline__ float f16hi(uint32_t w) {
 }
 __device__ __forceinline__ float e4m3_float(uint32_t byte) { return f16lo(e4m3x2_f16x2(byte)); }
 
-// A block of 16: its codes in two words and its scale's byte; r = 1 / (6 g).
-__device__ __forceinline__ uint32_t block4(const float* x, float g, float r, uint32_t* code) {
-    uint32_t big = 0;                           // of the magnitudes' bits: NaN is above all
+// The largest magnitude of eight, as its bits: they order as the numbers do, NaN above all.
+__device__ __forceinline__ uint32_t magnitude8(const float* x) {
+    uint32_t big = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) big = max(big, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    const bool nan = big > 0x7F800000u;
-    const uint32_t s = nan ? 0x7Fu : __nv_cvt_float_to_fp8(__uint_as_float(big) * r, __NV_SATFINITE, __NV_E4M3);
-    float inv = __frcp_rn(e4m3_float(s) * g);
-    if (!(inv < __uint_as_float(0x7f800000u))) inv = 0.f;
-    float y[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = x[i] * inv;
-    code[0] = nan ? 0u : e2m1x8(y);
-    code[1] = nan ? 0u : e2m1x8(y + 8);
+    for (int i = 0; i < 8; ++i) big = max(big, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    return big;
+}
+// A block's scale from its largest magnitude; r = 1 / (6 g).
+struct Scale4 {
+    uint32_t byte;
+    float inv;                                  // 0: the codes are 0
+    bool nan;
+};
+__device__ __forceinline__ Scale4 scale4(uint32_t big, float g, float r) {
+    Scale4 s;
+    s.nan = big > 0x7F800000u;
+    s.byte = s.nan ? 0x7Fu : __nv_cvt_float_to_fp8(__uint_as_float(big) * r, __NV_SATFINITE, __NV_E4M3);
+    s.inv = __frcp_rn(e4m3_float(s.byte) * g);
+    if (!(s.inv < __uint_as_float(0x7f800000u))) s.inv = 0.f;
     return s;
+}
+__device__ __forceinline__ uint32_t codes8(const float* x, const Scale4& s) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = x[i] * s.inv;
+    const uint32_t w = e2m1x8(y);
+    return s.nan ? 0u : w;
 }
 
 template <typename T>

@@ -11,7 +11,9 @@
 // Bound by memory: every element is read once and written once.  A block has a few rows: its threads
 // first make the rows' cosines and sines, then each has one place of a head (`unit`: two pieces of kSub
 // elements that hold whole pairs, so that a call in place needs no exchange) and goes over the heads
-// with it, queries, keys and values alike.
+// with it.  16384 rows of 40 heads of 128, bf16: 54 us for 336 MB (6.2 TB/s); 16384 rows of 32 heads on 8 with keys and
+// values stored in 4 bits: 72 us for 354 MB (4.9 TB/s), which is arithmetic of the blocks of 16 and the registers that
+// it holds from the loads; keys and values alone to 4 bits 27 us (86 MB), float32 to 4 bits (8192 rows) 60 us.
 #include <cmath>
 
 #include "launch.cuh"
@@ -22,6 +24,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kMaxRows = 4;                     // of a block
+constexpr int kItems = 2;                       // heads of keys and values in flight
+constexpr int kSub = 8;                         // elements of a piece
 constexpr int kMaxPairs = 128;                  // of a head
 constexpr int64_t kAlone = 256;                 // rows up to which one launch does, as in kv_write.cu
 
@@ -49,6 +53,14 @@ __device__ __forceinline__ float2 cos_sin(uint64_t a) {
     const float2 r = (q & 1) ? make_float2(-s, c) : make_float2(c, s);
     return (q & 2) ? make_float2(-r.x, -r.y) : r;
 }
+
+// Heads of queries in flight and blocks an SM asked for.  16384 rows of 32 heads on 8 of 128, bf16, to 4 bits, us:
+// 72 with 2 heads and 7 blocks, 75 with 3 and 6, 82 with 3 and 5, 95 with 3 heads and no blocks asked for; rotation alone takes
+// three heads and what registers it likes (40 heads 54, with 2 heads 57); float32 60 with 3 and 5, 70 with 2 and 7.
+template <typename T, Cache kCache>
+constexpr int kHeads = kCache == kNone || sizeof(T) == 4 ? 3 : 2;
+template <typename T, Cache kCache>
+constexpr int kBlocks = kCache == kNone ? 1 : sizeof(T) == 4 ? 5 : 7;
 
 // kN adjacent elements, as they lie in memory.
 template <typename T, int kN>
@@ -95,21 +107,77 @@ struct Piece {
     }
 };
 
+// Two pieces turned: pairs (j, kSub + j) of them, or adjacent elements.
+template <bool kInter>
+__device__ __forceinline__ void turn_floats(float* f, const float2* turn) {
+#pragma unroll
+    for (int j = 0; j < kSub; ++j) {
+        const int j1 = kInter ? 2 * j : j, j2 = kInter ? 2 * j + 1 : kSub + j;
+        const float x1 = f[j1], x2 = f[j2];
+        f[j1] = fmaf(x1, turn[j].x, -x2 * turn[j].y);
+        f[j2] = fmaf(x2, turn[j].x, x1 * turn[j].y);
+    }
+}
+template <typename T, bool kInter>
+__device__ __forceinline__ void turn_pieces(Piece<T, kSub>* x, const float2* turn) {
+    float f[2 * kSub];
+    x[0].floats(f);
+    x[1].floats(f + kSub);
+    turn_floats<kInter>(f, turn);
+    x[0].set(f);
+    x[1].set(f + kSub);
+}
+
 template <typename T, Cache kCache, bool kInter>
-__global__ void __launch_bounds__(kThreads) rotate_rows(const __grid_constant__ RotateArgs p) {
-    constexpr int kSub = kCache == kE2m1 ? 16 : 8;           // elements of a piece: a block of 16 stays in one thread
-    constexpr int kItems = kCache == kE2m1 ? 1 : 2;          // heads in flight
-    __shared__ float2 s_turn[kMaxRows][kMaxPairs];
-    __shared__ int64_t s_to[kMaxRows];                       // a row's place in the cache, in rows, -1: none
+__global__ void __launch_bounds__(kThreads, (kBlocks<T, kCache>)) rotate_rows(const __grid_constant__ RotateArgs p) {
+    __shared__ __align__(16) float2 s_turn[kMaxRows][kMaxPairs];
+    __shared__ int64_t s_to[kMaxRows];                       // a row's place in its page, -1: none
     __shared__ int s_block[kMaxRows];
     __shared__ bool s_live[kMaxRows];
+    constexpr int kHeads = dspark::kHeads<T, kCache>;
     const int tid = threadIdx.x, half = p.rot / 2;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_block;
+    // Where there are both, every second block has queries, the others keys and values: the former's
+    // bytes move while the latter's arithmetic runs (16384 rows to 4 bits: 79 us where a block did both).
+    const bool mixed = kCache != kNone && p.Hq > 0, stores = kCache != kNone && (!mixed || (blockIdx.x & 1) != 0);
+    const int64_t row0 = static_cast<int64_t>(mixed ? blockIdx.x >> 1 : blockIdx.x) * p.rows_per_block;
     const int64_t left = p.rows - row0;
     const int n = left < p.rows_per_block ? static_cast<int>(left) : p.rows_per_block;
     // Alone, the first block clears the status and looks at the slots of all rows.
     const bool all = p.alone && blockIdx.x == 0;
     if (all && tid < 4) reinterpret_cast<uint32_t*>(p.status)[tid] = 0;
+    const int u = tid % p.units, first = tid / p.units, groups = kThreads / p.units;
+    const bool turned = u < p.turned;
+    // the places of the unit's two pieces in a head
+    const int a = turned ? (kInter ? 2 * kSub * u : kSub * u) : p.rot + 2 * kSub * (u - p.turned);
+    const int b = turned && !kInter ? a + half : a + kSub;
+    const int heads = stores ? 2 * p.Hkv : p.Hq;             // keys', then values'; or queries'
+    // Keys and values of all rows: kItems heads at a time; the first are loaded while the angles are made.
+    struct Batch {
+        Piece<T, kSub> x[kItems][2];
+        int r[kItems], h[kItems];
+    };
+    int r_next = first < groups ? 0 : n, h_next = first;
+    auto load = [&](Batch& t) {
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            while (h_next >= heads) {
+                h_next -= heads;
+                ++r_next;
+            }
+            const int r = r_next, h = h_next;
+            t.r[i] = r;
+            t.h[i] = h;
+            h_next += groups;
+            if (r >= n) continue;
+            const bool is_v = h >= p.Hkv;
+            const T* from = static_cast<const T*>(is_v ? p.v : p.k) + (row0 + r) * (is_v ? p.v_stride : p.k_stride) +
+                            static_cast<int64_t>(is_v ? h - p.Hkv : h) * p.D;
+            t.x[i][0].load(from + a);
+            t.x[i][1].load(from + b);
+        }
+    };
+    Batch now;
+    if (stores) load(now);
     bool past = false;
     for (int r = tid; r < (all && p.slot != nullptr ? static_cast<int>(p.rows) : n); r += kThreads) {
         const bool live = p.position == nullptr || p.position[row0 + r] >= 0;
@@ -139,73 +207,66 @@ __global__ void __launch_bounds__(kThreads) rotate_rows(const __grid_constant__ 
     __syncthreads();
     if (past && (all || !p.alone)) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 1);
 
-    const int u = tid % p.units, first = tid / p.units, groups = kThreads / p.units;
-    const bool turned = u < p.turned;
-    // the places of the unit's two pieces in a head
-    const int a = turned ? (kInter ? 2 * kSub * u : kSub * u) : p.rot + 2 * kSub * (u - p.turned);
-    const int b = turned && !kInter ? a + half : a + kSub;
-    const int heads = p.Hq + (kCache != kNone ? 2 * p.Hkv : 0);
-    for (int r = 0; r < n; ++r) {
-        if (!s_live[r] || first >= groups) continue;
-        const int64_t row = row0 + r, to = s_to[r];
-        float2 turn[kSub];
-        if (turned) {
+    if (!stores) {
+        // ---- queries: a row at a time, so that its angles stay in registers
+        for (int r = 0; r < n; ++r) {
+            if (!s_live[r] || first >= groups) continue;
+            float2 turn[kSub];
+            if (turned) {
 #pragma unroll
-            for (int j = 0; j < kSub; j += 2)
-                *reinterpret_cast<float4*>(turn + j) = *reinterpret_cast<const float4*>(&s_turn[r][kSub * u + j]);
-        }
-        for (int h0 = first; h0 < heads; h0 += kItems * groups) {
-            Piece<T, kSub> x[kItems][2];
-#pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                const int h = h0 + i * groups;
-                if (h >= heads || (h >= p.Hq && to < 0)) continue;
-                const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-                const T* from = static_cast<const T*>(is_q ? p.q : is_v ? p.v : p.k) +
-                                row * (is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride) +
-                                static_cast<int64_t>(h - (is_q ? 0 : is_v ? p.Hq + p.Hkv : p.Hq)) * p.D;
-                x[i][0].load(from + a);
-                x[i][1].load(from + b);
+                for (int j = 0; j < kSub; j += 2)
+                    *reinterpret_cast<float4*>(turn + j) = *reinterpret_cast<const float4*>(&s_turn[r][kSub * u + j]);
             }
+            const T* from = static_cast<const T*>(p.q) + (row0 + r) * p.q_stride;
+            T* out = static_cast<T*>(p.out) + (row0 + r) * p.out_stride;
+            for (int h0 = first; h0 < heads; h0 += kHeads * groups) {
+                Piece<T, kSub> x[kHeads][2];
+#pragma unroll
+                for (int i = 0; i < kHeads; ++i) {
+                    const int h = h0 + i * groups;
+                    if (h >= heads) continue;
+                    x[i][0].load(from + h * p.D + a);
+                    x[i][1].load(from + h * p.D + b);
+                }
+#pragma unroll
+                for (int i = 0; i < kHeads; ++i) {
+                    const int h = h0 + i * groups;
+                    if (h >= heads) continue;
+                    if (turned) turn_pieces<T, kInter>(x[i], turn);
+                    x[i][0].store(out + h * p.D + a);
+                    x[i][1].store(out + h * p.D + b);
+                }
+            }
+        }
+    } else if constexpr (kCache != kNone) {
+        while (now.r[0] < n) {
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                const int h = h0 + i * groups;
-                if (h >= heads || (h >= p.Hq && to < 0)) continue;
-                const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-                float f[2 * kSub];
-                const bool as_is = is_v || !turned;
-                x[i][0].floats(f);
-                x[i][1].floats(f + kSub);
+                const int r = now.r[i], h = now.h[i];
+                if (r >= n || s_to[r] < 0) continue;
+                const int64_t to = s_to[r];
+                const bool is_v = h >= p.Hkv, as_is = is_v || !turned;
+                Piece<T, kSub>* x = now.x[i];
+                float2 turn[kSub];
                 if (!as_is) {
 #pragma unroll
-                    for (int j = 0; j < kSub; ++j) {
-                        const int j1 = kInter ? 2 * j : j, j2 = kInter ? 2 * j + 1 : kSub + j;
-                        const float x1 = f[j1], x2 = f[j2];
-                        f[j1] = fmaf(x1, turn[j].x, -x2 * turn[j].y);
-                        f[j2] = fmaf(x2, turn[j].x, x1 * turn[j].y);
-                    }
+                    for (int j = 0; j < kSub; j += 2)
+                        *reinterpret_cast<float4*>(turn + j) = *reinterpret_cast<const float4*>(&s_turn[r][kSub * u + j]);
                 }
-                if (is_q) {
-                    T* out = static_cast<T*>(p.out) + row * p.out_stride + static_cast<int64_t>(h) * p.D;
-                    if (!as_is) {
-                        x[i][0].set(f);
-                        x[i][1].set(f + kSub);
-                    }
-                    x[i][0].store(out + a);
-                    x[i][1].store(out + b);
-                    continue;
-                }
-                const int head = h - p.Hq - (is_v ? p.Hkv : 0);
+                const int head = is_v ? h - p.Hkv : h;
                 const int64_t page = static_cast<int64_t>(s_block[r]) * p.Hkv + head;
                 if constexpr (kCache == kSame) {
                     T* cache = static_cast<T*>(is_v ? p.vc : p.kc) + (page * p.page + to) * p.D;
-                    if (!as_is) {
-                        x[i][0].set(f);
-                        x[i][1].set(f + kSub);
-                    }
-                    x[i][0].store(cache + a);
-                    x[i][1].store(cache + b);
-                } else if constexpr (kCache == kE4m3) {
+                    if (!as_is) turn_pieces<T, kInter>(x, turn);
+                    x[0].store(cache + a);
+                    x[1].store(cache + b);
+                    continue;
+                }
+                float f[2 * kSub];
+                x[0].floats(f);
+                x[1].floats(f + kSub);
+                if (!as_is) turn_floats<kInter>(f, turn);
+                if constexpr (kCache == kE4m3) {
                     uint8_t* cache = static_cast<uint8_t*>(is_v ? p.vc : p.kc) + (page * p.page + to) * p.D;
                     const float scale = __ldg((is_v ? p.v_scale : p.k_scale) + head), inv = __fdiv_rn(1.f, scale), margin = margin_of(scale);
 #pragma unroll
@@ -221,16 +282,27 @@ __global__ void __launch_bounds__(kThreads) rotate_rows(const __grid_constant__ 
                 } else if constexpr (kCache == kE2m1) {
                     uint8_t* cache = static_cast<uint8_t*>(is_v ? p.vc : p.kc) + page * p.g.whole;
                     const float scale = __ldg((is_v ? p.v_scale : p.k_scale) + head), sixth = __frcp_rn(6.f * scale);
+                    uint8_t *codes = cache + to * p.g.code, *scales = cache + p.g.codes + to * p.g.scale;
+                    // Two pieces side by side are a block of 16; two that lie apart are halves of two, whose other
+                    // halves the neighbouring thread has (heads have an even number of units).
+                    uint32_t big[2] = {magnitude8(f), magnitude8(f + 8)};
+                    if (kInter || !turned) {
+                        big[0] = big[1] = max(big[0], big[1]);
+                    } else {
+                        const uint32_t pair = 3u << (tid & 30);
+                        big[0] = max(big[0], __shfl_xor_sync(pair, big[0], 1));
+                        big[1] = max(big[1], __shfl_xor_sync(pair, big[1], 1));
+                    }
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int at = j == 0 ? a : b;
-                        uint32_t code[2];
-                        const uint32_t s = block4(f + 16 * j, scale, sixth, code);
-                        *reinterpret_cast<uint2*>(cache + to * p.g.code + at / 2) = make_uint2(code[0], code[1]);
-                        cache[p.g.codes + to * p.g.scale + at / 16] = static_cast<uint8_t>(s);
+                        const Scale4 s = scale4(big[j], scale, sixth);
+                        *reinterpret_cast<uint32_t*>(codes + at / 2) = codes8(f + 8 * j, s);
+                        if ((at & 8) == 0) scales[at / 16] = static_cast<uint8_t>(s.byte);
                     }
                 }
             }
+            load(now);
         }
     }
     if (blockIdx.x == 0) head_cleared();
@@ -272,15 +344,14 @@ bool rows_ok(int64_t rows, int64_t width, dspark_dtype_t dt, const void* x, int6
 
 dspark_status_t launch_rotate(RotateArgs p, dspark_dtype_t dt, dspark_dtype_t cache_dt, cudaStream_t s) {
     const Cache c = p.Hkv == 0 ? kNone : cache_dt == DSPARK_E2M1 ? kE2m1 : cache_dt == DSPARK_E4M3 ? kE4m3 : kSame;
-    const int unit = c == kE2m1 ? 32 : 16;
-    p.units = p.D / unit;
-    p.turned = p.rot / unit;
+    p.units = p.D / 16;
+    p.turned = p.rot / 16;
     p.g = page4_of(p.page, p.D);
     p.rows_per_block = kMaxRows;
     while (p.rows_per_block > 1 && (p.rows + p.rows_per_block - 1) / p.rows_per_block < 2 * sm_count(current_device()))
         p.rows_per_block /= 2;
     p.alone = p.slot == nullptr || p.rows <= kAlone;
-    const unsigned grid = static_cast<unsigned>((p.rows + p.rows_per_block - 1) / p.rows_per_block);
+    const unsigned grid = static_cast<unsigned>((p.rows + p.rows_per_block - 1) / p.rows_per_block) * (p.Hq > 0 && p.Hkv > 0 ? 2 : 1);
     void (*kernel)(RotateArgs) = dt == DSPARK_BF16
                                      ? (p.interleaved ? kernel_of<__nv_bfloat16, true>(c) : kernel_of<__nv_bfloat16, false>(c))
                                      : (p.interleaved ? kernel_of<float, true>(c) : kernel_of<float, false>(c));
