@@ -31,38 +31,27 @@ constexpr int kSimtM = 16, kSimtKT = 32, kSimtThreads = 128;
 template <typename C>
 struct Staged {
     __host__ __device__ static int bytes(int D) { return D * static_cast<int>(sizeof(C)) + 16; }
-    __device__ static float4 four(const unsigned char* row, int d, int) {
+    __device__ static float4 four(const unsigned char* row, int d) {
         if constexpr (sizeof(C) == 4) return *reinterpret_cast<const float4*>(row + 4 * d);
         else return static_cast<float4>(*reinterpret_cast<const __nv_fp8x4_e4m3*>(row + d));
     }
-    __device__ static float2 two(const unsigned char* row, int d, int) {
+    __device__ static float2 two(const unsigned char* row, int d) {
         if constexpr (sizeof(C) == 4) return *reinterpret_cast<const float2*>(row + 4 * d);
         else return static_cast<float2>(*reinterpret_cast<const __nv_fp8x2_e4m3*>(row + d));
     }
 };
-// 4 bits: the codes, behind them the scales.
+// 4 bits: the codes, behind them the scales; a unit's rows become float rows before they are used.
 struct E2m1 {};
 template <>
 struct Staged<E2m1> {
     __host__ __device__ static int bytes(int D) { return (D / 2 + (D / 16 + 3) / 4 * 4 + 15) / 16 * 16 + 16; }
-    __device__ static float4 four(const unsigned char* row, int d, int D) {
-        uint32_t h[4];
-        e2m1x8_f16(*reinterpret_cast<const uint16_t*>(row + d / 2), h);
-        const float s = e4m3_float(row[D / 2 + d / 16]);
-        return make_float4(f16lo(h[0]) * s, f16hi(h[0]) * s, f16lo(h[1]) * s, f16hi(h[1]) * s);
-    }
-    __device__ static float2 two(const unsigned char* row, int d, int D) {
-        uint32_t h[4];
-        e2m1x8_f16(row[d / 2], h);
-        const float s = e4m3_float(row[D / 2 + d / 16]);
-        return make_float2(f16lo(h[0]) * s, f16hi(h[0]) * s);
-    }
 };
 template <typename C>
 constexpr bool kFour = std::is_same_v<C, E2m1>;
 template <typename C>
 size_t simt_smem(int D) {
-    return 4 * static_cast<size_t>(kSimtKT) * Staged<C>::bytes(D) + (static_cast<size_t>(kSimtM) * D + kSimtM * kSimtKT) * 4;
+    return 4 * static_cast<size_t>(kSimtKT) * Staged<C>::bytes(D) + (static_cast<size_t>(kSimtM) * D + kSimtM * kSimtKT) * 4 +
+           (kFour<C> ? 2 * static_cast<size_t>(kSimtKT) * Staged<float>::bytes(D) : 0);
 }
 
 template <typename C, int kCols>
@@ -73,6 +62,9 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
     unsigned char* s_kv = reinterpret_cast<unsigned char*>(smem4);                  // [2 stages][keys, values][KT] rows
     float* s_q = reinterpret_cast<float*>(s_kv + 4 * KT * row_bytes);              // [M][D]
     float* s_p = s_q + M * p.D;                        // [M][KT]: exp of the scores, -1 where masked
+    unsigned char* s_f = reinterpret_cast<unsigned char*>(s_p + M * KT);            // 4 bits: [keys, values][KT] float rows
+    using Row = std::conditional_t<kFour<C>, float, C>;
+    const int used_bytes = Staged<Row>::bytes(p.D);    // of a row as it is used
     __shared__ long long scratch[38];
     __shared__ float2 s_row[M];
     __shared__ int s_flag;
@@ -153,13 +145,33 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
             __syncthreads();
             const unsigned char* s_k = s_kv + ((u - pc.u0) & 1) * 2 * KT * row_bytes;
             const unsigned char* s_v = s_k + KT * row_bytes;
+            if constexpr (kFour<C>) {
+                // a block of 16 at a time, once for all four warps
+                const int blocks = p.D / 16;
+                for (int e = tid; e < 2 * KT * blocks; e += kSimtThreads) {
+                    const int r = e / blocks, i = e - r * blocks;
+                    const unsigned char* from = s_k + r * row_bytes;
+                    const uint2 w = *reinterpret_cast<const uint2*>(from + 8 * i);
+                    const float s = e4m3_float(from[p.D / 2 + i]);
+                    uint32_t h[8];
+                    e2m1x8_f16(w.x, h);
+                    e2m1x8_f16(w.y, h + 4);
+                    float4* to = reinterpret_cast<float4*>(s_f + r * used_bytes + 64 * i);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        to[j] = make_float4(f16lo(h[2 * j]) * s, f16hi(h[2 * j]) * s, f16lo(h[2 * j + 1]) * s, f16hi(h[2 * j + 1]) * s);
+                }
+                __syncthreads();
+                s_k = s_f;
+                s_v = s_f + KT * used_bytes;
+            }
             // The warp's rows are w, w + 4, ...: a tile with few rows has them spread over the warps.
             auto compute = [&](auto count) {
                 constexpr int R = decltype(count)::value;
                 float s[R] = {};
 #pragma unroll 4
                 for (int d = 0; d < p.D; d += 4) {
-                    const float4 k = Staged<C>::four(s_k + lane * row_bytes, d, p.D);
+                    const float4 k = Staged<Row>::four(s_k + lane * used_bytes, d);
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
                         const float4 q = *reinterpret_cast<const float4*>(s_q + (w + 4 * r) * p.D + d);
@@ -195,7 +207,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt(const __grid_constan
                         float2 v[kCols / 2];
 #pragma unroll
                         for (int c = 0; c < kCols / 2; ++c)
-                            v[c] = 2 * lane + 64 * c < p.D ? Staged<C>::two(s_v + (j + i) * row_bytes, 2 * lane + 64 * c, p.D) : make_float2(0.f, 0.f);
+                            v[c] = 2 * lane + 64 * c < p.D ? Staged<Row>::two(s_v + (j + i) * used_bytes, 2 * lane + 64 * c) : make_float2(0.f, 0.f);
 #pragma unroll
                         for (int r = 0; r < R; ++r) {
                             const float x = i == 0 ? e[r].x : i == 1 ? e[r].y : i == 2 ? e[r].z : e[r].w;
@@ -254,7 +266,7 @@ dspark_status_t launch_simt(const Args& p, cudaStream_t s) {
         }) != cudaSuccess)
         return DSPARK_ERR_CUDA;
     const size_t smem = simt_smem<C>(p.D);
-    const int per_sm = smem <= 52 * 1024 ? 4 : smem <= 108 * 1024 ? 2 : 1;
+    const int per_sm = smem <= 52 * 1024 ? 4 : kFour<C> && smem <= 72 * 1024 ? 3 : smem <= 108 * 1024 ? 2 : 1;
     const int grid = grid_for(sm_count(current_device()) * per_sm, kSimtM);
     if (grid < 1) return DSPARK_ERR_CUDA;
     return launch_cleared(p.status, kHeadBytes, attend_simt<C, kCols>, dim3(grid), kSimtThreads, smem, s, p);
@@ -266,12 +278,24 @@ dspark_status_t launch_f32(const Args& p, cudaStream_t s) {
     return launch_simt<C, 8>(p, s);
 }
 
-// 4-bit caches: 8, 16 or 32 query rows of a key head at a time, by the most that a request may have.
-dspark_status_t launch_bf16_e2m1(const Args& p, cudaStream_t s) {
+// 4-bit caches: tiles of 8, 16, 24 or 32 query rows of a key head, whichever takes the least for the most rows that
+// a request may have.  A tile's time goes as 8 + 5 for each eight (64 requests of up to 16384 keys: 150, 210 and
+// 329 us with 8, 16 and 32 rows).
+template <int DT>
+dspark_status_t launch_e2m1(const Args& p, cudaStream_t s) {
     const int64_t most = static_cast<int64_t>(p.max_rows) * p.G;
-    if (p.D <= 64) return most <= 8 ? launch_mma4<64, 1>(p, s) : most <= 16 ? launch_mma4<64, 2>(p, s) : launch_mma4<64, 4>(p, s);
-    if (p.D <= 128) return most <= 8 ? launch_mma4<128, 1>(p, s) : most <= 16 ? launch_mma4<128, 2>(p, s) : launch_mma4<128, 4>(p, s);
-    return most <= 8 ? launch_mma4<256, 1>(p, s) : launch_mma4<256, 2>(p, s);
+    int best = 1;
+    int64_t least = 0;
+    for (int n = 1; n <= (DT <= 128 ? 4 : 2); ++n) {
+        const int64_t cost = (most + 8 * n - 1) / (8 * n) * (8 + 5 * n);
+        if (n == 1 || cost < least) best = n, least = cost;
+    }
+    if (best == 1) return launch_mma4<DT, 1>(p, s);
+    if constexpr (DT <= 128) {
+        if (best == 3) return launch_mma4<DT, 3>(p, s);
+        if (best == 4) return launch_mma4<DT, 4>(p, s);
+    }
+    return launch_mma4<DT, 2>(p, s);
 }
 
 // bf16 rows: sixteen query rows at a time on the warp-level instructions, or 128 on tcgen05 where a
@@ -342,7 +366,10 @@ extern "C" dspark_status_t dspark_paged_attention(
     p.counters = reinterpret_cast<uint32_t*>(ws + kStatusBytes);
     p.part_ml = reinterpret_cast<float*>(ws + kStatusBytes + attn::kCounterBytes);
     p.part_o = p.part_ml + 2 * static_cast<size_t>(attn::kMaxPartRows);
-    if (cache_dt == DSPARK_E2M1) return dt == DSPARK_BF16 ? attn::launch_bf16_e2m1(p, s) : attn::launch_f32<attn::E2m1>(p, s);
+    if (cache_dt == DSPARK_E2M1) {
+        if (dt == DSPARK_F32) return attn::launch_f32<attn::E2m1>(p, s);
+        return D <= 64 ? attn::launch_e2m1<64>(p, s) : D <= 128 ? attn::launch_e2m1<128>(p, s) : attn::launch_e2m1<256>(p, s);
+    }
     const bool fp8 = cache_dt == DSPARK_E4M3;
     if (dt == DSPARK_BF16) return fp8 ? attn::launch_bf16<true>(p, s) : attn::launch_bf16<false>(p, s);
     return fp8 ? attn::launch_f32<__nv_fp8_e4m3>(p, s) : attn::launch_f32<float>(p, s);
