@@ -5,7 +5,8 @@ each round drafts a block, schedules its prefix, plans the rows the target has t
 stores their keys and values, attends over the paged cache, applies the requests'
 penalties and token mask to the target rows and verifies.  What is accepted advances
 the requests' lengths; the pages of rejected rows are reused.  Nothing is read back
-between rounds.
+between rounds.  With `rotary` the model turns its queries and keys by their positions, with
+`four_bits` the cache holds them in 4 bits; one call then rotates and stores.
 
     python examples/paged_round.py            # greedy, against decoding token by token
 """
@@ -40,7 +41,7 @@ class Rounds:
     """The serving state of B requests and the calls of one round, in order."""
 
     def __init__(self, model, prompts, gamma=4, page=8, blocks=256, room=None, repetition=1.3, presence=0.4,
-                 banned=(), max_new=64):
+                 banned=(), max_new=64, rotary=False, four_bits=False):
         self.m, self.B, self.gamma, self.page = model, len(prompts), gamma, page
         dev, B = model.emb.device, self.B
         self.room = room or B * (gamma + 1)
@@ -57,8 +58,15 @@ class Rounds:
         self.free_state = torch.tensor([0, blocks], **i32)
         self.free_ring = torch.arange(blocks, **i32)
         self.table = torch.zeros((B, -(-width // page)), **i32)
-        shape = (blocks, model.Hkv, page, model.D)
-        self.k_cache, self.v_cache = torch.zeros(shape, device=dev), torch.zeros(shape, device=dev)
+        self.freq = dsv.dspark_rotary_frequencies(model.D, device=dev)[0] if rotary else None
+        self.scales = {}
+        if four_bits:
+            self.k_cache, self.v_cache = (dsv.kv4_cache(blocks, model.Hkv, page, model.D, dev) for _ in range(2))
+            # a head's scale: its values' largest, here a few, over what a code and a block's scale reach
+            self.scales = {k: torch.full((model.Hkv,), 0.002, device=dev) for k in ("k_scale", "v_scale")}
+        else:
+            shape = (blocks, model.Hkv, page, model.D)
+            self.k_cache, self.v_cache = torch.zeros(shape, device=dev), torch.zeros(shape, device=dev)
         self.repetition = torch.full((B,), repetition, device=dev)
         self.presence = torch.full((B,), presence, device=dev)
         allowed = torch.ones(-(-model.V // 32) * 32, dtype=torch.bool)
@@ -74,10 +82,15 @@ class Rounds:
         m = self.m
         x = m.emb[tokens.clamp(min=0).long()]
         qkv = (x @ m.qkv).view(-1, m.Hq + 2 * m.Hkv, m.D)
-        dsv.dspark_write_kv(qkv[:, m.Hq:m.Hq + m.Hkv], qkv[:, m.Hq + m.Hkv:], plan["slot"], self.k_cache, self.v_cache)
+        q, k, v = qkv[:, :m.Hq], qkv[:, m.Hq:m.Hq + m.Hkv], qkv[:, m.Hq + m.Hkv:]
+        if self.freq is not None:
+            q = dsv.dspark_rotate_write_kv(q, k, v, plan["position"], self.freq, plan["slot"], self.k_cache, self.v_cache,
+                                           out=q, **self.scales)
+        else:
+            dsv.dspark_write_kv(k, v, plan["slot"], self.k_cache, self.v_cache, **self.scales)
         o = torch.zeros((x.shape[0], m.Hq, m.D), device=x.device)
-        dsv.dspark_paged_attention(qkv[:, :m.Hq], plan["row_offset"], plan["length"], self.table, self.k_cache,
-                                   self.v_cache, most, out=dict(out=o))
+        dsv.dspark_paged_attention(q, plan["row_offset"], plan["length"], self.table, self.k_cache, self.v_cache, most,
+                                   out=dict(out=o), **self.scales)
         return x + o.reshape(x.shape[0], -1) @ m.out
 
     def plan(self, rows, room):
@@ -132,8 +145,16 @@ class Rounds:
         return tokens, count
 
 
-def token_by_token(model, prompts, steps, repetition=1.3, presence=0.4, banned=()):
-    """The same greedy decoding without drafts, pages or the library, one request at a time."""
+def turned(x, freq):
+    """Row n of x [rows, heads, D] turned by n freq, in float64."""
+    a = torch.arange(x.shape[0], device=x.device)[:, None, None] * freq.double()
+    x1, x2 = x.chunk(2, -1)
+    return torch.cat([x1 * a.cos() - x2 * a.sin(), x2 * a.cos() + x1 * a.sin()], -1)
+
+
+def token_by_token(model, prompts, steps, repetition=1.3, presence=0.4, banned=(), freq=None, stored=None):
+    """The same greedy decoding without drafts, pages or the library, one request at a time; `stored` makes
+    of rows of keys or values what a cache holds of them."""
     got = []
     for p in prompts:
         said, new = list(p), []
@@ -141,7 +162,10 @@ def token_by_token(model, prompts, steps, repetition=1.3, presence=0.4, banned=(
             x = model.emb[torch.tensor(said, device=model.emb.device)].double()
             qkv = (x @ model.qkv.double()).view(len(said), -1, model.D)
             G = model.Hq // model.Hkv
-            k, v = (y.repeat_interleave(G, 1) for y in (qkv[:, model.Hq:model.Hq + model.Hkv], qkv[:, model.Hq + model.Hkv:]))
+            if freq is not None:
+                qkv[:, :model.Hq + model.Hkv] = turned(qkv[:, :model.Hq + model.Hkv], freq)
+            kv = (qkv[:, model.Hq:model.Hq + model.Hkv], qkv[:, model.Hq + model.Hkv:])
+            k, v = ((stored(y) if stored else y).repeat_interleave(G, 1) for y in kv)
             s = torch.einsum("hd,khd->hk", qkv[-1, :model.Hq], k) * model.D ** -0.5
             o = torch.einsum("hk,khd->hd", s.softmax(-1), v).reshape(-1)
             y = (x[-1] + o @ model.out.double()) @ model.head.double()

@@ -500,3 +500,30 @@ def test_streams_graphs_and_one_workspace(dsv):  # noqa: F811
         torch.cuda.synchronize()
         for k in ("q", "out", "lse"):
             assert torch.equal(out[k], want[i][k]) and torch.equal(other[k], want[1 - i][k])
+
+
+@pytest.mark.parametrize("four_bits", [False, True])
+def test_rounds_with_rotary_positions(dsv, four_bits):  # noqa: F811
+    """Whole decoding rounds whose target rotates, stores and attends: greedy speculative decoding emits what
+    decoding token by token does, with keys and values as the cache holds them."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import paged_round
+    m = paged_round.Model(D=32, seed=5)
+    prompts = [[1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11], [8, 9], [10, 300, 7]]
+    s = paged_round.Rounds(m, prompts, gamma=4, page=8, blocks=64, rotary=True, four_bits=four_bits)
+    s.prefill()
+    for i in range(8):
+        s.round(seed=i)
+    torch.cuda.synchronize()
+    g = np.full(m.Hkv, 0.002, np.float32)
+
+    def stored(x):
+        return torch.from_numpy(cache4.values(*cache4.quantise(x.float().cpu().numpy(), g), g)).to(x.device)
+
+    steps = int((s.history_len - s.prompt_len).max())
+    want = paged_round.token_by_token(m, prompts, steps, freq=s.freq, stored=stored if four_bits else None)
+    for b in range(3):
+        p, n = int(s.prompt_len[b]), int(s.history_len[b])
+        assert n - p >= 8 and s.history[b, p:n].tolist() == want[b][:n - p]
