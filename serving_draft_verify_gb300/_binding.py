@@ -859,6 +859,7 @@ def dspark_paged_attention(q, row_offset, length, block_table, k_cache, v_cache,
     """Attention of a step's rows over the paged cache.  q [n, Hq, D] (rows at any stride);
     row_offset [B + 1], length [B] (rows in the cache before the step), block_table [B,
     max_blocks] int32; max_rows: the most rows of one request; scale: 1 / sqrt(D) by default.
+    Caches of q's type, float8_e4m3fn, or 4-bit ones (kv4_cache), the latter two with k_scale, v_scale [Hkv].
     Returns dict out [n, Hq, D] and lse [n, Hq] float32 (an `out` without lse skips it)."""
     lib = load()
     dev = _device_of(k_cache, "k_cache")

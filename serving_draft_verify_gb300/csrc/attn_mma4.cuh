@@ -1,12 +1,18 @@
-// Attention over a 4-bit cache (kv_store.cuh has the format): 8, 16 or 32 query rows of a key head
+// Attention over a 4-bit cache (kv_store.cuh has the format): 8, 16, 24 or 32 query rows of a key head
 // at a time on the warp-level tensor instructions.
 //
 // The work is divided as in attn_mma.cuh: each of a block's four warps takes 32 keys of every unit of
 // 128, with a ring of its own, its own running maximum and sum and its own part of the output.  What
-// bounds it is not the bytes but turning codes into operands, some 250 instructions of a warp for 32 keys of
-// 128 elements, so keys and values are the side of the products that has 16 rows and the queries the one that
-// has 8: a step for up to 8 query rows (plain decoding with groups of 8 and fewer) then costs half the
-// products and half the exponentials.
+// bounds it is not the bytes but turning codes into operands (a conversion for two elements and a
+// multiplication for two, 256 of a warp's 640 instructions for 32 keys of 128 elements and 8 query rows), so keys and values
+// are the side of the products that has 16 rows and the queries the one that has 8: a step for up to 8 query rows (plain
+// decoding with groups of 8 and fewer) then costs half the products and half the exponentials.
+//
+// 32 heads on 8 of 128, pages of 16: 64 requests of one row and up to 16384 keys 150 us for 676 MB (4.5 TB/s,
+// issuing in 56 % of the cycles, three blocks an SM); 16 requests of 8 rows and up to 32768 keys 216 us
+// (32 rows a tile, two blocks an SM by registers, issuing in 47 %, tensor pipe 43 %); 128 requests of
+// up to 17 rows and 6000 keys 446 us (three tiles of 24).  Keys as the side of 8 took 235, 257 and 500; on
+// tcgen05, codes converted into shared memory by the way, 400, 271 and 640.
 //
 //   S' = K Q'    m16n8k16 in f16, query rows as columns,
 //   P' = 2^(S' - m), with a factor 2^14 that the sum carries too, rounded to 11 bits,
