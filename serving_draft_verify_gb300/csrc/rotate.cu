@@ -29,7 +29,8 @@ constexpr int kSub = 8;                         // elements of a piece
 constexpr int kMaxPairs = 128;                  // of a head
 constexpr int64_t kAlone = 256;                 // rows up to which one launch does, as in kv_write.cu
 
-enum Cache { kNone, kSame, kE4m3, kE2m1 };
+// kNone: queries alone; kFew: the same with fewer heads than a block has groups of threads.
+enum Cache { kNone, kFew, kSame, kE4m3, kE2m1 };
 
 // freq / 2 pi as a fraction of a turn in units of 2^-64: freq = m 2^(e - 25 + 2 - 64) with the constant
 // 2^66 / 2 pi.  Frequencies below 2^26; signs by the caller.
@@ -57,10 +58,11 @@ __device__ __forceinline__ float2 cos_sin(uint64_t a) {
 // Heads of queries in flight and blocks an SM asked for.  16384 rows of 32 heads on 8 of 128, bf16, to 4 bits, us:
 // 72 with 2 heads and 7 blocks, 75 with 3 and 6, 82 with 3 and 5, 95 with 3 heads and no blocks asked for; rotation alone takes
 // three heads and what registers it likes (40 heads 54, with 2 heads 57); float32 60 with 3 and 5, 70 with 2 and 7.
+// Few heads, 16384 rows of 8: 15.2 with 2 and 8, 16.3 without blocks asked for, 18.2 with 3, and 25.7 a row at a time.
 template <typename T, Cache kCache>
-constexpr int kHeads = kCache == kNone || sizeof(T) == 4 ? 3 : 2;
+constexpr int kHeads = kCache == kNone || (kCache != kFew && sizeof(T) == 4) ? 3 : 2;
 template <typename T, Cache kCache>
-constexpr int kBlocks = kCache == kNone ? 1 : sizeof(T) == 4 ? 5 : 7;
+constexpr int kBlocks = kCache == kNone ? 1 : sizeof(T) == 4 ? 5 : kCache == kFew ? 8 : 7;
 
 // kN adjacent elements, as they lie in memory.
 template <typename T, int kN>
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, kCache>)) rotate_rows(co
     const int tid = threadIdx.x, half = p.rot / 2;
     // Where there are both, every second block has queries, the others keys and values: the former's
     // bytes move while the latter's arithmetic runs (16384 rows to 4 bits: 79 us where a block did both).
-    const bool mixed = kCache != kNone && p.Hq > 0, stores = kCache != kNone && (!mixed || (blockIdx.x & 1) != 0);
+    const bool mixed = kCache > kFew && p.Hq > 0, stores = kCache > kFew && (!mixed || (blockIdx.x & 1) != 0);
     const int64_t row0 = static_cast<int64_t>(mixed ? blockIdx.x >> 1 : blockIdx.x) * p.rows_per_block;
     const int64_t left = p.rows - row0;
     const int n = left < p.rows_per_block ? static_cast<int>(left) : p.rows_per_block;
@@ -178,6 +180,22 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, kCache>)) rotate_rows(co
     };
     Batch now;
     if (stores) load(now);
+    // Few heads of queries: those of all rows in one line, the first loaded by now as well.
+    const int items = n * heads;
+    Piece<T, kSub> line[kCache == kFew ? kHeads : 1][2];
+    auto load_line = [&](int at) {
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+            const int e = at + i * groups, r = e / heads;
+            if (e >= items) continue;
+            const T* from = static_cast<const T*>(p.q) + (row0 + r) * p.q_stride + (e - r * heads) * p.D;
+            line[i][0].load(from + a);
+            line[i][1].load(from + b);
+        }
+    };
+    if constexpr (kCache == kFew) {
+        if (first < groups) load_line(first);
+    }
     bool past = false;
     for (int r = tid; r < (all && p.slot != nullptr ? static_cast<int>(p.rows) : n); r += kThreads) {
         const bool live = p.position == nullptr || p.position[row0 + r] >= 0;
@@ -207,7 +225,26 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, kCache>)) rotate_rows(co
     __syncthreads();
     if (past && (all || !p.alone)) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 1);
 
-    if (!stores) {
+    if constexpr (kCache == kFew) {
+        for (int at = first; first < groups && at < items; at += kHeads * groups) {
+            if (at != first) load_line(at);
+#pragma unroll
+            for (int i = 0; i < kHeads; ++i) {
+                const int e = at + i * groups, r = e / heads;
+                if (e >= items || !s_live[r]) continue;
+                if (turned) {
+                    float2 turn[kSub];
+#pragma unroll
+                    for (int j = 0; j < kSub; j += 2)
+                        *reinterpret_cast<float4*>(turn + j) = *reinterpret_cast<const float4*>(&s_turn[r][kSub * u + j]);
+                    turn_pieces<T, kInter>(line[i], turn);
+                }
+                T* out = static_cast<T*>(p.out) + (row0 + r) * p.out_stride + (e - r * heads) * p.D;
+                line[i][0].store(out + a);
+                line[i][1].store(out + b);
+            }
+        }
+    } else if (!stores) {
         // ---- queries: a row at a time, so that its angles stay in registers
         for (int r = 0; r < n; ++r) {
             if (!s_live[r] || first >= groups) continue;
@@ -238,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, kCache>)) rotate_rows(co
                 }
             }
         }
-    } else if constexpr (kCache != kNone) {
+    } else if constexpr (kCache > kFew) {
         while (now.r[0] < n) {
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
@@ -312,6 +349,7 @@ template <typename T, bool kInter>
 void (*kernel_of(Cache c))(RotateArgs) {
     switch (c) {
         case kNone: return rotate_rows<T, kNone, kInter>;
+        case kFew: return rotate_rows<T, kFew, kInter>;
         case kSame: return rotate_rows<T, kSame, kInter>;
         case kE4m3: return rotate_rows<T, kE4m3, kInter>;
         default: return rotate_rows<T, kE2m1, kInter>;
@@ -343,7 +381,7 @@ bool rows_ok(int64_t rows, int64_t width, dspark_dtype_t dt, const void* x, int6
 }  // namespace
 
 dspark_status_t launch_rotate(RotateArgs p, dspark_dtype_t dt, dspark_dtype_t cache_dt, cudaStream_t s) {
-    const Cache c = p.Hkv == 0 ? kNone : cache_dt == DSPARK_E2M1 ? kE2m1 : cache_dt == DSPARK_E4M3 ? kE4m3 : kSame;
+    const Cache c = p.Hkv == 0 ? (p.Hq <= kThreads / (p.D / 16) ? kFew : kNone) : cache_dt == DSPARK_E2M1 ? kE2m1 : cache_dt == DSPARK_E4M3 ? kE4m3 : kSame;
     p.units = p.D / 16;
     p.turned = p.rot / 16;
     p.g = page4_of(p.page, p.D);

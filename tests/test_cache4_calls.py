@@ -162,3 +162,24 @@ def test_many_requests_of_one_key(dsv):
         out, code = _run_attend(dsv, c)
         assert code[0] == 0
         _check(out, _oracle(c, vals), vals, dtype, 32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("n,heads,D,rot", [(700, 16, 128, 128), (1300, 17, 128, 64), (1301, 1, 16, 16), (1250, 7, 96, 64),
+                                           (1219, 21, 96, 96), (1300, 8, 256, 256), (640, 9, 256, 128), (5, 32, 64, 64)])
+def test_heads_about_a_blocks_groups(dsv, n, heads, D, rot, inter, dtype):
+    """As many heads as a block has groups of threads, one more, and few; several rows a block, the last block not full."""
+    x, position, freq = _case(n, n, heads, D, rot, dtype, 70000, 0)
+    out = torch.full(x.shape, 7.0, dtype=x.dtype, device="cuda")
+    dsv.dspark_rotate(x.cuda(), position.cuda(), freq.cuda(), inter, True, out=out)
+    xs, live = x.double().numpy(), position.numpy() >= 0
+    want = rotary.rotate(xs, position.numpy(), freq.numpy(), inter, True, 1.0)
+    tol = _tolerance(xs, want, freq.numpy(), inter, 1.0, torch.finfo(x.dtype).eps)
+    got = out.double().cpu().numpy()
+    assert (np.abs(got - want) <= tol)[live].all() and (got[~live] == 7).all()
+    y = x.cuda()
+    dsv.dspark_rotate(y, position.cuda(), freq.cuda(), inter, True, out=y)
+    assert torch.equal(y[position.cuda() >= 0], out[position.cuda() >= 0])
+    assert torch.equal(y[position.cuda() < 0], x.cuda()[position.cuda() < 0])
