@@ -54,7 +54,9 @@ struct Mma4Shape {
     static constexpr int kRow = DT / 2;                     // bytes of a row's codes
     static constexpr int kScale = DT / 16;                  // and of its scales
     static constexpr int kStage = 2 * KS * (kRow + kScale); // codes of keys, of values, scales of keys, of values
-    static constexpr int kPerSm = NT >= 3 || DT > 128 ? 2 : 3;
+    // Blocks an SM, by registers.  Four of 8 rows and heads of 128 have room for two stages only: 154 us for the 150
+    // above (heads of 64 105, with three blocks 109); two blocks 156.
+    static constexpr int kPerSm = NT >= 3 || DT > 128 ? 2 : NT == 1 && DT <= 64 ? 4 : 3;
     static constexpr int kStages = DT <= 64 ? 4 : DT <= 128 ? (NT == 4 ? 4 : 3) : 2;
     static constexpr int kWarpBytes = kStage * kStages;     // also holds a warp's result at the end
     static constexpr int kLd = DT + 4;                      // row of that result, floats
