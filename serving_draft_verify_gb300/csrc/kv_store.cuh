@@ -81,33 +81,33 @@ __device__ __forceinline__ float f16hi(uint32_t w) {
 }
 __device__ __forceinline__ float e4m3_float(uint32_t byte) { return f16lo(e4m3x2_f16x2(byte)); }
 
-// The largest magnitude of eight, as its bits: they order as the numbers do, NaN above all.
-__device__ __forceinline__ uint32_t magnitude8(const float* x) {
-    uint32_t big = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) big = max(big, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    return big;
+// The largest magnitude of eight, a NaN if there is one.
+__device__ __forceinline__ float magnitude3(float x, float y, float z) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+__device__ __forceinline__ float magnitude8(const float* x) {
+    return magnitude3(magnitude3(x[0], x[1], x[2]), magnitude3(x[3], x[4], x[5]), magnitude3(x[6], x[7], 0.f));
 }
 // A block's scale from its largest magnitude; r = 1 / (6 g).
 struct Scale4 {
     uint32_t byte;
-    float inv;                                  // 0: the codes are 0
-    bool nan;
+    float inv;                                  // 0: the codes are 0; NaN where the block has one
 };
-__device__ __forceinline__ Scale4 scale4(uint32_t big, float g, float r) {
+__device__ __forceinline__ Scale4 scale4(float big, float g, float r) {
     Scale4 s;
-    s.nan = big > 0x7F800000u;
-    s.byte = s.nan ? 0x7Fu : __nv_cvt_float_to_fp8(__uint_as_float(big) * r, __NV_SATFINITE, __NV_E4M3);
+    s.byte = big != big ? 0x7Fu : __nv_cvt_float_to_fp8(big * r, __NV_SATFINITE, __NV_E4M3);
     s.inv = __frcp_rn(e4m3_float(s.byte) * g);
-    if (!(s.inv < __uint_as_float(0x7f800000u))) s.inv = 0.f;
+    if (fabsf(s.inv) == __uint_as_float(0x7f800000u)) s.inv = 0.f;
     return s;
 }
-__device__ __forceinline__ uint32_t codes8(const float* x, const Scale4& s) {
+__device__ __forceinline__ uint32_t codes8(const float* x, float inv) {
     float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = x[i] * s.inv;
+    for (int i = 0; i < 8; ++i) y[i] = x[i] * inv;
     const uint32_t w = e2m1x8(y);
-    return s.nan ? 0u : w;
+    return inv != inv ? 0u : w;
 }
 
 template <typename T>

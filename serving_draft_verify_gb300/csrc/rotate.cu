@@ -13,7 +13,7 @@
 // elements that hold whole pairs, so that a call in place needs no exchange) and goes over the heads
 // with it.  16384 rows of 40 heads of 128, bf16: 54 us for 336 MB (6.2 TB/s); 16384 rows of 32 heads on 8 with keys and
 // values stored in 4 bits: 72 us for 354 MB (4.9 TB/s), which is arithmetic of the blocks of 16 and the registers that
-// it holds from the loads; keys and values alone to 4 bits 27 us (86 MB), float32 to 4 bits (8192 rows) 60 us.
+// it holds from the loads; keys and values alone to 4 bits 24 us (86 MB), float32 to 4 bits (8192 rows) 60 us.
 #include <cmath>
 
 #include "launch.cuh"
@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kMaxRows = 4;                     // of a block
-constexpr int kItems = 2;                       // heads of keys and values in flight
+constexpr int kItems = 2;                       // heads in flight where they stand in one line over the rows
 constexpr int kSub = 8;                         // elements of a piece
 constexpr int kMaxPairs = 128;                  // of a head
 constexpr int64_t kAlone = 256;                 // rows up to which one launch does, as in kv_write.cu
@@ -58,9 +58,9 @@ __device__ __forceinline__ float2 cos_sin(uint64_t a) {
 // Heads of queries in flight and blocks an SM asked for.  16384 rows of 32 heads on 8 of 128, bf16, to 4 bits, us:
 // 72 with 2 heads and 7 blocks, 75 with 3 and 6, 82 with 3 and 5, 95 with 3 heads and no blocks asked for; rotation alone takes
 // three heads and what registers it likes (40 heads 54, with 2 heads 57); float32 60 with 3 and 5, 70 with 2 and 7.
-// Few heads, 16384 rows of 8: 15.2 with 2 and 8, 16.3 without blocks asked for, 18.2 with 3, and 25.7 a row at a time.
+// Few heads, 16384 rows of 8: 14.5 with 8 blocks, 16.3 without asking for any, and 25.7 a row at a time.
 template <typename T, Cache kCache>
-constexpr int kHeads = kCache == kNone || (kCache != kFew && sizeof(T) == 4) ? 3 : 2;
+constexpr int kHeads = kCache == kNone || sizeof(T) == 4 ? 3 : 2;
 template <typename T, Cache kCache>
 constexpr int kBlocks = kCache == kNone ? 1 : sizeof(T) == 4 ? 5 : kCache == kFew ? 8 : 7;
 
@@ -153,7 +153,9 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, kCache>)) rotate_rows(co
     const int a = turned ? (kInter ? 2 * kSub * u : kSub * u) : p.rot + 2 * kSub * (u - p.turned);
     const int b = turned && !kInter ? a + half : a + kSub;
     const int heads = stores ? 2 * p.Hkv : p.Hq;             // keys', then values'; or queries'
-    // Keys and values of all rows: kItems heads at a time; the first are loaded while the angles are made.
+    // Heads of all the block's rows in one line, kItems at a time, the first loaded while the angles are made:
+    // keys and values, and queries with fewer heads than there are groups of threads, which would have
+    // one at a time (16384 rows of 12 heads on 1: 38 us, a row at a time 43; 32 heads on 8: 82 and 72).
     struct Batch {
         Piece<T, kSub> x[kItems][2];
         int r[kItems], h[kItems];
@@ -172,30 +174,15 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, kCache>)) rotate_rows(co
             h_next += groups;
             if (r >= n) continue;
             const bool is_v = h >= p.Hkv;
-            const T* from = static_cast<const T*>(is_v ? p.v : p.k) + (row0 + r) * (is_v ? p.v_stride : p.k_stride) +
-                            static_cast<int64_t>(is_v ? h - p.Hkv : h) * p.D;
+            const T* from = static_cast<const T*>(!stores ? p.q : is_v ? p.v : p.k) +
+                            (row0 + r) * (!stores ? p.q_stride : is_v ? p.v_stride : p.k_stride) + (stores && is_v ? h - p.Hkv : h) * p.D;
             t.x[i][0].load(from + a);
             t.x[i][1].load(from + b);
         }
     };
     Batch now;
-    if (stores) load(now);
-    // Few heads of queries: those of all rows in one line, the first loaded by now as well.
-    const int items = n * heads;
-    Piece<T, kSub> line[kCache == kFew ? kHeads : 1][2];
-    auto load_line = [&](int at) {
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-            const int e = at + i * groups, r = e / heads;
-            if (e >= items) continue;
-            const T* from = static_cast<const T*>(p.q) + (row0 + r) * p.q_stride + (e - r * heads) * p.D;
-            line[i][0].load(from + a);
-            line[i][1].load(from + b);
-        }
-    };
-    if constexpr (kCache == kFew) {
-        if (first < groups) load_line(first);
-    }
+    const bool rowwise = kCache == kNone || (kCache != kFew && !stores && heads > groups);
+    if (!rowwise) load(now);
     bool past = false;
     for (int r = tid; r < (all && p.slot != nullptr ? static_cast<int>(p.rows) : n); r += kThreads) {
         const bool live = p.position == nullptr || p.position[row0 + r] >= 0;
@@ -225,26 +212,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, kCache>)) rotate_rows(co
     __syncthreads();
     if (past && (all || !p.alone)) tell(p.status, DSPARK_ERR_DEVICE_CHECK, 1);
 
-    if constexpr (kCache == kFew) {
-        for (int at = first; first < groups && at < items; at += kHeads * groups) {
-            if (at != first) load_line(at);
-#pragma unroll
-            for (int i = 0; i < kHeads; ++i) {
-                const int e = at + i * groups, r = e / heads;
-                if (e >= items || !s_live[r]) continue;
-                if (turned) {
-                    float2 turn[kSub];
-#pragma unroll
-                    for (int j = 0; j < kSub; j += 2)
-                        *reinterpret_cast<float4*>(turn + j) = *reinterpret_cast<const float4*>(&s_turn[r][kSub * u + j]);
-                    turn_pieces<T, kInter>(line[i], turn);
-                }
-                T* out = static_cast<T*>(p.out) + (row0 + r) * p.out_stride + (e - r * heads) * p.D;
-                line[i][0].store(out + a);
-                line[i][1].store(out + b);
-            }
-        }
-    } else if (!stores) {
+    if (rowwise) {
         // ---- queries: a row at a time, so that its angles stay in registers
         for (int r = 0; r < n; ++r) {
             if (!s_live[r] || first >= groups) continue;
@@ -275,20 +243,29 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, kCache>)) rotate_rows(co
                 }
             }
         }
-    } else if constexpr (kCache > kFew) {
+    } else if constexpr (kCache != kNone) {
+        int of = -1;                                         // the head whose scale these are
+        float scale = 0.f, sixth = 0.f;
         while (now.r[0] < n) {
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
                 const int r = now.r[i], h = now.h[i];
-                if (r >= n || s_to[r] < 0) continue;
+                if (r >= n || !(stores ? s_to[r] >= 0 : s_live[r])) continue;
                 const int64_t to = s_to[r];
-                const bool is_v = h >= p.Hkv, as_is = is_v || !turned;
+                const bool is_v = h >= p.Hkv, as_is = (stores && is_v) || !turned;
                 Piece<T, kSub>* x = now.x[i];
                 float2 turn[kSub];
                 if (!as_is) {
 #pragma unroll
                     for (int j = 0; j < kSub; j += 2)
                         *reinterpret_cast<float4*>(turn + j) = *reinterpret_cast<const float4*>(&s_turn[r][kSub * u + j]);
+                }
+                if (!stores) {
+                    T* out = static_cast<T*>(p.out) + (row0 + r) * p.out_stride + h * p.D;
+                    if (!as_is) turn_pieces<T, kInter>(x, turn);
+                    x[0].store(out + a);
+                    x[1].store(out + b);
+                    continue;
                 }
                 const int head = is_v ? h - p.Hkv : h;
                 const int64_t page = static_cast<int64_t>(s_block[r]) * p.Hkv + head;
@@ -318,25 +295,29 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, kCache>)) rotate_rows(co
                     }
                 } else if constexpr (kCache == kE2m1) {
                     uint8_t* cache = static_cast<uint8_t*>(is_v ? p.vc : p.kc) + page * p.g.whole;
-                    const float scale = __ldg((is_v ? p.v_scale : p.k_scale) + head), sixth = __frcp_rn(6.f * scale);
+                    if (h != of) of = h, scale = __ldg((is_v ? p.v_scale : p.k_scale) + head), sixth = __frcp_rn(6.f * scale);
                     uint8_t *codes = cache + to * p.g.code, *scales = cache + p.g.codes + to * p.g.scale;
                     // Two pieces side by side are a block of 16; two that lie apart are halves of two, whose other
-                    // halves the neighbouring thread has (heads have an even number of units).
-                    uint32_t big[2] = {magnitude8(f), magnitude8(f + 8)};
+                    // halves the neighbouring thread has (heads have an even number of units): the first thread
+                    // makes the scale of the first block, the second that of the other.
+                    float big = magnitude8(f), inv[2];
+                    const float big2 = magnitude8(f + 8);
                     if (kInter || !turned) {
-                        big[0] = big[1] = max(big[0], big[1]);
+                        const Scale4 s = scale4(magnitude3(big, big2, 0.f), scale, sixth);
+                        inv[0] = inv[1] = s.inv;
+                        scales[a / 16] = static_cast<uint8_t>(s.byte);
                     } else {
                         const uint32_t pair = 3u << (tid & 30);
-                        big[0] = max(big[0], __shfl_xor_sync(pair, big[0], 1));
-                        big[1] = max(big[1], __shfl_xor_sync(pair, big[1], 1));
+                        const bool second = (tid & 1) != 0;
+                        const float theirs = __shfl_xor_sync(pair, second ? big : big2, 1);
+                        const Scale4 s = scale4(magnitude3(second ? big2 : big, theirs, 0.f), scale, sixth);
+                        const float other = __shfl_xor_sync(pair, s.inv, 1);
+                        inv[0] = second ? other : s.inv;
+                        inv[1] = second ? s.inv : other;
+                        scales[(second ? b : a) / 16] = static_cast<uint8_t>(s.byte);
                     }
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int at = j == 0 ? a : b;
-                        const Scale4 s = scale4(big[j], scale, sixth);
-                        *reinterpret_cast<uint32_t*>(codes + at / 2) = codes8(f + 8 * j, s);
-                        if ((at & 8) == 0) scales[at / 16] = static_cast<uint8_t>(s.byte);
-                    }
+                    *reinterpret_cast<uint32_t*>(codes + a / 2) = codes8(f, inv[0]);
+                    *reinterpret_cast<uint32_t*>(codes + b / 2) = codes8(f + 8, inv[1]);
                 }
             }
             load(now);
