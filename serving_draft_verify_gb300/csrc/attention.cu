@@ -279,8 +279,8 @@ dspark_status_t launch_f32(const Args& p, cudaStream_t s) {
 }
 
 // 4-bit caches: tiles of 8, 16, 24 or 32 query rows of a key head, whichever takes the least for the most rows that
-// a request may have.  A tile's time goes as 8 + 5 for each eight (64 requests of up to 16384 keys: 150, 210 and
-// 329 us with 8, 16 and 32 rows).
+// a request may have.  A tile's time goes as 8 + 5 for each eight (64 requests of up to 16384 keys: 148, 203 and
+// 298 us with 8, 16 and 32 rows).
 template <int DT>
 dspark_status_t launch_e2m1(const Args& p, cudaStream_t s) {
     const int64_t most = static_cast<int64_t>(p.max_rows) * p.G;

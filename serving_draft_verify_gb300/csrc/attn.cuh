@@ -12,9 +12,10 @@
 // Work list.  The query rows of one key head (row i, head g of its group; index
 // i G + g) are cut into tiles of M, and the keys a tile can see into units of KT.
 // All units of all (request, key head, tile) segments stand in one line, and block c
-// of n (n no more than W) takes units [c W / n, (c + 1) W / n): an even division whatever the lengths
-// are, found by every block from the lengths on the device.  A segment that no
-// block holds whole is joined by the last of its blocks to finish (a counter, nobody
+// of n (n no more than T, the line's length) takes units [c T / n, (c + 1) T / n): an even division
+// whatever the lengths are, found by every block from the lengths on the device.  Where a piece of a
+// segment costs as much by itself as W units do, W places that are no units stand before each
+// segment's.  A segment that no block holds whole is joined by the last of its blocks to finish (a counter, nobody
 // waits), its parts always in the order of the keys, so results do not depend on
 // who came last.
 #pragma once
@@ -95,16 +96,16 @@ __device__ __forceinline__ int tiles_of(const Args& p, const Request& r) {
 // waits for.
 struct Asked {
     Request r;
-    int64_t units;
+    int64_t units;                    // places in the line
 };
-template <int M, int KT>
+template <int M, int KT, int W>
 __device__ __noinline__ Asked ask(const Args& p, int b, bool report) {
     Asked a;
     a.r = request_of(p, b, report);
     a.units = 0;
     const int nt = tiles_of<M>(p, a.r);
 #pragma unroll 1
-    for (int t = 0; t < nt; ++t) a.units += span_of<M, KT>(p, a.r, t).units(KT);
+    for (int t = 0; t < nt; ++t) a.units += span_of<M, KT>(p, a.r, t).units(KT) + W;
     return a;
 }
 
@@ -123,7 +124,7 @@ struct Start {
     int64_t into;                     // units before `first` in request b
     Asked a;                          // request b
 };
-template <int M, int KT, int kThreads>
+template <int M, int KT, int kThreads, int W = 0>
 __device__ __forceinline__ Start find_start(const Args& p, long long* scratch) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int per = (p.B + kThreads - 1) / kThreads;
@@ -132,7 +133,7 @@ __device__ __forceinline__ Start find_start(const Args& p, long long* scratch) {
     Asked a{};
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-        a = ask<M, KT>(p, b, blockIdx.x == 0);
+        a = ask<M, KT, W>(p, b, blockIdx.x == 0);
         mine += p.Hkv * a.units;
     }
     long long inc = mine;
@@ -162,7 +163,7 @@ __device__ __forceinline__ Start find_start(const Args& p, long long* scratch) {
         int b = b0;
 #pragma unroll 1
         for (; b < b1; ++b) {
-            if (b1 - b0 > 1) a = ask<M, KT>(p, b, false);
+            if (b1 - b0 > 1) a = ask<M, KT, W>(p, b, false);
             if (s.first < u + p.Hkv * a.units) break;
             u += p.Hkv * a.units;
         }
@@ -198,10 +199,10 @@ struct Piece {
 
 // Walks the block's units piece by piece (every thread the same way).  The first piece is looked for
 // tile by tile; a further one starts the segment after the last (a prompt of 8192 rows has thousands).
-template <int M, int KT>
+template <int M, int KT, int W = 0>
 struct Walk {
     const Args& p;
-    int64_t at, last;
+    int64_t at, last;                 // at: the place of the piece's first unit
     int b, h, tile, u0;               // u0: units of the segment before the piece, -1 behind a segment
     Request r;
     __device__ __forceinline__ Walk(const Args& args, const Start& s)
@@ -212,15 +213,17 @@ struct Walk {
         const int nt = tiles_of<M>(p, r);
 #pragma unroll 1
         for (; tile + 1 < nt; ++tile) {
-            const int n = span_of<M, KT>(p, r, tile).units(KT);
+            const int n = span_of<M, KT>(p, r, tile).units(KT) + W;
             if (into < n) break;
             into -= n;
         }
-        u0 = static_cast<int>(into);
+        if (into < W) at += W - into;
+        u0 = into > W ? static_cast<int>(into) - W : 0;
     }
     __device__ __forceinline__ bool next(Piece& out) {
         if (at >= last) return false;
         if (u0 < 0) {
+            if (W > 0 && (at += W) >= last) return false;
             u0 = 0;
             if (++tile >= tiles_of<M>(p, r)) {
                 tile = 0;

@@ -8,10 +8,10 @@
 // are the side of the products that has 16 rows and the queries the one that has 8: a step for up to 8 query rows (plain
 // decoding with groups of 8 and fewer) then costs half the products and half the exponentials.
 //
-// 32 heads on 8 of 128, pages of 16: 64 requests of one row and up to 16384 keys 150 us for 676 MB (4.5 TB/s,
-// issuing in 56 % of the cycles, three blocks an SM); 16 requests of 8 rows and up to 32768 keys 216 us
+// 32 heads on 8 of 128, pages of 16: 64 requests of one row and up to 16384 keys 148 us for 676 MB (4.6 TB/s,
+// issuing in 56 % of the cycles, three blocks an SM); 16 requests of 8 rows and up to 32768 keys 210 us
 // (32 rows a tile, two blocks an SM by registers, issuing in 47 %, tensor pipe 43 %); 128 requests of
-// up to 17 rows and 6000 keys 446 us (three tiles of 24).  Keys as the side of 8 took 235, 257 and 500; on
+// up to 17 rows and 6000 keys 391 us (three tiles of 24).  Keys as the side of 8 took 235, 257 and 500; on
 // tcgen05, codes converted into shared memory by the way, 400, 271 and 640.
 //
 //   S' = K Q'    m16n8k16 in f16, query rows as columns,
@@ -51,11 +51,14 @@ struct Mma4Shape {
     static constexpr int M = 8 * NT;                        // query rows of a tile
     static constexpr int KS = 32;                           // keys of a warp's step
     static constexpr int KT = KS * kWarps;                  // keys of a unit
+    // What a piece costs by itself, in units (12,200 cycles and 3,900 with 32 query rows, 6,000 and 2,200 with 8).
+    // 256 requests of up to 500 keys: 8 rows 119 us, without 142, with five 122; 1 row 48, 60 and 48.
+    static constexpr int kOver = 3;
     static constexpr int kRow = DT / 2;                     // bytes of a row's codes
     static constexpr int kScale = DT / 16;                  // and of its scales
     static constexpr int kStage = 2 * KS * (kRow + kScale); // codes of keys, of values, scales of keys, of values
-    // Blocks an SM, by registers.  Four of 8 rows and heads of 128 have room for two stages only: 154 us for the 150
-    // above (heads of 64 105, with three blocks 109); two blocks 156.
+    // Blocks an SM, by registers.  Four of 8 rows and heads of 128 have room for two stages only: 154 us for 150
+    // (heads of 64 105, with three blocks 109); two blocks 156.
     static constexpr int kPerSm = NT >= 3 || DT > 128 ? 2 : NT == 1 && DT <= 64 ? 4 : 3;
     static constexpr int kStages = DT <= 64 ? 4 : DT <= 128 ? (NT == 4 ? 4 : 3) : 2;
     static constexpr int kWarpBytes = kStage * kStages;     // also holds a warp's result at the end
@@ -164,8 +167,8 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
     const char* kc = static_cast<const char*>(p.kc);
     const char* vc = static_cast<const char*>(p.vc);
 
-    const Start st = find_start<M, KT, kThreads>(p, scratch);
-    Walk<M, KT> walk(p, st);
+    const Start st = find_start<M, KT, kThreads, Sh::kOver>(p, scratch);
+    Walk<M, KT, Sh::kOver> walk(p, st);
     Piece pc;
     while (walk.next(pc)) {
         const int left = pc.r.n * p.G - pc.tile * M;
@@ -234,6 +237,10 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
             }
             copy_commit();
         };
+        Place ahead[kStages];
+#pragma unroll
+        for (int s = 0; s < kStages; ++s) ahead[s] = find_rows(s);
+        const float ks = fabsf(p.scale_log2) * p.k_scale[pc.h];
         // The queries first (16-bit, rows past the last zero): they arrive with the first keys.
         for (int e = tid; e < M * (DT / 8); e += kThreads) {
             const int m = e / (DT / 8), c = e - m * (DT / 8), qi = pc.tile * M + m;
@@ -243,37 +250,35 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
                                     : 0;
             copy16(q_a + query_at<DT>(m, c), static_cast<const __nv_bfloat16*>(p.q) + at, real);
         }
-        Place ahead[kStages];
-#pragma unroll
-        for (int s = 0; s < kStages; ++s) ahead[s] = find_rows(s);
 #pragma unroll
         for (int s = 0; s < kStages - 1; ++s) load(s, ring_a + s * Sh::kStage, ahead[s]);
         Place rows = ahead[kStages - 1];
         copy_wait<kStages - 2>();
         __syncthreads();
-        // rows to f16, in place: the largest element comes to 2^10 .. 2^11, a negative scale's sign with it
-        for (int m = w; m < M; m += kWarps) {
-            uint32_t own[kPairs];
+        // Rows to f16, in place, eight a warp and four lanes a row: the largest element comes to 2^10 .. 2^11, a
+        // negative scale's sign with it.
+        if (w < NT) {
+            const int m = 8 * w + g;
+            uint4 own[DT / 32];
             float big = 0.f;
 #pragma unroll
-            for (int k = 0; k < kPairs; ++k) {
-                const int i = lane + 32 * k;                 // pair i: columns 2i, 2i + 1
-                own[k] = i < DT / 2 ? *reinterpret_cast<const uint32_t*>(s_q + query_at<DT>(m, i >> 2) + (i & 3) * 4) : 0u;
-                big = fmaxf(big, fmaxf(fabsf(bf16lo(own[k])), fabsf(bf16hi(own[k]))));
+            for (int c = 0; c < DT / 32; ++c) {
+                own[c] = *reinterpret_cast<const uint4*>(s_q + query_at<DT>(m, 4 * c + t));
+                const uint32_t u[4] = {own[c].x, own[c].y, own[c].z, own[c].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) big = fmaxf(big, fmaxf(fabsf(bf16lo(u[i])), fabsf(bf16hi(u[i]))));
             }
-            big = warp_max(big);
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
             // 2^up and 2^-up by their exponent bits (up stays where both are normal numbers)
             int up = 0;
             if (big > 0.f && big < __uint_as_float(0x7f800000u)) up = min(10 - (static_cast<int>(__float_as_uint(big) >> 23) - 127), 126);
             const float grow = __uint_as_float((p.scale_log2 < 0.f ? 0x80000000u : 0u) | static_cast<uint32_t>(127 + up) << 23);
-            const float back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+            auto f16 = [&](uint32_t u) { return pack_f16(bf16lo(u) * grow, bf16hi(u) * grow); };
 #pragma unroll
-            for (int k = 0; k < kPairs; ++k) {
-                const int i = lane + 32 * k;
-                if (i < DT / 2)
-                    *reinterpret_cast<uint32_t*>(s_q + query_at<DT>(m, i >> 2) + (i & 3) * 4) = pack_f16(bf16lo(own[k]) * grow, bf16hi(own[k]) * grow);
-            }
-            if (lane == 0) s_qs[m] = fabsf(p.scale_log2) * p.k_scale[pc.h] * back;
+            for (int c = 0; c < DT / 32; ++c)
+                *reinterpret_cast<uint4*>(s_q + query_at<DT>(m, 4 * c + t)) = make_uint4(f16(own[c].x), f16(own[c].y), f16(own[c].z), f16(own[c].w));
+            if (t == 0) s_qs[m] = ks * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
         }
         __syncthreads();
         uint4 qf[Sh::kQReg ? DT / 32 : 1][Sh::kQReg ? NT : 1];
@@ -506,6 +511,7 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
         __syncwarp();
 
         // ---- the four warps' results join
+        const float vs = p.v_scale[pc.h];
         float* mine = reinterpret_cast<float*>(ring);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -532,7 +538,7 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
             float big = ninf, sum = 0.f;
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) big = fmaxf(big, s_m[i][tid]);
-            const float use = big == ninf ? 0.f : big, vs = p.v_scale[pc.h];
+            const float use = big == ninf ? 0.f : big;
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) sum += s_l[i][tid] * fast_exp2(s_m[i][tid] - use);
             const float f = !whole ? vs : sum != 0.f ? vs / sum : 0.f;

@@ -183,3 +183,17 @@ def test_heads_about_a_blocks_groups(dsv, n, heads, D, rot, inter, dtype):
     dsv.dspark_rotate(y, position.cuda(), freq.cuda(), inter, True, out=y)
     assert torch.equal(y[position.cuda() >= 0], out[position.cuda() >= 0])
     assert torch.equal(y[position.cuda() < 0], x.cuda()[position.cuda() < 0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("most,Hq,Hkv,D", [(1, 2, 2, 32), (5, 8, 2, 64), (9, 4, 1, 128)])
+def test_ragged_requests_in_number(dsv, most, Hq, Hkv, D, dtype):
+    """More segments than blocks, of no keys to some units, whole ones and split ones in one block."""
+    r = np.random.default_rng(most)
+    lens = [(int(r.integers(0, 700)) if r.random() < 0.7 else int(r.integers(0, 3)), int(r.integers(0, most + 1)))
+            for _ in range(400)]
+    c, vals = _attend_case(most, lens, Hq, Hkv, D, 16, dtype, 0)
+    out, code = _run_attend(dsv, c)
+    assert code[0] == 0
+    _check(out, _oracle(c, vals), vals, dtype, D)
