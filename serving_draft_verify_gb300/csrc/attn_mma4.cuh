@@ -11,7 +11,7 @@
 // 32 heads on 8 of 128, pages of 16: 64 requests of one row and up to 16384 keys 148 us for 676 MB (4.6 TB/s,
 // issuing in 56 % of the cycles, three blocks an SM); 16 requests of 8 rows and up to 32768 keys 210 us
 // (32 rows a tile, two blocks an SM by registers, issuing in 47 %, tensor pipe 43 %); 128 requests of
-// up to 17 rows and 6000 keys 391 us (three tiles of 24).  Keys as the side of 8 took 235, 257 and 500; on
+// up to 17 rows and 6000 keys 386 us (three tiles of 24).  Keys as the side of 8 took 235, 257 and 500; on
 // tcgen05, codes converted into shared memory by the way, 400, 271 and 640.
 //
 //   S' = K Q'    m16n8k16 in f16, query rows as columns,
@@ -554,11 +554,11 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
             }
         }
         __syncthreads();
-        const int four = p.D / 4;
-        float* part = p.part_o + part_place(blockIdx.x, pc.u0 == 0) * M * p.D;
+        constexpr int kCols = DT / 4;                        // threads of a row
+        const int d = tid % kCols * 4;
+        float* part = p.part_o + part_place(blockIdx.x, pc.u0 == 0) * M * p.D + d;
 #pragma unroll 2
-        for (int e = tid; e < valid * four; e += kThreads) {
-            const int m = e / four, d = (e - m * four) * 4;
+        for (int m = tid / kCols; m < (d < p.D ? valid : 0); m += kThreads / kCols) {
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) {
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
                 const int64_t row = static_cast<int64_t>(pc.r.row0) + qi / p.G;
                 store_four(static_cast<__nv_bfloat16*>(p.out) + (row * p.Hq + head) * p.D + d, x);
             } else {
-                store_four(part + m * p.D + d, x);
+                store_four(part + m * p.D, x);
             }
         }
         if (!whole && part_done(p, pc, st, &s_flag, tid, [] { __syncthreads(); }))
