@@ -15,11 +15,13 @@
 // tcgen05, codes converted into shared memory by the way, 400, 271 and 640.
 //
 //   S' = K Q'    m16n8k16 in f16, query rows as columns,
-//   P' = 2^(S' - m), with a factor 2^14 that the sum carries too, rounded to 11 bits,
+//   P' = 2^((S' - m) c + 14), rounded to 11 bits; the sum carries the factor 2^14 too,
 //   O' += V' P'  P' turned from accumulators to operands by movmatrix.
 //
-// m is the largest score of a row, or up to 1 (in units of log 2) below it: f16 has room for that, so
-// the maximum has to be found across the warp, and the output scaled, only in steps where a vote says so.
+// m is the largest product of a row so far, before its scale c (to units of log 2), or one whose score is up to 1 below
+// the largest: f16 has room for that, so the maximum has to be found across the warp, and the output scaled, only in steps
+// where a vote says so.  The difference is taken before it is scaled: m c rounded to float32 is off by 2 and more
+// from 2^25 on, which took P' past f16's largest.
 //
 // A stored value is code x block scale x head scale.  The product of the first two is exact in f16; the
 // head's scale goes into the scores' scale (keys) and the end result (values).  Q's rows are scaled by a
@@ -148,6 +150,7 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
     constexpr int kV = KS * kRow, kKs = 2 * KS * kRow, kVs = kKs + KS * kScale;      // parts of a stage behind the keys
     constexpr int kPairs = (DT + 63) / 64;                   // words of scales a thread keeps of one row
     constexpr float kShift = 14.f;                           // P carries 2^kShift
+    constexpr float kNone = -3.40282347e38f;                 // below any sum of products, and finite
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long scratch[38];
     __shared__ float s_m[kWarps][M], s_l[kWarps][M], s_qs[M];
@@ -278,7 +281,8 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
 #pragma unroll
             for (int c = 0; c < DT / 32; ++c)
                 *reinterpret_cast<uint4*>(s_q + query_at<DT>(m, 4 * c + t)) = make_uint4(f16(own[c].x), f16(own[c].y), f16(own[c].z), f16(own[c].w));
-            if (t == 0) s_qs[m] = ks * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+            // not 0: -inf times it is -inf, and kNone times it is below -1
+            if (t == 0) s_qs[m] = fmaxf(ks * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 1.17549435e-38f);
         }
         __syncthreads();
         uint4 qf[Sh::kQReg ? DT / 32 : 1][Sh::kQReg ? NT : 1];
@@ -290,15 +294,14 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
                 for (int n = 0; n < NT; ++n) qf[c][n] = load_q(c, n);
         }
         // This thread's query rows: 8n + 2t and 8n + 2t + 1, shared with the seven other g.
-        float sc[NT][2], mx[NT][2], use[NT][2], l[NT][2];    // use: m as the exponents take it, without P's shift
+        float sc[NT][2], mx[NT][2], l[NT][2];                // mx: m, kNone before a key is seen
         float o[NT][DT / 16][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                sc[n][r] = fmaxf(s_qs[8 * n + 2 * t + r], 1.17549435e-38f);         // -inf times it is -inf
-                mx[n][r] = ninf;
-                use[n][r] = -kShift;
+                sc[n][r] = s_qs[8 * n + 2 * t + r];
+                mx[n][r] = kNone;
                 l[n][r] = 0.f;
             }
 #pragma unroll
@@ -364,8 +367,7 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
                     }
                 }
             }
-            // ---- scores; hidden keys at -inf.  Their scale (to units of log 2) is not negative, so the
-            // largest is found before scaling and the scaling is part of the exponent's addition.
+            // ---- scores; hidden keys at -inf.  Their scale is positive, so the largest is found before scaling.
             const bool masked = first + KS - 1 > pos_lo || (p.window > 0 && first <= pos_hi - p.window);
             uint32_t hidden[NT];                             // bit 4r + i: key 8i + g is hidden from row 2t + r
             bool above = false;
@@ -390,7 +392,7 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     big[n][r] = fmaxf(fmaxf(sv[n][0][r], sv[n][0][2 + r]), fmaxf(sv[n][1][r], sv[n][1][2 + r]));
-                    above |= fmaf(big[n][r], sc[n][r], -mx[n][r]) > 1.f;
+                    above |= (big[n][r] - mx[n][r]) * sc[n][r] > 1.f;
                 }
             }
             if (__any_sync(0xffffffffu, above)) {
@@ -401,11 +403,10 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
                         float m = big[n][r];
 #pragma unroll
                         for (int x = 4; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-                        m = fmaxf(mx[n][r], m == ninf ? ninf : m * sc[n][r]);
-                        const float a = fast_exp2(mx[n][r] - (m == ninf ? 0.f : m));
+                        m = fmaxf(mx[n][r], m);
+                        const float a = fast_exp2((mx[n][r] - m) * sc[n][r]);
                         l[n][r] *= a;
                         mx[n][r] = m;
-                        use[n][r] = (m == ninf ? 0.f : m) - kShift;
 #pragma unroll
                         for (int d = 0; d < DT / 16; ++d) {
                             o[n][d][r] *= a;
@@ -421,8 +422,8 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float e0 = fast_exp2(fmaf(sv[n][b][2 * i], sc[n][0], -use[n][0]));
-                        const float e1 = fast_exp2(fmaf(sv[n][b][2 * i + 1], sc[n][1], -use[n][1]));
+                        const float e0 = fast_exp2(fmaf(sv[n][b][2 * i] - mx[n][0], sc[n][0], kShift));
+                        const float e1 = fast_exp2(fmaf(sv[n][b][2 * i + 1] - mx[n][1], sc[n][1], kShift));
                         l[n][0] += e0;
                         l[n][1] += e1;
                         pb[n][b][i] = turned8x8(pack_f16(e0, e1));
@@ -535,21 +536,25 @@ __global__ void __launch_bounds__(128, (Mma4Shape<DT, NT>::kPerSm)) attend_mma4(
         if (tid < M) {
             // a row's maximum and sum, and each warp's factor in its output (the values' scale and, where
             // this is the whole, the sum with it)
-            float big = ninf, sum = 0.f;
+            const float c = s_qs[tid];
+            float big = kNone, sum = 0.f;
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) big = fmaxf(big, s_m[i][tid]);
-            const float use = big == ninf ? 0.f : big;
+            // The maximum is m c as a float32 from here on; what that leaves out goes into the sum and the output
+            // (up to 2^63 either way, which scores below 2^30 stay within).
+            const float top = big == kNone ? ninf : big * c;
+            const float rest = top == ninf ? -kShift : fminf(fmaxf(fmaf(big, c, -top), -63.f), 63.f) - kShift;
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) sum += s_l[i][tid] * fast_exp2(s_m[i][tid] - use);
+            for (int i = 0; i < kWarps; ++i) sum += s_l[i][tid] * fast_exp2(fmaf(s_m[i][tid] - big, c, rest));
             const float f = !whole ? vs : sum != 0.f ? vs / sum : 0.f;
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) s_m[i][tid] = f * fast_exp2(s_m[i][tid] - use);
+            for (int i = 0; i < kWarps; ++i) s_m[i][tid] = f * fast_exp2(fmaf(s_m[i][tid] - big, c, rest));
             if (tid < valid) {
                 if (!whole) {
-                    reinterpret_cast<float2*>(p.part_ml)[part_place(blockIdx.x, pc.u0 == 0) * M + tid] = make_float2(big - kShift, sum);
+                    reinterpret_cast<float2*>(p.part_ml)[part_place(blockIdx.x, pc.u0 == 0) * M + tid] = make_float2(top, sum);
                 } else if (p.lse != nullptr) {
                     const int qi = pc.tile * M + tid;
-                    p.lse[(static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.Hq + pc.h * p.G + qi % p.G] = lse_of(big - kShift, sum);
+                    p.lse[(static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.Hq + pc.h * p.G + qi % p.G] = lse_of(top, sum);
                 }
             }
         }
