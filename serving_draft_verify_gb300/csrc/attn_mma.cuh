@@ -22,7 +22,8 @@
 // product but no bytes.  8-bit caches: stored values are exact in f16, so both products
 // run in f16; Q's rows are scaled by a power of two into f16's range, P carries a factor
 // 2^14 that the sum carries too and is rounded to 11 bits (half a step of 2^-12, below the
-// output's own 2^-9).  Bytes of a 16-byte chunk are taken in the order that one ldmatrix
+// output's own 2^-9).  f16 has no room for P where a score's rounding to float32 is 2 and more (from 2^25 on, in
+// units of log 2), so there m is the largest product before its scale c and P = 2^((S - m) c + 14).  Bytes of a 16-byte chunk are taken in the order that one ldmatrix
 // gives them (Q's columns are stored in that order), so a conversion is all they need.
 #pragma once
 
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
     constexpr int kSub = KS / 16;                            // 16-key blocks of a step
     constexpr int kChunks = kRow / 16;                       // 16-byte chunks of a stored row
     constexpr float kShift = kFp8 ? 14.f : 0.f;              // P carries 2^kShift
+    constexpr float kNone = kFp8 ? -3.40282347e38f : -__builtin_huge_valf();    // below any score; 8 bits: and finite
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long scratch[38];
     __shared__ float s_m[kWarps][M], s_l[kWarps][M], s_qs[M];
@@ -273,7 +275,8 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
                     if (i < DT / 2)
                         *reinterpret_cast<uint32_t*>(s_q + chunk_at<2 * DT>(m, to >> 2) + (to & 3) * 4) = own[k];
                 }
-                if (lane == 0) s_qs[m] = fabsf(p.scale_log2) * p.k_scale[pc.h] * back;
+                // not 0: -inf times it is -inf, and kNone times it is below -1
+                if (lane == 0) s_qs[m] = fmaxf(fabsf(p.scale_log2) * p.k_scale[pc.h] * back, 1.17549435e-38f);
             }
             __syncthreads();
         }
@@ -285,12 +288,12 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
 #pragma unroll
             for (int ks = 0; ks < DT / 16; ++ks) load_q(ks, qf[ks]);
         }
-        float sc[2], mx[2], l[2];
+        float sc[2], mx[2], l[2];                            // mx: the largest score; 8 bits: before its scale
         float o[DT / 8][4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            sc[r] = fmaxf(kFp8 ? s_qs[g + 8 * r] : fabsf(p.scale_log2), 1.17549435e-38f);   // -inf times it is -inf
-            mx[r] = ninf;
+            sc[r] = kFp8 ? s_qs[g + 8 * r] : fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);   // -inf times it is -inf
+            mx[r] = kNone;
             l[r] = 0.f;
         }
 #pragma unroll
@@ -332,7 +335,7 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
                     mma16816<false>(sv[1], a, kf[2], kf[3]);
                 }
             }
-            // ---- scores; hidden keys at -inf.  Their scale (to units of log 2) is not negative, so the
+            // ---- scores; hidden keys at -inf.  Their scale (to units of log 2) is positive, so the
             // largest is found before scaling and the scaling is part of the exponent's addition.
             const bool masked = first + KS - 1 > pos_lo || (p.window > 0 && first <= pos_hi - p.window);
             uint32_t hidden[2];                          // bit 2n + i: key 8n + 2t + i is hidden from row g (+ 8)
@@ -362,14 +365,15 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
                 float mm = fmaxf(m2[0], m2[1]);
                 mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 1));
                 mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 2));
-                mm = fmaxf(mx[r], mm == ninf ? ninf : mm * sc[r]);
+                if constexpr (kFp8) mm = fmaxf(mx[r], mm);
+                else mm = fmaxf(mx[r], mm == ninf ? ninf : mm * sc[r]);
                 nm[r] = mm;
                 moved |= mm != mx[r];
             }
             if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float a = fast_exp2(mx[r] - (nm[r] == ninf ? 0.f : nm[r]));
+                    const float a = kFp8 ? fast_exp2((mx[r] - nm[r]) * sc[r]) : fast_exp2(mx[r] - (nm[r] == ninf ? 0.f : nm[r]));
                     l[r] *= a;
                     mx[r] = nm[r];
 #pragma unroll
@@ -383,11 +387,11 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
             uint32_t ph[kSub][4], pl[kSub][4];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const float use = (mx[r] == ninf ? 0.f : mx[r]) - kShift;
+                const float use = mx[r] == ninf ? 0.f : mx[r];
+                auto weight = [&](float s) { return fast_exp2(kFp8 ? fmaf(s - use, sc[r], kShift) : fmaf(s, sc[r], -use)); };
 #pragma unroll
                 for (int n = 0; n < 2 * kSub; ++n) {
-                    const float e0 = fast_exp2(fmaf(sv[n][2 * r], sc[r], -use));
-                    const float e1 = fast_exp2(fmaf(sv[n][2 * r + 1], sc[r], -use));
+                    const float e0 = weight(sv[n][2 * r]), e1 = weight(sv[n][2 * r + 1]);
                     l[r] += e0 + e1;
                     sv[n][2 * r] = e0;
                     sv[n][2 * r + 1] = e1;
@@ -505,21 +509,26 @@ __global__ void __launch_bounds__(128, (MmaShape<kFp8, DT>::kPerSm)) attend_mma(
         if (tid < M) {
             // a row's maximum and sum, and each warp's factor in its output (the values' scale and, where
             // this is the whole, the sum with it)
-            float big = ninf, sum = 0.f;
+            float big = kNone, sum = 0.f;
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) big = fmaxf(big, s_m[i][tid]);
-            const float use = big == ninf ? 0.f : big, vs = kFp8 ? p.v_scale[pc.h] : 1.f;
+            // 8 bits: the maximum is m c as a float32 from here on; what that leaves out goes into the sum and the
+            // output (up to 2^63 either way, which scores below 2^30 stay within).
+            const float c = kFp8 ? s_qs[tid] : 1.f, vs = kFp8 ? p.v_scale[pc.h] : 1.f;
+            const float top = big == kNone ? ninf : big * c, use = top == ninf && !kFp8 ? 0.f : big;
+            const float rest = !kFp8 ? 0.f : top == ninf ? -kShift : fminf(fmaxf(fmaf(big, c, -top), -63.f), 63.f) - kShift;
+            auto factor = [&](float m) { return fast_exp2(kFp8 ? fmaf(m - use, c, rest) : m - use); };
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) sum += s_l[i][tid] * fast_exp2(s_m[i][tid] - use);
+            for (int i = 0; i < kWarps; ++i) sum += s_l[i][tid] * factor(s_m[i][tid]);
             const float f = !whole ? vs : sum != 0.f ? vs / sum : 0.f;
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) s_m[i][tid] = f * fast_exp2(s_m[i][tid] - use);
+            for (int i = 0; i < kWarps; ++i) s_m[i][tid] = f * factor(s_m[i][tid]);
             if (tid < valid) {
                 if (!whole) {
-                    reinterpret_cast<float2*>(p.part_ml)[part_place(blockIdx.x, pc.u0 == 0) * M + tid] = make_float2(big - kShift, sum);
+                    reinterpret_cast<float2*>(p.part_ml)[part_place(blockIdx.x, pc.u0 == 0) * M + tid] = make_float2(top, sum);
                 } else if (p.lse != nullptr) {
                     const int qi = pc.tile * M + tid;
-                    p.lse[(static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.Hq + pc.h * p.G + qi % p.G] = lse_of(big - kShift, sum);
+                    p.lse[(static_cast<int64_t>(pc.r.row0) + qi / p.G) * p.Hq + pc.h * p.G + qi % p.G] = lse_of(top, sum);
                 }
             }
         }

@@ -19,7 +19,7 @@ from tests import test_gpu_cache4 as four, test_gpu_target as wide
 from tests.test_gpu_target import U, dsv  # noqa: F401
 
 pytestmark = pytest.mark.gpu
-KINDS = [("bf16", "bf16"), ("f32", "f32"), ("f32", "e4m3"), ("bf16", "e2m1"), ("f32", "e2m1")]
+KINDS = wide.KINDS + [("bf16", "e2m1"), ("f32", "e2m1")]
 LEVELS = np.array([1.125, 1.25, 1.375, 1.5, 1.625, 1.75])
 
 
