@@ -702,15 +702,38 @@ def kv4_page_bytes(page, D):
 
 
 def kv4_cache(num_blocks, Hkv, page, D, device="cuda"):
-    """A 4-bit cache of zeros: uint8 [num_blocks, Hkv, kv4_page_bytes(page, D)]."""
+    """A 4-bit cache of zeros: uint8 [num_blocks, Hkv, kv4_page_bytes(page, D)].  The tensor keeps (page, D) as its
+    attribute `kv4`, by which the calls refuse rows of other heads; views and copies of it do not have that."""
     if page < 1 or D < 32 or D > 256 or D % 32:
         raise ValueError(f"4-bit caches have pages of at least one row and heads of 32, 64, .. 256 elements, not {page} and {D}")
-    return torch.zeros((num_blocks, Hkv, kv4_page_bytes(page, D)), dtype=torch.uint8, device=device)
+    cache = torch.zeros((num_blocks, Hkv, kv4_page_bytes(page, D)), dtype=torch.uint8, device=device)
+    cache.kv4 = (page, D)
+    return cache
 
 
-def _cache_code(k_cache, v_cache, k_scale, v_scale, dev, dtype, D=None):
+def _kv4_page(k_cache, v_cache, page, D, whole):
+    """Rows of a page of `whole` bytes a head in 4-bit caches for heads of D.  Pages of several sizes may have the same bytes
+    (16 rows of 128 elements, 32 of 64), so what the caches or the caller say of them is held against D."""
+    for cache, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        made = cache.__dict__.get("kv4")
+        if made is not None:
+            if made[1] != D:
+                raise ValueError(f"{name} holds heads of {made[1]}, the rows have heads of {D}")
+            if page is not None and page != made[0]:
+                raise ValueError(f"{name} has pages of {made[0]} rows, not {page}")
+            page = made[0]
+    rows = page
+    if page is None:
+        # the bytes alone: a row has 20 at least, more than a page is rounded up by, so one size fits these heads, or none
+        rows = whole // (D // 2 + -(-(D // 16) // 4) * 4) if D >= 32 else 0
+    if D < 32 or D % 32 or rows < 1 or kv4_page_bytes(rows, D) != whole:
+        raise ValueError(f"no 4-bit cache of heads of {D} has pages of {whole} bytes" + ("" if page is None else f" for {page} rows"))
+    return rows
+
+
+def _cache_code(k_cache, v_cache, k_scale, v_scale, dev, dtype, D=None, page=None):
     """Shape (num_blocks, Hkv, page, D) and type code of the caches, and the addresses of their scales.  D: of
-    the rows; a 4-bit cache's shape gives only its pages' bytes, from which it and the page follow."""
+    the rows; page: as the caller states it, or None."""
     shape = k_cache.shape
     t = k_cache.dtype
     four = t is torch.uint8
@@ -721,13 +744,13 @@ def _cache_code(k_cache, v_cache, k_scale, v_scale, dev, dtype, D=None):
         if k_scale is None or v_scale is None:
             raise ValueError("8-bit and 4-bit caches need k_scale and v_scale")
         _check_all(dev, ((k_scale, shape[1:2], torch.float32, "k_scale"), (v_scale, shape[1:2], torch.float32, "v_scale")))
-        if not four:
-            return shape, DSPARK_E4M3, k_scale.data_ptr(), v_scale.data_ptr()
-        # a row has 20 bytes at least, more than a page is rounded up by: one page size fits, or none
-        page = shape[2] // (D // 2 + -(-(D // 16) // 4) * 4) if D >= 32 else 0
-        if D % 32 or page < 1 or kv4_page_bytes(page, D) != shape[2]:
-            raise ValueError(f"no 4-bit cache of heads of {D} has pages of {shape[2]} bytes")
-        return (shape[0], shape[1], page, D), DSPARK_E2M1, k_scale.data_ptr(), v_scale.data_ptr()
+        if four:
+            page = _kv4_page(k_cache, v_cache, page, D, shape[2])
+            return (shape[0], shape[1], page, D), DSPARK_E2M1, k_scale.data_ptr(), v_scale.data_ptr()
+    if page is not None and page != shape[2]:
+        raise ValueError(f"the caches have pages of {shape[2]} rows, not {page}")
+    if t is torch.float8_e4m3fn:
+        return shape, DSPARK_E4M3, k_scale.data_ptr(), v_scale.data_ptr()
     if dtype is not None and t is not dtype:
         raise TypeError(f"caches of {t} for rows of {dtype}")
     if k_scale is not None or v_scale is not None:
@@ -735,15 +758,18 @@ def _cache_code(k_cache, v_cache, k_scale, v_scale, dev, dtype, D=None):
     return shape, _code_of(t), None, None
 
 
-def dspark_write_kv(k, v, slot, k_cache, v_cache, k_scale=None, v_scale=None, workspace=None, stream=None):
+def dspark_write_kv(k, v, slot, k_cache, v_cache, k_scale=None, v_scale=None, workspace=None, stream=None, page=None):
     """Stores the rows' keys and values: k, v [n, Hkv, D] (rows at any stride: slices of a fused
     projection) at slot [n] int64 (negative: none) of the caches [num_blocks, Hkv, page, D], of
-    the rows' type or float8_e4m3fn, or 4-bit ones (kv4_cache), with k_scale, v_scale [Hkv] float32."""
+    the rows' type or float8_e4m3fn, or 4-bit ones (kv4_cache), with k_scale, v_scale [Hkv] float32.
+    page: rows of a page, to be held against the caches.  A 4-bit cache that is not kv4_cache's own tensor (a view, a
+    copy, memory of the caller's) has no shape to tell heads of 128 on pages of 16 rows from heads of 64 on pages of 32:
+    without `page` its pages are what the rows' heads make of their bytes."""
     lib = load()
     dev = _device_of(k_cache, "k_cache")
     dt = _code_of(k.dtype)
     ks, vs = _heads(k, dev, k.dtype, "k"), _heads(v, dev, k.dtype, "v")
-    (nb, Hkv, page, D), code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, k.dtype, k.shape[2])
+    (nb, Hkv, page, D), code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, k.dtype, k.shape[2], page)
     n = k.shape[0]
     if k.shape != (n, Hkv, D) or v.shape != (n, Hkv, D):
         raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} for caches of {Hkv} heads of {D}")
@@ -793,14 +819,15 @@ def dspark_rotate(x, position, freq, interleaved=False, transposed=False, magnit
 
 
 def dspark_rotate_write_kv(q, k, v, position, freq, slot, k_cache, v_cache, k_scale=None, v_scale=None, interleaved=False,
-                           magnitude=1.0, out=None, workspace=None, stream=None):
+                           magnitude=1.0, out=None, workspace=None, stream=None, page=None):
     """dspark_rotate of q [n, Hq, D] and k [n, Hkv, D] with dspark_write_kv of the rotated keys and of v, in
-    one launch.  Returns the rotated queries (`out`, which may be q itself); q may be None."""
+    one launch.  Returns the rotated queries (`out`, which may be q itself); q may be None.  page: as for
+    dspark_write_kv."""
     lib = load()
     dev = _device_of(k_cache, "k_cache")
     dt = _code_of(k.dtype)
     ks, vs = _heads(k, dev, k.dtype, "k"), _heads(v, dev, k.dtype, "v")
-    (nb, Hkv, page, D), code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, k.dtype, k.shape[2])
+    (nb, Hkv, page, D), code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, k.dtype, k.shape[2], page)
     n = k.shape[0]
     if k.shape != (n, Hkv, D) or v.shape != (n, Hkv, D):
         raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} for caches of {Hkv} heads of {D}")
@@ -827,16 +854,17 @@ def dspark_rotate_write_kv(q, k, v, position, freq, slot, k_cache, v_cache, k_sc
 
 
 def dspark_read_kv(slot, k_cache, v_cache, k_scale=None, v_scale=None, D=None, dtype=torch.bfloat16, out=None,
-                   workspace=None, stream=None):
+                   workspace=None, stream=None, page=None):
     """Rows of the caches at slot [n] int64 (negative: not written) as `dtype`: dict k, v [n, Hkv, D].  `out` may
-    hold them (rows at any stride); without it a 4-bit cache's head size D has to be given."""
+    hold them (rows at any stride); without it the head size D of a 4-bit cache has to be given, unless it is
+    kv4_cache's own tensor.  page: as for dspark_write_kv."""
     lib = load()
     dev = _device_of(k_cache, "k_cache")
     if out is not None:
         D, dtype = out["k"].shape[2], out["k"].dtype
     elif D is None:
-        D = k_cache.shape[-1] if k_cache.dim() == 4 else 0
-    (nb, Hkv, page, D), code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, None, D)
+        D = k_cache.shape[-1] if k_cache.dim() == 4 else k_cache.__dict__.get("kv4", (0, 0))[1]
+    (nb, Hkv, page, D), code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, None, D, page)
     n, = slot.shape
     if out is None:
         new = lambda: torch.empty((n, Hkv, D), dtype=dtype, device=k_cache.device)  # noqa: E731
@@ -855,18 +883,19 @@ def dspark_read_kv(slot, k_cache, v_cache, k_scale=None, v_scale=None, D=None, d
 
 
 def dspark_paged_attention(q, row_offset, length, block_table, k_cache, v_cache, max_rows, scale=None, window=0,
-                           k_scale=None, v_scale=None, out=None, workspace=None, stream=None):
+                           k_scale=None, v_scale=None, out=None, workspace=None, stream=None, page=None):
     """Attention of a step's rows over the paged cache.  q [n, Hq, D] (rows at any stride);
     row_offset [B + 1], length [B] (rows in the cache before the step), block_table [B,
     max_blocks] int32; max_rows: the most rows of one request; scale: 1 / sqrt(D) by default.
     Caches of q's type, float8_e4m3fn, or 4-bit ones (kv4_cache), the latter two with k_scale, v_scale [Hkv].
+    page: as for dspark_write_kv.
     Returns dict out [n, Hq, D] and lse [n, Hq] float32 (an `out` without lse skips it)."""
     lib = load()
     dev = _device_of(k_cache, "k_cache")
     B, = length.shape
     qs = _heads(q, dev, q.dtype, "q")
     n, Hq, qd = q.shape
-    (nb, Hkv, page, D), code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, q.dtype, qd)
+    (nb, Hkv, page, D), code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, q.dtype, qd, page)
     if qd != D:
         raise ValueError(f"q has heads of {qd}, the caches of {D}")
     width = block_table.shape[1]
