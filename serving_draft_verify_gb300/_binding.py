@@ -864,7 +864,9 @@ def dspark_read_kv(slot, k_cache, v_cache, k_scale=None, v_scale=None, D=None, d
         D, dtype = out["k"].shape[2], out["k"].dtype
     elif D is None:
         D = k_cache.shape[-1] if k_cache.dim() == 4 else k_cache.__dict__.get("kv4", (0, 0))[1]
-    (nb, Hkv, page, D), code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, None, D, page)
+    (nb, Hkv, page, width), code, ksc, vsc = _cache_code(k_cache, v_cache, k_scale, v_scale, dev, None, D, page)
+    if width != D:
+        raise ValueError(f"heads of {D} asked of caches of heads of {width}")
     n, = slot.shape
     if out is None:
         new = lambda: torch.empty((n, Hkv, D), dtype=dtype, device=k_cache.device)  # noqa: E731

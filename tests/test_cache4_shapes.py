@@ -85,6 +85,16 @@ def test_other_pages_are_refused(dsv, one_gpu):
             call()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32, torch.float8_e4m3fn])
+def test_heads_asked_of_other_caches_are_refused(dsv, one_gpu, dtype):
+    """Reading with a D that is not the cache's: a cache whose shape says its heads holds it against them."""
+    cache = _OnGpu(torch.zeros((3, 2, 16, 128)).to(dtype))
+    g = _OnGpu(torch.ones(2)) if dtype is torch.float8_e4m3fn else None
+    slot = _OnGpu(torch.zeros(2, dtype=torch.int64))
+    with pytest.raises(ValueError, match="heads of 64 asked of caches of heads of 128"):
+        dsv.dspark_read_kv(slot, cache, cache, g, g, D=64)
+
+
 @pytest.mark.gpu
 def test_calls_on_the_gpu(dsv):
     """A cache for heads of 128 on pages of 16 rows refuses heads of 64 and 256 and is left as it was; its own heads are
