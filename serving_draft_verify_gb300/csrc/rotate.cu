@@ -397,7 +397,8 @@ extern "C" dspark_status_t dspark_rotary_frequencies(int rot, double base, dspar
         return DSPARK_ERR_INVALID_ARGUMENT;
     if (scaling == DSPARK_ROTARY_BASE && rot == 2) return DSPARK_ERR_INVALID_ARGUMENT;
     const double turn = 6.283185307179586476925;
-    const double used = scaling == DSPARK_ROTARY_BASE ? base * std::pow(factor, rot / (rot - 2.0)) : base;
+    // of the base in use, which itself may leave the doubles
+    const double log_base = log(base) + (scaling == DSPARK_ROTARY_BASE ? rot / (rot - 2.0) * log(factor) : 0.0);
     auto pair_with = [&](double turns) { return rot * log(original / (turns * turn)) / (2.0 * log(base)); };
     double first = 0.0, last = 0.0;
     if (scaling == DSPARK_ROTARY_RAMP) {
@@ -406,7 +407,7 @@ extern "C" dspark_status_t dspark_rotary_frequencies(int rot, double base, dspar
         if (last <= first) last = first + 0.001;
     }
     for (int i = 0; i < rot / 2; ++i) {
-        const double f = exp(-2.0 * i / rot * log(used));
+        const double f = exp(-2.0 * i / rot * log_base);
         double keep = 1.0;                                   // of f; the rest is f / factor
         if (scaling == DSPARK_ROTARY_LINEAR) keep = 0.0;
         if (scaling == DSPARK_ROTARY_RAMP) keep = 1.0 - (i - first) / (last - first);
