@@ -29,3 +29,12 @@ def test_raised_base_past_doubles(dsv, rot, base, factor):
     assert (np.abs(got - want) <= want * (2.0 ** -24 + 2.0 ** -39) + 2.0 ** -150).all()
     if factor == 8.0:
         np.testing.assert_allclose(want, rotary.frequencies(rot, base, "base", factor)[0], rtol=1e-12)
+
+
+def test_ramp_halfway():
+    """4096 positions at base 10^4 and 128 elements: d(32) = 20.9 and d(1) = 45.03, so pairs 20 to 46 are blended, and
+    pair 33 keeps one half: 1/2 + 1/2 / 4 of its frequency."""
+    ramp, _ = rotary.frequencies(128, 1e4, "ramp", 4, original=4096)
+    f = rotary.frequencies(128, 1e4)[0]
+    np.testing.assert_allclose(ramp[33], 0.625 * f[33])
+    np.testing.assert_allclose(ramp[20:47] / f[20:47], 1 - 0.75 * np.arange(27) / 26)
