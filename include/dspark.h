@@ -492,7 +492,7 @@ dspark_status_t dspark_write_kv(int64_t rows, int Hkv, int D, int page, int num_
  *   y1 = m (x1 cos a - x2 sin a),  y2 = m (x2 cos a + x1 sin a),  m = magnitude,
  * and by -a where `transposed` is 1, which makes of a gradient with respect to y the one with respect to
  * x.  Elements from rot on are copied.  The angle is taken modulo a turn before it is rounded, so far
- * positions are as exact as near ones.
+ * positions are as exact as near ones (|freq| < 4; above, off by up to position |freq| 2^-66 of a turn).
  *   x, out: row n at n * x_stride (out_stride) elements, `heads` heads of D adjacent elements in
  *   `dt`, rows 16-byte aligned; queries and keys that lie side by side are one call.  out may be x itself
  *   with the same stride, or rows that share no element with x's (other slices of one buffer); anything
@@ -572,7 +572,7 @@ dspark_status_t dspark_read_kv(int64_t rows, int Hkv, int D, int page, int num_b
  * at least 15 bits (bf16 caches; a visible value of +-inf stays that down to weights of 2^-103
  * of the largest) or 11 bits (8- and 4-bit caches, where weights below 2^-28 of the largest and q's
  * elements below 2^-25 of their row's largest lose bits too), below out's own rounding; lse counts them
- * whole.
+ * whole.  Scores may reach 2^30 either way (in units of log 2; float32 tells them apart by 64 there).
  * Keys and values a row does not see have no part in it, whatever they hold.  Table entries
  * of pages past the last position, and with a window of pages wholly before position
  * len[b] - window + 1, are not read.

@@ -24,7 +24,8 @@ constexpr int kWide = 64;
 // ------------------------------------------------------------ float32 rows ---
 // Sixteen query rows (up to four a warp) over 32 keys a unit, float32 throughout: a lane is a key
 // for the scores and has pairs of columns of the values.  The next unit's keys and values are copied
-// (asynchronously, as they are stored) while this one's are computed on.
+// (asynchronously, as they are stored) while this one's are computed on.  Over 4-bit caches it spills at the 128 registers that
+// it gets: 8 bytes for heads of 64, 32 and 36 (stores, loads) for 128, 72 and 84 for 256.
 constexpr int kSimtM = 16, kSimtKT = 32, kSimtThreads = 128;
 
 // Rows as they are staged, and four and two adjacent elements of one as float.
@@ -279,8 +280,8 @@ dspark_status_t launch_f32(const Args& p, cudaStream_t s) {
 }
 
 // 4-bit caches: tiles of 8, 16, 24 or 32 query rows of a key head, whichever takes the least for the most rows that
-// a request may have.  A tile's time goes as 8 + 5 for each eight (64 requests of up to 16384 keys: 148, 203 and
-// 298 us with 8, 16 and 32 rows).
+// a request may have.  A tile's time goes as 8 + 5 for each eight (64 requests of up to 16384 keys: 147, 201 and
+// 287 us with 8, 16 and 32 rows).
 template <int DT>
 dspark_status_t launch_e2m1(const Args& p, cudaStream_t s) {
     const int64_t most = static_cast<int64_t>(p.max_rows) * p.G;

@@ -2,16 +2,18 @@
 // at a time on the warp-level tensor instructions.
 //
 // The work is divided as in attn_mma.cuh: each of a block's four warps takes 32 keys of every unit of
-// 128, with a ring of its own, its own running maximum and sum and its own part of the output.  What
-// bounds it is not the bytes but turning codes into operands (a conversion for two elements and a
-// multiplication for two, 256 of a warp's 640 instructions for 32 keys of 128 elements and 8 query rows), so keys and values
+// 128, with a ring of its own, its own running maximum and sum and its own part of the output.  Turning codes into
+// operands is what most instructions do (a conversion for two elements and a multiplication for two, 256 of a
+// warp's 650 for 32 keys of 128 elements and 8 query rows), so keys and values
 // are the side of the products that has 16 rows and the queries the one that has 8: a step for up to 8 query rows (plain
-// decoding with groups of 8 and fewer) then costs half the products and half the exponentials.
+// decoding with groups of 8 and fewer) then costs half the products and half the exponentials.  No pipe is full, though: what
+// it waits for most is the fixed latency between dependent instructions, with two or three warps a scheduler.
 //
-// 32 heads on 8 of 128, pages of 16: 64 requests of one row and up to 16384 keys 148 us for 676 MB (4.6 TB/s,
-// issuing in 56 % of the cycles, three blocks an SM); 16 requests of 8 rows and up to 32768 keys 210 us
-// (32 rows a tile, two blocks an SM by registers, issuing in 47 %, tensor pipe 43 %); 128 requests of
-// up to 17 rows and 6000 keys 386 us (three tiles of 24).  Keys as the side of 8 took 235, 257 and 500; on
+// 32 heads on 8 of 128, pages of 16: 64 requests of one row and up to 16384 keys 147 us for 676 MB (4.6 TB/s; three blocks an
+// SM; with a quarter of the requests issuing in 50 % of the cycles, ALU pipe 41 %, tensor pipe 28 %); 16 requests of 8 rows and
+// up to 32768 keys 203 us (32 rows a tile, two blocks an SM by 255 registers, 72 bytes of spill stores and 104 of loads that
+// are a thousandth of the instructions; issuing in 48 %, tensor pipe 41 %); 128 requests of
+// up to 17 rows and 6000 keys 380 us (three tiles of 24).  Keys as the side of 8 took 235, 257 and 500; on
 // tcgen05, codes converted into shared memory by the way, 400, 271 and 640.
 //
 //   S' = K Q'    m16n8k16 in f16, query rows as columns,
@@ -53,8 +55,9 @@ struct Mma4Shape {
     static constexpr int M = 8 * NT;                        // query rows of a tile
     static constexpr int KS = 32;                           // keys of a warp's step
     static constexpr int KT = KS * kWarps;                  // keys of a unit
-    // What a piece costs by itself, in units (12,200 cycles and 3,900 with 32 query rows, 6,000 and 2,200 with 8).
-    // 256 requests of up to 500 keys: 8 rows 119 us, without 142, with five 122; 1 row 48, 60 and 48.
+    // What a piece costs by itself, in units (12,200 cycles and 3,900 with 32 query rows, 6,000 and 2,200 with 8, by the
+    // SM's clock before the results were written by columns).  256 requests of up to 500 keys: 8 rows 109 us, without
+    // 135, with five 114; 1 row 48, 60 and 48; a prompt of 2048 rows 264, 347 and 277.
     static constexpr int kOver = 3;
     static constexpr int kRow = DT / 2;                     // bytes of a row's codes
     static constexpr int kScale = DT / 16;                  // and of its scales

@@ -5,15 +5,19 @@
 //
 // The angle.  n freq in float32 is off by 2^-24 of itself, which at position 10^6 is a sixteenth of a
 // radian.  Here freq / 2 pi is a 64-bit fraction of a turn, formed with integers from freq's 24 bits
-// (wrong by 2^-64 at most for |freq| < 4), so that n times it, modulo 2^64, is the angle modulo a turn to 2^-33;
+// (wrong by 2^-64 at most for |freq| < 4, and by |freq| / 4 of that above), so that n times it, modulo 2^64, is the angle modulo
+// a turn to 2^-33;
 // the nearest quarter turn is taken off before anything is rounded to float32.
 //
 // Bound by memory: every element is read once and written once.  A block has a few rows: its threads
 // first make the rows' cosines and sines, then each has one place of a head (`unit`: two pieces of kSub
 // elements that hold whole pairs, so that a call in place needs no exchange) and goes over the heads
-// with it.  16384 rows of 40 heads of 128, bf16: 54 us for 336 MB (6.2 TB/s); 16384 rows of 32 heads on 8 with keys and
-// values stored in 4 bits: 72 us for 354 MB (4.9 TB/s), which is arithmetic of the blocks of 16 and the registers that
-// it holds from the loads; keys and values alone to 4 bits 24 us (86 MB), float32 to 4 bits (8192 rows) 60 us.
+// with it.  In a graph, one call after the other: 16384 rows of 40 heads of 128, bf16: 54 us for 336 MB (6.2 TB/s; 52 by the
+// profiler, without the gap between launches; 55 to 56 through the Python binding), float32 8192 rows of them 54; 16384 rows of
+// 32 heads on 8 with keys and values stored in 4 bits: 72 us for 354 MB (4.9 TB/s), issuing in 57 % of the cycles, its warps
+// waiting for memory (3.9 of the 11 cycles between two instructions of one), then for shared memory and for fixed latency
+// (1.8 each); keys and values alone to 4 bits, not rotated, 24 us (86 MB, 3.6 TB/s), issuing in 62 %, waits of 2.2 cycles of 10 for
+// memory, 2.1 for fixed latency, 1.4 at the barrier behind the rows' places; float32 to 4 bits (8192 rows) 59 us.
 #include <cmath>
 
 #include "launch.cuh"
@@ -55,7 +59,9 @@ __device__ __forceinline__ float2 cos_sin(uint64_t a) {
     return (q & 2) ? make_float2(-r.x, -r.y) : r;
 }
 
-// Heads of queries in flight and blocks an SM asked for.  16384 rows of 32 heads on 8 of 128, bf16, to 4 bits, us:
+// Heads of queries in flight and blocks an SM asked for.  At seven blocks (72 registers) bf16 rows to 4 bits spill 28 bytes of
+// stores and 80 of loads (interleaved 44 and 60), to 8 bits 8 and 36 (4 and 4); float32 ones to 4 bits at five blocks, interleaved,
+// 20 and 36: 1 % of the instructions where it was counted (the first).  16384 rows of 32 heads on 8 of 128, bf16, to 4 bits, us:
 // 72 with 2 heads and 7 blocks, 75 with 3 and 6, 82 with 3 and 5, 95 with 3 heads and no blocks asked for; rotation alone takes
 // three heads and what registers it likes (40 heads 54, with 2 heads 57); float32 60 with 3 and 5, 70 with 2 and 7.
 // Few heads, 16384 rows of 8: 14.5 with 8 blocks, 16.3 without asking for any, and 25.7 a row at a time.
